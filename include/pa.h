@@ -75,9 +75,10 @@ typedef enum {
   PA_DEVICE_WORK_OVERFLOW = 2,  /* a work list or block-table slice exceeded its planned capacity */
   PA_DEVICE_CAPACITY = 4,       /* a length or query packing beyond what the plan allows; that
                                    request's rows are left untouched */
-  PA_DEVICE_PAGE_ID = 8         /* a block-table entry of a page holding attended keys lies outside
+  PA_DEVICE_PAGE_ID = 8,        /* a block-table entry of a page holding attended keys lies outside
                                    [0, num_pages) (or an append slot's page does); that page reads
                                    as zeros (is not written), every other page is unaffected */
+  PA_DEVICE_POSITION = 16       /* a position outside the rotation table; that token is not written */
 } pa_device_code;
 
 typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
@@ -277,6 +278,169 @@ pa_status pa_append_kv(const void* k_new, const void* v_new, int64_t new_stride_
                        int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
                        int32_t kv_dtype, const int64_t* slot_mapping, int32_t num_tokens,
                        float k_scale, float v_scale, void* scratch, void* stream);
+
+/* ---- long contexts: rotation, key bounds, page selection, sparse attention ----
+ * A layer's step over a long context calls, in this order on one stream,
+ *   pa_append_rope_kv   norm and rotate the new queries and keys, append K / V
+ *   pa_page_bounds      refresh the key bounds of the pages that changed
+ *   pa_select_pages     choose, for each query and kv head, the pages to attend
+ *   pa_sparse_attend    attend over the chosen pages only
+ * Each can be called alone; pa_decode / pa_extend read the same cache. */
+
+/* Norm and rotation of pa_append_rope_kv (plain data; the pointers are device
+ * memory of the caller's). */
+typedef struct {
+  int32_t rot_dim;       /* leading dims of each head that rotate: a multiple of 8, 0 (none) .. head_dim */
+  int32_t interleaved;   /* pair i is dims (i, i + rot_dim / 2) when 0, (2i, 2i + 1) when 1 */
+  int32_t num_axes;      /* position axes, 1 .. 4 (1 for text; 3 for time, height, width) */
+  int32_t sections[4];   /* pairs of each axis, in order; they sum to rot_dim / 2 */
+  int32_t max_position;  /* rows of cos_sin */
+  const float* cos_sin;  /* fp32 [max_position, rot_dim]: a position's cosines of pairs 0 .. rot_dim / 2 - 1,
+                            then its sines; 16-byte aligned */
+  int64_t cos_sin_stride;   /* elements from row to row (a multiple of 4) */
+  const void* q_norm;    /* bf16 [head_dim] RMS norm weights of the queries, or NULL (no norm); 8-byte aligned */
+  const void* k_norm;    /* the same for the keys */
+  float norm_eps;        /* >= 0 */
+  float norm_offset;     /* added to every weight (0, or 1 where weights are stored as w - 1) */
+} pa_rope;
+
+/* Norm, rotate and append: for token t and head h, in fp32,
+ *   y = x / sqrt(mean(x^2) + norm_eps) * (w + norm_offset)       (where w is given)
+ *   (a, b) <- (a cos - b sin, b cos + a sin)                     (each pair of the first rot_dim dims)
+ * with cos / sin of pair i taken from cos_sin row positions[axis(i)][t].  The
+ * queries go to q_out (bf16), the keys to the page slot (bf16, or e4m3(y / k_scale)),
+ * both rounded once; the values go to their slot exactly as pa_append_kv writes them.
+ *   q, q_out       device bf16 [num_tokens, num_q_heads, head_dim] with their strides, or
+ *                  both NULL (num_q_heads 0: keys and values alone); q_out may be q itself
+ *   k_new, v_new   device bf16 [num_tokens, num_kv_heads, head_dim], one pair of strides
+ *                  (views of one projection output will do); all rows 8-byte aligned
+ *   positions      device int32 [num_axes, positions_stride]: each token's position on each axis
+ *                  (may be NULL when rot_dim is 0)
+ *   k_cache .. slot_mapping, k_scale, v_scale, scratch   as for pa_append_kv; the slots of a
+ *                  call are distinct.  A token with a negative slot is padding: nothing of it
+ *                  is written, its q_out rows included.
+ * A slot outside the pool (PA_DEVICE_PAGE_ID) or a position outside [0, max_position)
+ * (PA_DEVICE_POSITION) leaves that token unwritten, q_out included; the code is recorded where
+ * scratch is given.  Asynchronous on `stream`; one kernel launch. */
+pa_status pa_append_rope_kv(const pa_rope* rope,
+                            const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                            void* q_out, int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_q_heads,
+                            const void* k_new, const void* v_new, int64_t new_stride_tok, int64_t new_stride_head,
+                            const int32_t* positions, int64_t positions_stride,
+                            void* k_cache, void* v_cache,
+                            int64_t kv_stride_page, int64_t kv_stride_tok, int64_t kv_stride_head,
+                            int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t kv_dtype, const int64_t* slot_mapping, int32_t num_tokens,
+                            float k_scale, float v_scale, void* scratch, void* stream);
+
+/* Key bounds of pages: bounds[page][kv head][0][d] is the smallest and
+ * bounds[page][kv head][1][d] the largest value of dim d over the page's filled
+ * slots (those of keys j < seq_lens[b]), in bf16 -- exact, for an e4m3 cache
+ * bounds of bf16(float(code) * scale).  A NaN among the values gives a NaN bound.
+ *   k_cache, strides, num_pages, kv_dtype, k_scale, k_scales   as for pa_decode
+ *   block_table    device int32 [batch, bt_stride]; max_pages_per_seq (<= bt_stride) bounds a row
+ *   seq_lens       device int32 [batch]
+ *   query_start_loc  device int32 [batch + 1]: the last (query_start_loc[b+1] - query_start_loc[b])
+ *                  tokens of request b are new, and only the pages that hold some of them are
+ *                  written; NULL: every page of every request
+ *   bounds         device bf16 [num_pages, num_kv_heads, 2, head_dim], the last two dims
+ *                  contiguous, strides bounds_stride_page / bounds_stride_head (16-byte aligned)
+ *   scratch        optional (may be NULL), as for pa_append_kv: records PA_DEVICE_PAGE_ID (that
+ *                  page is passed over) and PA_DEVICE_CAPACITY (a length beyond
+ *                  max_pages_per_seq, or more new tokens than the length: that request is
+ *                  passed over)
+ * A page that several requests share is written with the same bounds by each of them as long as
+ * they fill the same slots of it.  Asynchronous on `stream`; one kernel launch. */
+pa_status pa_page_bounds(const void* k_cache, int64_t kv_stride_page, int64_t kv_stride_tok, int64_t kv_stride_head,
+                         int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim,
+                         int32_t kv_dtype, const int32_t* block_table, int64_t bt_stride,
+                         int32_t max_pages_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc,
+                         int32_t batch, float k_scale, const float* k_scales,
+                         void* bounds, int64_t bounds_stride_page, int64_t bounds_stride_head,
+                         void* scratch, void* stream);
+
+/* Static description of page selection and sparse attention (capacities). */
+typedef struct {
+  int32_t num_q_heads;        /* Hq; Hq % Hkv == 0 and Hq / Hkv <= 128 */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t head_dim;           /* D in {64, 128, 256} */
+  int32_t page_size;          /* ps in {16, 32, 64} */
+  int32_t kv_dtype;           /* pa_kv_dtype */
+  int32_t max_batch;          /* capacity: requests per call */
+  int32_t max_pages_per_seq;  /* capacity: block-table row width, at most 65536 */
+  int32_t max_total_q;        /* capacity of query rows per call */
+  int32_t top_pages;          /* K: pages a (query, kv head) attends to at most, 1 .. 4096 */
+  int32_t first_pages;        /* always among them: the first pages of the context (>= 0) */
+  int32_t last_pages;         /* and the last ones up to the query's own (>= 1); first + last <= K */
+  int32_t has_sinks;          /* 1: pa_sparse_attend gets a [Hq] fp32 sink logit array */
+  float soft_cap;             /* 0 = off; else s = cap * tanh(s / cap) */
+  int32_t num_splits;         /* 0 = by rule, >0 = max splits of a row's pages */
+  int32_t num_sms;            /* SMs to plan for; 0 = query the current device */
+} pa_sparse_shape;
+
+/* Plan produced by pa_sparse_plan; plain data, may be copied. */
+typedef struct {
+  pa_sparse_shape shape;
+  int32_t tile_tokens;        /* keys per pipeline stage of the attention */
+  int32_t stages;             /* pipeline depth per warp */
+  int32_t warps;              /* compute warps per CTA */
+  int32_t smem_bytes;         /* dynamic shared memory per attention CTA */
+  int32_t partial_rows;       /* capacity of (query row, split) pairs in the scratch workspace */
+  int32_t score_rows;         /* query rows scored at a time; a call of more makes several passes */
+  int64_t scratch_bytes;      /* device scratch the calls need (>= 65536, the header) */
+  int32_t reserved[6];
+} pa_sparse_plan_t;
+
+/* Plan from capacities.  Pure host code: no CUDA call unless shape->num_sms == 0. */
+pa_status pa_sparse_plan(const pa_sparse_shape* shape, pa_sparse_plan_t* plan);
+
+/* Choose the pages that each query row and kv head attends to.  For the row of
+ * request b at position pos (rows and positions as for pa_extend; with
+ * query_start_loc NULL, as for pa_decode: one row per request, total_q == batch)
+ * the pages 0 .. n - 1, n = pos / page_size + 1, can be chosen.  If n <= K all
+ * are; else the first first_pages, the last last_pages, and of the others the
+ * K - first - last with the highest score
+ *   score(page) = max over the group's q heads of  sum_d max(q_d lo_d, q_d hi_d),
+ * lo / hi the page's bounds: no key of the page has a larger q.k.  The order is
+ * that of the exact sums (what the tensor cores leave undecided is summed again
+ * in 64 bits); equal scores go to the lower page.  A head's score that is not
+ * finite (an infinity or NaN in q or the bounds) counts as +infinity.
+ *   q              device bf16 [total_q, Hq, D], strides q_stride_tok / q_stride_head, rows 16-byte aligned
+ *   bounds         as pa_page_bounds writes them (16-byte aligned)
+ *   block_table    device int32 [batch, bt_stride]; seq_lens, query_start_loc device int32
+ *   pages          device int32 [total_q, Hkv, K] contiguous: the chosen page indices of the
+ *                  request (not pool pages), ascending, then -1.  A row without keys gets -1
+ *                  alone; rows behind query_start_loc[batch] are left as they were.
+ *   scratch        >= plan->scratch_bytes, 256-byte aligned, initialised by pa_scratch_init; may be
+ *                  shared with pa_sparse_attend calls of the same plan on the same stream.
+ * A length beyond the plan's capacity or a packing with more rows than tokens leaves that
+ * request's rows untouched (PA_DEVICE_CAPACITY).  A block-table entry outside the pool reads as
+ * bounds of zero (PA_DEVICE_PAGE_ID). */
+pa_status pa_select_pages(const pa_sparse_plan_t* plan,
+                          const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                          const void* bounds, int64_t bounds_stride_page, int64_t bounds_stride_head,
+                          int32_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                          const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q,
+                          int32_t* pages, void* scratch, int64_t scratch_bytes, void* stream);
+
+/* Attention over chosen pages: as pa_decode / pa_extend, with the keys of query
+ * row r and kv head g being { j <= pos : j / page_size in pages[r][g][:] }.
+ *   pages          device int32 [total_q, Hkv, K] contiguous, as pa_select_pages writes them or the
+ *                  caller's own: page indices of the request in any order, each at most once,
+ *                  ended by the first negative one.  Pages behind the query hold no key j <= pos
+ *                  and add nothing.  No page: out = 0, lse = the sink or -infinity.
+ * Rows, positions, errors and untouched rows as for pa_select_pages; the other arguments as for
+ * pa_extend.  Asynchronous on `stream`; one kernel launch. */
+pa_status pa_sparse_attend(const pa_sparse_plan_t* plan,
+                           const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                           const void* k_cache, const void* v_cache,
+                           int64_t kv_stride_page, int64_t kv_stride_tok, int64_t kv_stride_head,
+                           int32_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q,
+                           const int32_t* pages, float scale, const float* sinks, float k_scale, float v_scale,
+                           const float* k_scales, const float* v_scales,
+                           void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
+                           void* scratch, int64_t scratch_bytes, void* stream);
 
 /* Zero the 64 KiB header at the start of a scratch buffer (enqueued on
  * `stream`): the error word, and the split-arrival counters that decode

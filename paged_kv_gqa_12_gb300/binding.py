@@ -26,6 +26,7 @@ DEVICE_WAIT_TIMEOUT = 1
 DEVICE_WORK_OVERFLOW = 2
 DEVICE_CAPACITY = 4
 DEVICE_PAGE_ID = 8
+DEVICE_POSITION = 16
 
 # bytes of the scratch header (error word, then split-arrival counters) at
 # the start of every scratch workspace
@@ -41,7 +42,8 @@ KV_FP8_E4M3 = 1
 
 EXPORTED_SYMBOLS = ("pa_plan", "pa_decode", "pa_extend", "pa_scratch_init", "pa_check",
                     "pa_status_string", "pa_version", "pa_decode_static_scratch", "pa_append_kv",
-                    "pa_debug_wait_expiry")
+                    "pa_debug_wait_expiry", "pa_append_rope_kv", "pa_page_bounds", "pa_sparse_plan",
+                    "pa_select_pages", "pa_sparse_attend")
 
 
 class PaShape(ctypes.Structure):
@@ -83,6 +85,56 @@ class PaPlan(ctypes.Structure):
     ]
 
 
+class PaRope(ctypes.Structure):
+    _fields_ = [
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("num_axes", ctypes.c_int32),
+        ("sections", ctypes.c_int32 * 4),
+        ("max_position", ctypes.c_int32),
+        ("cos_sin", ctypes.c_void_p),
+        ("cos_sin_stride", ctypes.c_int64),
+        ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float),
+        ("norm_offset", ctypes.c_float),
+    ]
+
+
+class PaSparseShape(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("max_total_q", ctypes.c_int32),
+        ("top_pages", ctypes.c_int32),
+        ("first_pages", ctypes.c_int32),
+        ("last_pages", ctypes.c_int32),
+        ("has_sinks", ctypes.c_int32),
+        ("soft_cap", ctypes.c_float),
+        ("num_splits", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+    ]
+
+
+class PaSparsePlan(ctypes.Structure):
+    _fields_ = [
+        ("shape", PaSparseShape),
+        ("tile_tokens", ctypes.c_int32),
+        ("stages", ctypes.c_int32),
+        ("warps", ctypes.c_int32),
+        ("smem_bytes", ctypes.c_int32),
+        ("partial_rows", ctypes.c_int32),
+        ("score_rows", ctypes.c_int32),
+        ("scratch_bytes", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 6),
+    ]
+
+
 class PaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -117,6 +169,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.pa_append_kv.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp, i32, f32, f32,
                                vp, vp]
     L.pa_append_kv.restype = ctypes.c_int
+    L.pa_append_rope_kv.argtypes = [ctypes.POINTER(PaRope), vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp, i64,
+                                    vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp, i32, f32, f32, vp, vp]
+    L.pa_append_rope_kv.restype = ctypes.c_int
+    L.pa_page_bounds.argtypes = [vp, i64, i64, i64, i32, i32, i32, i32, i32, vp, i64, i32, vp, vp, i32, f32, vp, vp,
+                                 i64, i64, vp, vp]
+    L.pa_page_bounds.restype = ctypes.c_int
+    L.pa_sparse_plan.argtypes = [ctypes.POINTER(PaSparseShape), ctypes.POINTER(PaSparsePlan)]
+    L.pa_sparse_plan.restype = ctypes.c_int
+    L.pa_select_pages.argtypes = [ctypes.POINTER(PaSparsePlan), vp, i64, i64, vp, i64, i64, i32, vp, i64, vp, vp, i32,
+                                  i32, vp, vp, i64, vp]
+    L.pa_select_pages.restype = ctypes.c_int
+    L.pa_sparse_attend.argtypes = [ctypes.POINTER(PaSparsePlan), vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64,
+                                   vp, vp, i32, i32, vp, f32, vp, f32, f32, vp, vp, vp, i64, i64, vp, vp, i64, vp]
+    L.pa_sparse_attend.restype = ctypes.c_int
     L.pa_debug_wait_expiry.argtypes = [vp, i32, i64, vp]
     L.pa_debug_wait_expiry.restype = ctypes.c_int
     L.pa_scratch_init.argtypes = [vp, vp]
@@ -233,6 +299,188 @@ def append_kv(k_new, v_new, k_cache, v_cache, slot_mapping, *, kv_dtype: int = K
         k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], k_cache.shape[3], int(kv_dtype), _ptr(slot_mapping),
         k_new.shape[0], float(k_scale), float(v_scale), _ptr(scratch), _stream(stream))
     _check(status, "pa_append_kv")
+
+
+def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None, q_norm=None, k_norm=None,
+         norm_eps: float = 1e-6, norm_offset: float = 0.0) -> PaRope:
+    """Norm and rotation for append_rope_kv.  ``cos_sin``: fp32 [max_position, rot_dim] (cosines, then sines; None
+    with rot_dim 0); ``sections``: pairs per position axis (None: one axis); ``q_norm`` / ``k_norm``: bf16 [head_dim]
+    RMS norm weights or None.  The tensors are kept alive by the returned struct."""
+    _typed("q_norm", q_norm, torch.bfloat16, 1)
+    _typed("k_norm", k_norm, torch.bfloat16, 1)
+    _typed("cos_sin", cos_sin, torch.float32, 2)
+    if (cos_sin is None) != (rot_dim == 0):
+        raise ValueError("cos_sin is given exactly when rot_dim > 0")
+    if cos_sin is not None and cos_sin.shape[1] != rot_dim:
+        raise ValueError("cos_sin must be [max_position, rot_dim]")
+    sec = [int(x) for x in sections] if sections is not None else [rot_dim // 2]
+    if not 1 <= len(sec) <= 4:
+        raise ValueError("1 to 4 position axes")
+    r = PaRope(rot_dim=rot_dim, interleaved=1 if interleaved else 0, num_axes=len(sec),
+               sections=(ctypes.c_int32 * 4)(*sec), max_position=0 if cos_sin is None else cos_sin.shape[0],
+               cos_sin=_ptr(cos_sin), cos_sin_stride=0 if cos_sin is None else cos_sin.stride(0), q_norm=_ptr(q_norm),
+               k_norm=_ptr(k_norm), norm_eps=float(norm_eps), norm_offset=float(norm_offset))
+    r.tensors = (cos_sin, q_norm, k_norm)
+    return r
+
+
+def _typed(name, t, dtype, dims):
+    """Refuse a tensor of another type, rank or device, or without a contiguous innermost dimension."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-d {dtype} tensor")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _cache(name, t, kv_dtype):
+    _typed(name, t, torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16, 4)
+
+
+def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_mapping, *, q=None, q_out=None,
+                   kv_dtype: int = KV_BF16, k_scale: float = 1.0, v_scale: float = 1.0, scratch=None, stream=None):
+    """pa_append_rope_kv: norm and rotate q (bf16 [T, Hq, D], into q_out) and k_new (bf16 [T, Hkv, D]), write k_new
+    and v_new into the paged caches at slot_mapping (int64 [T]).  positions: int32 [T], or [axes, T]."""
+    sp, st, sh = _kv_strides(k_cache, v_cache)
+    T = k_new.shape[0]
+    for name, t in (("q", q), ("q_out", q_out), ("k_new", k_new), ("v_new", v_new)):
+        _typed(name, t, torch.bfloat16, 3)
+    _cache("k_cache", k_cache, kv_dtype)
+    _cache("v_cache", v_cache, kv_dtype)
+    _typed("slot_mapping", slot_mapping, torch.int64, 1)
+    if tuple(k_new.stride()) != tuple(v_new.stride()) or k_new.shape != v_new.shape:
+        raise ValueError("k_new and v_new must share shape and strides")
+    if k_new.shape[1:] != k_cache.shape[2:] or slot_mapping.shape[0] != T:
+        raise ValueError("k_new must be [tokens, kv_heads, head_dim] of the cache, slot_mapping [tokens]")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None and (q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != k_new.shape[2]):
+        raise ValueError("q and q_out must be [tokens, q_heads, head_dim]")
+    for name, w in zip(("q_norm", "k_norm"), getattr(r, "tensors", (None,) * 3)[1:]):
+        if w is not None and w.shape[0] != k_new.shape[2]:
+            raise ValueError(f"{name} must be [head_dim]")
+    ps = 0
+    if r.rot_dim > 0:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        _typed("positions", positions, torch.int32, positions.dim())
+        if tuple(positions.shape) not in ((r.num_axes, T), (T,) if r.num_axes == 1 else ()):
+            raise ValueError("positions must be [axes, tokens] ([tokens] for one axis)")
+        ps = positions.stride(0) if positions.dim() == 2 else T
+    hq = 0 if q is None else q.shape[1]
+    status = load().pa_append_rope_kv(
+        ctypes.byref(r), _ptr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1), _ptr(q_out),
+        0 if q is None else q_out.stride(0), 0 if q is None else q_out.stride(1), hq, _ptr(k_new), _ptr(v_new),
+        k_new.stride(0), k_new.stride(1), _ptr(positions), ps, _ptr(k_cache), _ptr(v_cache), sp, st, sh,
+        k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], k_cache.shape[3], int(kv_dtype), _ptr(slot_mapping), T,
+        float(k_scale), float(v_scale), _ptr(scratch), _stream(stream))
+    _check(status, "pa_append_rope_kv")
+
+
+def _requests(block_table, seq_lens, query_start_loc):
+    _typed("block_table", block_table, torch.int32, 2)
+    _typed("seq_lens", seq_lens, torch.int32, 1)
+    _typed("query_start_loc", query_start_loc, torch.int32, 1)
+    if block_table.shape[0] < seq_lens.shape[0]:
+        raise ValueError("block_table must have a row per request")
+    if query_start_loc is not None and query_start_loc.shape[0] != seq_lens.shape[0] + 1:
+        raise ValueError("query_start_loc must be [batch + 1]")
+
+
+def page_bounds(k_cache, block_table, seq_lens, bounds, *, query_start_loc=None, kv_dtype: int = KV_BF16,
+                k_scale: float = 1.0, k_scales=None, scratch=None, stream=None):
+    """pa_page_bounds: refresh bounds (bf16 [pages, kv_heads, 2, head_dim]: smallest, largest key value per dim) of
+    the pages that hold new tokens (query_start_loc), or of every page of the requests (None)."""
+    _cache("k_cache", k_cache, kv_dtype)
+    _requests(block_table, seq_lens, query_start_loc)
+    _typed("k_scales", k_scales, torch.float32, 1)
+    _bounds(bounds, k_cache.shape[0], k_cache.shape[2], k_cache.shape[3])
+    if k_scales is not None and k_scales.shape[0] != seq_lens.shape[0]:
+        raise ValueError("k_scales must be [batch]")
+    status = load().pa_page_bounds(
+        _ptr(k_cache), k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), k_cache.shape[0], k_cache.shape[1],
+        k_cache.shape[2], k_cache.shape[3], int(kv_dtype), _ptr(block_table), block_table.stride(0),
+        block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), seq_lens.shape[0], float(k_scale), _ptr(k_scales),
+        _ptr(bounds), bounds.stride(0), bounds.stride(1), _ptr(scratch), _stream(stream))
+    _check(status, "pa_page_bounds")
+
+
+def _bounds(bounds, pages, kv_heads, head_dim):
+    _typed("bounds", bounds, torch.bfloat16, 4)
+    if tuple(bounds.shape) != (pages, kv_heads, 2, head_dim) or bounds.stride(2) != head_dim:
+        raise ValueError("bounds must be [pages, kv_heads, 2, head_dim], the last two dimensions contiguous")
+
+
+def sparse_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, kv_dtype: int = KV_BF16,
+                max_batch: int, max_pages_per_seq: int, max_total_q: int, top_pages: int, first_pages: int = 1,
+                last_pages: int = 2, has_sinks: bool = False, soft_cap: float = 0.0, num_splits: int = 0,
+                num_sms: int = 0) -> PaSparsePlan:
+    """pa_sparse_plan: the plan of select_pages and sparse_attend."""
+    s = PaSparseShape(num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, page_size=page_size,
+                      kv_dtype=kv_dtype, max_batch=max_batch, max_pages_per_seq=max_pages_per_seq,
+                      max_total_q=max_total_q, top_pages=top_pages, first_pages=first_pages, last_pages=last_pages,
+                      has_sinks=1 if has_sinks else 0, soft_cap=soft_cap, num_splits=num_splits, num_sms=num_sms)
+    p = PaSparsePlan()
+    _check(load().pa_sparse_plan(ctypes.byref(s), ctypes.byref(p)), "pa_sparse_plan")
+    return p
+
+
+def _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc):
+    s = p.shape
+    _typed("q", q, torch.bfloat16, 3)
+    _typed("pages", pages, torch.int32, 3)
+    _requests(block_table, seq_lens, query_start_loc)
+    if tuple(q.shape[1:]) != (s.num_q_heads, s.head_dim):
+        raise ValueError("q must be [rows, q_heads, head_dim] of the plan")
+    if tuple(pages.shape) != (q.shape[0], s.num_kv_heads, s.top_pages) or not pages.is_contiguous():
+        raise ValueError("pages must be contiguous [rows, kv_heads, top_pages] of the plan")
+
+
+def select_pages(p: PaSparsePlan, q, bounds, block_table, seq_lens, pages, *, query_start_loc=None, scratch,
+                 stream=None):
+    """pa_select_pages: pages (int32 [rows, kv_heads, top_pages]) of each query row (bf16 q [rows, Hq, D]) by the key
+    bounds page_bounds wrote.  One row per request without query_start_loc, packed rows with it."""
+    _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc)
+    _bounds(bounds, bounds.shape[0], p.shape.num_kv_heads, p.shape.head_dim)
+    status = load().pa_select_pages(
+        ctypes.byref(p), _ptr(q), q.stride(0), q.stride(1), _ptr(bounds), bounds.stride(0), bounds.stride(1),
+        bounds.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens), _ptr(query_start_loc),
+        seq_lens.shape[0], q.shape[0], _ptr(pages), _ptr(scratch), scratch.numel() * scratch.element_size(),
+        _stream(stream))
+    _check(status, "pa_select_pages")
+
+
+def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, pages, *, query_start_loc=None,
+                  scale: float, out, lse=None, sinks=None, k_scale: float = 1.0, v_scale: float = 1.0, k_scales=None,
+                  v_scales=None, scratch, stream=None):
+    """pa_sparse_attend: attention of each query row over the pages chosen for it (q / out bf16 [rows, Hq, D], lse
+    fp32 [rows, Hq])."""
+    s = p.shape
+    sp, st, sh = _kv_strides(k_cache, v_cache)
+    _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc)
+    _cache("k_cache", k_cache, s.kv_dtype)
+    _cache("v_cache", v_cache, s.kv_dtype)
+    _typed("out", out, torch.bfloat16, 3)
+    _typed("lse", lse, torch.float32, 2)
+    for name, t, n in (("sinks", sinks, s.num_q_heads), ("k_scales", k_scales, seq_lens.shape[0]),
+                       ("v_scales", v_scales, seq_lens.shape[0])):
+        _typed(name, t, torch.float32, 1)
+        if t is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must be [{n}]")
+    if tuple(k_cache.shape[1:]) != (s.page_size, s.num_kv_heads, s.head_dim):
+        raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] of the plan")
+    if out.shape != q.shape or (lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous())):
+        raise ValueError("out must be [rows, q_heads, head_dim], lse contiguous [rows, q_heads]")
+    status = load().pa_sparse_attend(
+        ctypes.byref(p), _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), sp, st, sh,
+        k_cache.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens), _ptr(query_start_loc),
+        seq_lens.shape[0], q.shape[0], _ptr(pages), float(scale), _ptr(sinks), float(k_scale), float(v_scale),
+        _ptr(k_scales), _ptr(v_scales), _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(scratch),
+        scratch.numel() * scratch.element_size(), _stream(stream))
+    _check(status, "pa_sparse_attend")
 
 
 def debug_wait_expiry(scratch, which: int, limit_ns: int, stream=None):
