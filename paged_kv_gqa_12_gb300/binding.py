@@ -306,11 +306,13 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
     """Norm and rotation for append_rope_kv.  ``cos_sin``: fp32 [max_position, rot_dim] (cosines, then sines; None
     with rot_dim 0); ``sections``: pairs per position axis (None: one axis); ``q_norm`` / ``k_norm``: bf16 [head_dim]
     RMS norm weights or None.  The tensors are kept alive by the returned struct."""
-    _typed("q_norm", q_norm, torch.bfloat16, 1)
-    _typed("k_norm", k_norm, torch.bfloat16, 1)
-    _typed("cos_sin", cos_sin, torch.float32, 2)
     if (cos_sin is None) != (rot_dim == 0):
         raise ValueError("cos_sin is given exactly when rot_dim > 0")
+    dev = _device(*(t for t in (cos_sin, q_norm, k_norm) if t is not None))
+    for name, t, dtype, dims in (("q_norm", q_norm, torch.bfloat16, 1), ("k_norm", k_norm, torch.bfloat16, 1),
+                                 ("cos_sin", cos_sin, torch.float32, 2)):
+        if t is not None:
+            _typed(name, t, dtype, dims, dev)
     if cos_sin is not None and cos_sin.shape[1] != rot_dim:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
     sec = [int(x) for x in sections] if sections is not None else [rot_dim // 2]
@@ -324,94 +326,134 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
     return r
 
 
-def _typed(name, t, dtype, dims):
+# A call of a few microseconds on the GPU should not wait for its checks: they
+# take each property once and raise from _typed alone.
+
+def _device(*tensors) -> int:
+    """The current CUDA device, which the first tensor (or none) has to be on."""
+    if tensors and tensors[0].get_device() < 0:
+        raise ValueError("tensors must be on the current CUDA device")
+    return torch.cuda.current_device() if tensors else -1
+
+
+def _typed(name, t, dtype, dims, dev):
     """Refuse a tensor of another type, rank or device, or without a contiguous innermost dimension."""
-    if t is None:
-        return
-    if t.dtype != dtype or t.dim() != dims:
+    if t.dtype is not dtype or t.dim() != dims:
         raise ValueError(f"{name} must be a {dims}-d {dtype} tensor")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the current CUDA device")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(dims - 1) != 1 and t.shape[dims - 1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
-def _cache(name, t, kv_dtype):
-    _typed(name, t, torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16, 4)
+def _raw_stream(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _pair(k_name, k, v_name, v, dtype, dims, dev):
+    """Two tensors of one type, shape and strides; returns both tuples."""
+    _typed(k_name, k, dtype, dims, dev)
+    _typed(v_name, v, dtype, dims, dev)
+    shape, stride = k.shape, k.stride()
+    if v.shape != shape or v.stride() != stride:
+        raise ValueError(f"{k_name} and {v_name} must share shape and strides")
+    return shape, stride
+
+
+def _cache_type(kv_dtype):
+    return torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16
 
 
 def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_mapping, *, q=None, q_out=None,
                    kv_dtype: int = KV_BF16, k_scale: float = 1.0, v_scale: float = 1.0, scratch=None, stream=None):
     """pa_append_rope_kv: norm and rotate q (bf16 [T, Hq, D], into q_out) and k_new (bf16 [T, Hkv, D]), write k_new
     and v_new into the paged caches at slot_mapping (int64 [T]).  positions: int32 [T], or [axes, T]."""
-    sp, st, sh = _kv_strides(k_cache, v_cache)
-    T = k_new.shape[0]
-    for name, t in (("q", q), ("q_out", q_out), ("k_new", k_new), ("v_new", v_new)):
-        _typed(name, t, torch.bfloat16, 3)
-    _cache("k_cache", k_cache, kv_dtype)
-    _cache("v_cache", v_cache, kv_dtype)
-    _typed("slot_mapping", slot_mapping, torch.int64, 1)
-    if tuple(k_new.stride()) != tuple(v_new.stride()) or k_new.shape != v_new.shape:
-        raise ValueError("k_new and v_new must share shape and strides")
-    if k_new.shape[1:] != k_cache.shape[2:] or slot_mapping.shape[0] != T:
+    dev = _device(k_new)
+    (T, hkv, D), ns = _pair("k_new", k_new, "v_new", v_new, torch.bfloat16, 3, dev)
+    cs, kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _cache_type(kv_dtype), 4, dev)
+    _typed("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    if cs[2] != hkv or cs[3] != D or slot_mapping.shape[0] != T:
         raise ValueError("k_new must be [tokens, kv_heads, head_dim] of the cache, slot_mapping [tokens]")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    if q is not None and (q.shape != q_out.shape or q.shape[0] != T or q.shape[2] != k_new.shape[2]):
-        raise ValueError("q and q_out must be [tokens, q_heads, head_dim]")
-    for name, w in zip(("q_norm", "k_norm"), getattr(r, "tensors", (None,) * 3)[1:]):
-        if w is not None and w.shape[0] != k_new.shape[2]:
-            raise ValueError(f"{name} must be [head_dim]")
-    ps = 0
+    hq, qp, qs, op, os_ = 0, None, (0, 0), None, (0, 0)
+    if q is not None:
+        _typed("q", q, torch.bfloat16, 3, dev)
+        _typed("q_out", q_out, torch.bfloat16, 3, dev)
+        shape = q.shape
+        if q_out.shape != shape or shape[0] != T or shape[2] != D:
+            raise ValueError("q and q_out must be [tokens, q_heads, head_dim]")
+        hq, qp, qs, op, os_ = shape[1], q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
+    for w in getattr(r, "tensors", (None,))[1:]:
+        if w is not None and w.shape[0] != D:
+            raise ValueError("q_norm and k_norm must be [head_dim]")
+    pp, ps = None, 0
     if r.rot_dim > 0:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        _typed("positions", positions, torch.int32, positions.dim())
-        if tuple(positions.shape) not in ((r.num_axes, T), (T,) if r.num_axes == 1 else ()):
+        dims, axes = positions.dim(), r.num_axes
+        _typed("positions", positions, torch.int32, dims, dev)
+        shape = positions.shape
+        if not (dims == 2 and shape[0] == axes and shape[1] == T or dims == 1 and axes == 1 and shape[0] == T):
             raise ValueError("positions must be [axes, tokens] ([tokens] for one axis)")
-        ps = positions.stride(0) if positions.dim() == 2 else T
-    hq = 0 if q is None else q.shape[1]
+        pp, ps = positions.data_ptr(), positions.stride(0) if dims == 2 else T
     status = load().pa_append_rope_kv(
-        ctypes.byref(r), _ptr(q), 0 if q is None else q.stride(0), 0 if q is None else q.stride(1), _ptr(q_out),
-        0 if q is None else q_out.stride(0), 0 if q is None else q_out.stride(1), hq, _ptr(k_new), _ptr(v_new),
-        k_new.stride(0), k_new.stride(1), _ptr(positions), ps, _ptr(k_cache), _ptr(v_cache), sp, st, sh,
-        k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], k_cache.shape[3], int(kv_dtype), _ptr(slot_mapping), T,
-        float(k_scale), float(v_scale), _ptr(scratch), _stream(stream))
+        ctypes.byref(r), qp, qs[0], qs[1], op, os_[0], os_[1], hq, k_new.data_ptr(), v_new.data_ptr(), ns[0], ns[1], pp,
+        ps, k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2], cs[0], cs[1], hkv, D, kv_dtype,
+        slot_mapping.data_ptr(), T, k_scale, v_scale, None if scratch is None else scratch.data_ptr(),
+        _raw_stream(stream, dev))
     _check(status, "pa_append_rope_kv")
 
 
-def _requests(block_table, seq_lens, query_start_loc):
-    _typed("block_table", block_table, torch.int32, 2)
-    _typed("seq_lens", seq_lens, torch.int32, 1)
-    _typed("query_start_loc", query_start_loc, torch.int32, 1)
-    if block_table.shape[0] < seq_lens.shape[0]:
+def _requests(block_table, seq_lens, query_start_loc, dev):
+    """Checks of the request metadata; returns the batch size."""
+    _typed("block_table", block_table, torch.int32, 2, dev)
+    _typed("seq_lens", seq_lens, torch.int32, 1, dev)
+    batch = seq_lens.shape[0]
+    if block_table.shape[0] < batch:
         raise ValueError("block_table must have a row per request")
-    if query_start_loc is not None and query_start_loc.shape[0] != seq_lens.shape[0] + 1:
-        raise ValueError("query_start_loc must be [batch + 1]")
+    if query_start_loc is not None:
+        _typed("query_start_loc", query_start_loc, torch.int32, 1, dev)
+        if query_start_loc.shape[0] != batch + 1:
+            raise ValueError("query_start_loc must be [batch + 1]")
+    return batch
+
+
+def _bounds(bounds, pages, kv_heads, head_dim, dev):
+    """Checks of a bounds tensor; returns its strides."""
+    _typed("bounds", bounds, torch.bfloat16, 4, dev)
+    s = bounds.stride()
+    if bounds.shape != (pages, kv_heads, 2, head_dim) or s[2] != head_dim:
+        raise ValueError("bounds must be [pages, kv_heads, 2, head_dim], the last two dimensions contiguous")
+    return s
+
+
+def _floats(name, t, n, dev):
+    """Pointer of an optional fp32 [n] tensor."""
+    if t is None:
+        return None
+    _typed(name, t, torch.float32, 1, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}]")
+    return t.data_ptr()
 
 
 def page_bounds(k_cache, block_table, seq_lens, bounds, *, query_start_loc=None, kv_dtype: int = KV_BF16,
                 k_scale: float = 1.0, k_scales=None, scratch=None, stream=None):
     """pa_page_bounds: refresh bounds (bf16 [pages, kv_heads, 2, head_dim]: smallest, largest key value per dim) of
     the pages that hold new tokens (query_start_loc), or of every page of the requests (None)."""
-    _cache("k_cache", k_cache, kv_dtype)
-    _requests(block_table, seq_lens, query_start_loc)
-    _typed("k_scales", k_scales, torch.float32, 1)
-    _bounds(bounds, k_cache.shape[0], k_cache.shape[2], k_cache.shape[3])
-    if k_scales is not None and k_scales.shape[0] != seq_lens.shape[0]:
-        raise ValueError("k_scales must be [batch]")
+    dev = _device(k_cache)
+    _typed("k_cache", k_cache, _cache_type(kv_dtype), 4, dev)
+    batch = _requests(block_table, seq_lens, query_start_loc, dev)
+    (pages, ps, hkv, D), ks = k_cache.shape, k_cache.stride()
+    bs = _bounds(bounds, pages, hkv, D, dev)
     status = load().pa_page_bounds(
-        _ptr(k_cache), k_cache.stride(0), k_cache.stride(1), k_cache.stride(2), k_cache.shape[0], k_cache.shape[1],
-        k_cache.shape[2], k_cache.shape[3], int(kv_dtype), _ptr(block_table), block_table.stride(0),
-        block_table.shape[1], _ptr(seq_lens), _ptr(query_start_loc), seq_lens.shape[0], float(k_scale), _ptr(k_scales),
-        _ptr(bounds), bounds.stride(0), bounds.stride(1), _ptr(scratch), _stream(stream))
+        k_cache.data_ptr(), ks[0], ks[1], ks[2], pages, ps, hkv, D, kv_dtype, block_table.data_ptr(),
+        block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
+        None if query_start_loc is None else query_start_loc.data_ptr(), batch, k_scale,
+        _floats("k_scales", k_scales, batch, dev), bounds.data_ptr(), bs[0], bs[1],
+        None if scratch is None else scratch.data_ptr(), _raw_stream(stream, dev))
     _check(status, "pa_page_bounds")
-
-
-def _bounds(bounds, pages, kv_heads, head_dim):
-    _typed("bounds", bounds, torch.bfloat16, 4)
-    if tuple(bounds.shape) != (pages, kv_heads, 2, head_dim) or bounds.stride(2) != head_dim:
-        raise ValueError("bounds must be [pages, kv_heads, 2, head_dim], the last two dimensions contiguous")
 
 
 def sparse_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, kv_dtype: int = KV_BF16,
@@ -428,28 +470,32 @@ def sparse_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size
     return p
 
 
-def _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc):
-    s = p.shape
-    _typed("q", q, torch.bfloat16, 3)
-    _typed("pages", pages, torch.int32, 3)
-    _requests(block_table, seq_lens, query_start_loc)
-    if tuple(q.shape[1:]) != (s.num_q_heads, s.head_dim):
+def _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev):
+    """Checks of query rows and their page lists against a plan's shape; returns (rows, batch)."""
+    _typed("q", q, torch.bfloat16, 3, dev)
+    _typed("pages", pages, torch.int32, 3, dev)
+    batch = _requests(block_table, seq_lens, query_start_loc, dev)
+    rows, hq, D = q.shape
+    if hq != s.num_q_heads or D != s.head_dim:
         raise ValueError("q must be [rows, q_heads, head_dim] of the plan")
-    if tuple(pages.shape) != (q.shape[0], s.num_kv_heads, s.top_pages) or not pages.is_contiguous():
+    if pages.shape != (rows, s.num_kv_heads, s.top_pages) or not pages.is_contiguous():
         raise ValueError("pages must be contiguous [rows, kv_heads, top_pages] of the plan")
+    return rows, batch
 
 
 def select_pages(p: PaSparsePlan, q, bounds, block_table, seq_lens, pages, *, query_start_loc=None, scratch,
                  stream=None):
     """pa_select_pages: pages (int32 [rows, kv_heads, top_pages]) of each query row (bf16 q [rows, Hq, D]) by the key
     bounds page_bounds wrote.  One row per request without query_start_loc, packed rows with it."""
-    _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc)
-    _bounds(bounds, bounds.shape[0], p.shape.num_kv_heads, p.shape.head_dim)
+    dev, s = _device(q), p.shape
+    rows, batch = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
+    pool = bounds.shape[0]
+    bs = _bounds(bounds, pool, s.num_kv_heads, s.head_dim, dev)
+    qs = q.stride()
     status = load().pa_select_pages(
-        ctypes.byref(p), _ptr(q), q.stride(0), q.stride(1), _ptr(bounds), bounds.stride(0), bounds.stride(1),
-        bounds.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens), _ptr(query_start_loc),
-        seq_lens.shape[0], q.shape[0], _ptr(pages), _ptr(scratch), scratch.numel() * scratch.element_size(),
-        _stream(stream))
+        ctypes.byref(p), q.data_ptr(), qs[0], qs[1], bounds.data_ptr(), bs[0], bs[1], pool, block_table.data_ptr(),
+        block_table.stride(0), seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(),
+        batch, rows, pages.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
     _check(status, "pa_select_pages")
 
 
@@ -458,28 +504,26 @@ def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, p
                   v_scales=None, scratch, stream=None):
     """pa_sparse_attend: attention of each query row over the pages chosen for it (q / out bf16 [rows, Hq, D], lse
     fp32 [rows, Hq])."""
-    s = p.shape
-    sp, st, sh = _kv_strides(k_cache, v_cache)
-    _sparse_rows(p, q, pages, block_table, seq_lens, query_start_loc)
-    _cache("k_cache", k_cache, s.kv_dtype)
-    _cache("v_cache", v_cache, s.kv_dtype)
-    _typed("out", out, torch.bfloat16, 3)
-    _typed("lse", lse, torch.float32, 2)
-    for name, t, n in (("sinks", sinks, s.num_q_heads), ("k_scales", k_scales, seq_lens.shape[0]),
-                       ("v_scales", v_scales, seq_lens.shape[0])):
-        _typed(name, t, torch.float32, 1)
-        if t is not None and t.shape[0] != n:
-            raise ValueError(f"{name} must be [{n}]")
-    if tuple(k_cache.shape[1:]) != (s.page_size, s.num_kv_heads, s.head_dim):
+    dev, s = _device(q), p.shape
+    rows, batch = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
+    (pool, ps, hkv, D), kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _cache_type(s.kv_dtype), 4, dev)
+    if ps != s.page_size or hkv != s.num_kv_heads or D != s.head_dim:
         raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] of the plan")
-    if out.shape != q.shape or (lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous())):
-        raise ValueError("out must be [rows, q_heads, head_dim], lse contiguous [rows, q_heads]")
+    _typed("out", out, torch.bfloat16, 3, dev)
+    if out.shape != q.shape:
+        raise ValueError("out must be [rows, q_heads, head_dim]")
+    if lse is not None:
+        _typed("lse", lse, torch.float32, 2, dev)
+        if lse.shape != (rows, s.num_q_heads) or not lse.is_contiguous():
+            raise ValueError("lse must be contiguous [rows, q_heads]")
+    qs, os_ = q.stride(), out.stride()
     status = load().pa_sparse_attend(
-        ctypes.byref(p), _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(v_cache), sp, st, sh,
-        k_cache.shape[0], _ptr(block_table), block_table.stride(0), _ptr(seq_lens), _ptr(query_start_loc),
-        seq_lens.shape[0], q.shape[0], _ptr(pages), float(scale), _ptr(sinks), float(k_scale), float(v_scale),
-        _ptr(k_scales), _ptr(v_scales), _ptr(out), out.stride(0), out.stride(1), _ptr(lse), _ptr(scratch),
-        scratch.numel() * scratch.element_size(), _stream(stream))
+        ctypes.byref(p), q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2],
+        pool, block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(),
+        None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows, pages.data_ptr(), scale,
+        _floats("sinks", sinks, s.num_q_heads, dev), k_scale, v_scale, _floats("k_scales", k_scales, batch, dev),
+        _floats("v_scales", v_scales, batch, dev), out.data_ptr(), os_[0], os_[1],
+        None if lse is None else lse.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
     _check(status, "pa_sparse_attend")
 
 

@@ -213,8 +213,6 @@ def test_binding_refuses_tensors_of_another_kind(lib):
     cpu = torch.zeros(8, 32, 128, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA device"):
         pb.select_pages(p, cpu, None, None, None, None, scratch=None)
-    with pytest.raises(ValueError, match="3-d"):
-        pb.select_pages(p, cpu.float(), None, None, None, None, scratch=None)
     with pytest.raises(ValueError, match="rot_dim"):
         pb.rope(rot_dim=64)
     with pytest.raises(ValueError, match="axes"):
