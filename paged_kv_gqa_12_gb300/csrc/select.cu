@@ -10,12 +10,12 @@
 // kv head and block of query rows.
 //
 // The chosen pages are those of the exact sums.  The tensor cores sum in 32
-// bits: products of bf16 are exact there, each of the 2 D additions is off by at
-// most 2^-22 of the largest partial sum (a factor of two above one truncated
-// 24-bit addition), and every partial sum is at most |q|_1 A, A the largest
-// bound in magnitude.  So |s - u| <= eps = D 2^-21 |q|_1 A, and against the K-th
-// largest s, t, pages above t + 2 eps are in, pages below t - 2 eps are out, and
-// only those between are summed again, in 64 bits.
+// bits: products of bf16 are exact there, one of a dim's two products is zero,
+// and each of the other D, with the 2 D / 16 running sums they are added to, is
+// off by at most 2^-23 of the largest partial sum; that is at most |q|_1 A, A
+// the largest bound in magnitude.  So |s - u| <= eps = D 2^-22 |q|_1 A, and against
+// the K-th largest s, t, pages above t + 2 eps are in, pages below t - 2 eps are
+// out, and only those between are summed again, in 64 bits.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -29,8 +29,9 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kScoreCtas = 8;          // per SM, at least, while a chunk keeps kScorePagesMin pages
+constexpr int kPer = 8;                // scores a selection thread keeps in registers
+constexpr int kBins = 2048;            // steps of the score histogram
 constexpr int kListCap = 512;          // undecided pages ranked in shared memory
 
 struct SelectParams {
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
   const int r_begin = p.row0 + blockIdx.x * p.block_rows;
   const int r_end = min(r_begin + p.block_rows, p.row0 + p.rows);
   const int G = p.group, C = p.cols;
+  pdl_launch_dependents();   // the selection may start up; it waits for this grid's scores
 
   int row = r_begin;
   while (row < r_end) {
@@ -127,20 +129,47 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     const int64_t out_row0 = (static_cast<int64_t>(first_row - p.row0) * p.num_kv_heads + kvh) * p.row_pages;
     const int64_t tok_stride = static_cast<int64_t>(p.num_kv_heads) * p.row_pages;
     float a_max = 0.f;
-    for (int p0 = chunk0 + warp * 16; p0 < end; p0 += kScoreWarps * 16) {
-      uint4 a[2][NP];
+    // the 16 pages at p0: pool pages of rows g and g + 8 (-1: none), their bounds
+    auto page_ids = [&](int p0, int (&id)[2]) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int pg = p0 + g + 8 * h;
-        int id = pg < end ? bt[pg] : -1;
-        if (pg < end && static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-          if (c == 0) atomicOr(p.err, kErrPageId);
-          id = -1;
-        }
-        const uint16_t* src = p.bounds + id * p.bounds_stride_page + kvh * p.bounds_stride_head + 8 * c;
+        id[h] = pg < end ? bt[pg] : -1;
+      }
+    };
+    auto fetch = [&](int p0, const int (&id)[2], auto& a) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool ok = static_cast<unsigned>(id[h]) < static_cast<unsigned>(p.num_pages);
+        if (!ok && p0 + g + 8 * h < end && c == 0) atomicOr(p.err, kErrPageId);
+        const uint16_t* src = p.bounds + id[h] * p.bounds_stride_page + kvh * p.bounds_stride_head + 8 * c;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
-          a[h][i] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+          a[h][i] = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    constexpr int kStep = kScoreWarps * 16;
+    constexpr bool kAhead = D <= 128;  // a second set of fragments fits the registers
+    int id[2];
+    uint4 next[kAhead ? 2 : 1][kAhead ? NP : 1];
+    int p0 = chunk0 + warp * 16;
+    page_ids(p0, id);
+    if constexpr (kAhead) {
+      if (p0 < end) fetch(p0, id, next);
+      page_ids(p0 + kStep, id);
+    }
+    for (; p0 < end; p0 += kStep) {
+      uint4 a[2][NP];
+      if constexpr (kAhead) {          // the next pages' bounds, and the ids of those behind them
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < NP; ++i) a[h][i] = next[h][i];
+        if (p0 + kStep < end) fetch(p0 + kStep, id, next);
+        page_ids(p0 + 2 * kStep, id);
+      } else {
+        fetch(p0, id, a);
+        page_ids(p0 + kStep, id);
       }
       // the largest finite bound (a page with another one has no finite score)
 #pragma unroll
@@ -219,104 +248,104 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
 
 // ---- selection ----------------------------------------------------------------
 
-// Order-preserving map of a float (no NaN; -0 counts as 0) to unsigned.
-__device__ __forceinline__ uint32_t key32(float f) {
-  const uint32_t u = __float_as_uint(f + 0.f);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float from_key32(uint32_t k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
-}
-__device__ __forceinline__ uint64_t key64(double f) {
+__device__ __forceinline__ uint64_t key64(double f) {   // order-preserving; -0 counts as 0
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(f + 0.0));
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
 struct SelShared {
-  uint32_t hist[256];
-  uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
-  uint32_t digit, left;
-  int n_list;
+  uint32_t hist[kBins];
+  float red[4][32];
+  uint32_t warp_sum[32];
+  uint32_t infs, decided, n_open, digit, left;
   double value[kListCap];
   int index[kListCap];
 };
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* tmp) {
+// Over the CTA: the maximum of each of N values (T threads; every thread gets it).
+template <int T, int N>
+__device__ __forceinline__ void block_max(float (&v)[N], SelShared& s) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, k));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) v = max(v, tmp[w]);
-  return v;
-}
-__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t* tmp) {
+    for (int k = 16; k > 0; k >>= 1) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], k));
+  if (lane == 0)
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
+    for (int i = 0; i < N; ++i) s.red[i][threadIdx.x >> 5] = v[i];
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
 #pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) v += tmp[w];
-  return v;
+  for (int i = 0; i < N; ++i) {
+    v[i] = s.red[i][lane < T / 32 ? lane : 0];
+#pragma unroll
+    for (int k = T / 64; k > 0; k >>= 1) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], k));
+    v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+  }
 }
 
-// The k-th largest (k >= 1) of the keys that get(i, &key) yields for i in [0, n),
-// by 8 bits at a time from the top of the range they span.
-template <class Get>
-__device__ uint32_t kth_largest(SelShared& s, int n, uint32_t k, Get get) {
-  const int tid = threadIdx.x;
-  uint32_t top = 0, low_inv = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    uint32_t key;
-    if (!get(i, &key)) continue;
-    top = max(top, key);
-    low_inv = max(low_inv, ~key);
-  }
-  top = block_max(top, s.warp_a);
-  const uint32_t low = ~block_max(low_inv, s.warp_b);
-  const uint32_t span = top - low;
-  int shift = span == 0 ? 0 : 32 - __clz(span);     // bits the range takes
-  uint32_t prefix = 0;                              // of key - low, above `shift`
-  while (shift > 0) {
-    const int bits = min(8, shift);
-    const int below = shift - bits;
-    s.hist[tid] = 0;                                // (256 threads, 256 bins)
-    __syncthreads();
-    for (int i = tid; i < n; i += kSelThreads) {
-      uint32_t key;
-      if (!get(i, &key)) continue;
-      const uint32_t x = key - low;
-      if ((shift < 32 ? x >> shift : 0u) == prefix) atomicAdd(&s.hist[(x >> below) & ((1u << bits) - 1u)], 1u);
-    }
-    __syncthreads();
-    // count of the bins above each: thread t takes bin 255 - t
-    uint32_t mine = s.hist[255 - tid], sum = mine;
+// Sum of v over the threads before this one.
+template <int T>
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, SelShared& s) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t sum = v;
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, m);
-      if ((tid & 31) >= m) sum += v;
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, sum, m);
+    if (lane >= m) sum += x;
+  }
+  __syncthreads();
+  if (lane == 31) s.warp_sum[warp] = sum;
+  __syncthreads();
+  uint32_t w = lane < warp ? s.warp_sum[lane] : 0u;
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) w += __shfl_xor_sync(0xffffffffu, w, k);
+  return w + sum - v;
+}
+
+// The bin of s.hist[0 .. n_bins) (n_bins a multiple of T or half of it) that
+// holds the k-th largest, into s.digit, and its rank within the bin, into s.left.
+template <int T>
+__device__ __forceinline__ void find_bin(SelShared& s, int n_bins, uint32_t k) {
+  const int per = n_bins > T ? n_bins / T : 1;
+  const int first = n_bins - 1 - static_cast<int>(threadIdx.x) * per;   // this thread's highest bin
+  uint32_t mine = 0;
+  if (first >= 0)
+    for (int i = 0; i < per; ++i) mine += s.hist[first - i];
+  uint32_t before = sum_before<T>(mine, s);
+  if (before < k && before + mine >= k)   // (one thread)
+    for (int i = 0; i < per; ++i) {
+      const uint32_t h = s.hist[first - i];
+      if (before + h >= k) {
+        s.digit = first - i;
+        s.left = k - before;
+        break;
+      }
+      before += h;
     }
-    if ((tid & 31) == 31) s.warp_a[tid >> 5] = sum;
+  __syncthreads();
+}
+
+// The k-th largest of the 32-bit keys in `keys` of the pages marked in `open`.
+template <int T>
+__device__ uint32_t kth_largest(SelShared& s, const uint32_t* keys, const uint32_t* open, int n, uint32_t k) {
+  uint32_t prefix = 0;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = threadIdx.x; i < 256; i += T) s.hist[i] = 0;
     __syncthreads();
-    for (int w = 0; w < (tid >> 5); ++w) sum += s.warp_a[w];
-    if (sum >= k && sum - mine < k) {               // exactly one bin
-      s.digit = 255 - tid;
-      s.left = k - (sum - mine);
-    }
+    for (int i = threadIdx.x; i < n; i += T)
+      if ((open[i >> 5] >> (i & 31) & 1u) != 0 && (shift == 24 || keys[i] >> (shift + 8) == prefix))
+        atomicAdd(&s.hist[keys[i] >> shift & 255u], 1u);
     __syncthreads();
-    prefix = (prefix << bits) | s.digit;
+    find_bin<T>(s, 256, k);
+    prefix = prefix << 8 | s.digit;
     k = s.left;
-    shift = below;
     __syncthreads();
   }
-  return low + prefix;
+  return prefix;
 }
 
-// Exact score of a page for the group, in 64 bits, by one warp.
+// Exact score of a page for the group, in 64 bits, by one warp.  Four heads at a
+// time: their sums are independent, the 64-bit pipe is slow.
 template <int D>
 __device__ double exact_score(const SelectParams& p, const int32_t* bt, int row, int kvh, int page) {
   constexpr int V = D / 32;                          // dims per lane
@@ -334,43 +363,52 @@ __device__ double exact_score(const SelectParams& p, const int32_t* bt, int row,
   }
   if (__any_sync(0xffffffffu, odd)) return INFINITY;
   double best = -INFINITY;
-  for (int j = 0; j < p.group; ++j) {
-    const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
-                        static_cast<int64_t>(kvh * p.group + j) * p.q_stride_head + lane * V;
-    double sum = 0.0;
+  for (int j0 = 0; j0 < p.group; j0 += 4) {
+    double sum[4];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float x = bf16_to_f32(q[e]);
-      sum += static_cast<double>(x) * static_cast<double>(x < 0.f ? l[e] : h[e]);
+    for (int u = 0; u < 4; ++u) {                    // (heads beyond the group repeat its last one)
+      const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
+                          static_cast<int64_t>(kvh * p.group + min(j0 + u, p.group - 1)) * p.q_stride_head + lane * V;
+      sum[u] = 0.0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float x = bf16_to_f32(q[e]);
+        sum[u] += static_cast<double>(x) * static_cast<double>(x < 0.f ? l[e] : h[e]);
+      }
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-    if (!(fabs(sum) <= DBL_MAX)) sum = INFINITY;
-    best = fmax(best, sum);
+    for (int k = 16; k > 0; k >>= 1)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], k);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) best = fmax(best, fabs(sum[u]) <= DBL_MAX ? sum[u] : INFINITY);
   }
   return best;
 }
 
-// One CTA = one (query row, kv head).  Which pages are chosen, and which are
-// still undecided, is kept as bit maps in shared memory; the chosen ones are
-// written out in ascending order at the end.
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t bits[];                 // chosen, then undecided
+// One CTA = one (query row, kv head); a thread keeps kPer of the row's scores in
+// registers (rows of more than kPer T pages read them again).  The K-th largest
+// is located by one histogram over kBins equal steps between the smallest and
+// the largest score: its step's two edges take the place of t, so a page is in
+// above the upper edge + 2 eps and out below the lower edge - 2 eps.  What is
+// chosen and what is open is kept as bit maps in shared memory, and the chosen
+// pages are written in ascending order at the end.
+template <int D, int T>
+__global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
+  constexpr int W = T / 32;
+  extern __shared__ uint32_t bits[];                 // chosen, then open
   __shared__ SelShared s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = p.row0 + blockIdx.x;
   const int kvh = blockIdx.y;
-  const RowPlace at = find_row<kSelThreads>(p.seq_lens, p.qsl, p.batch, row, p.max_len);
-  if (at.b < 0) return;
-  if (at.bad) {
-    if (tid == 0) atomicOr(p.err, kErrCapacity);
-    return;
-  }
+  const RowPlace at = find_row<T>(p.seq_lens, p.qsl, p.batch, row, p.max_len);
   const int n = at.pos < 0 ? 0 : (at.pos >> p.ps_log2) + 1;
   int32_t* out = p.pages + (static_cast<int64_t>(row) * p.num_kv_heads + kvh) * p.top;
-  if (n <= p.top) {                                  // every page
-    for (int i = tid; i < p.top; i += kSelThreads) out[i] = i < n ? i : -1;
+  if (at.b < 0 || at.bad || n <= p.top) {
+    if (at.b >= 0 && at.bad && tid == 0) atomicOr(p.err, kErrCapacity);
+    if (at.b >= 0 && !at.bad)
+      for (int i = tid; i < p.top; i += T) out[i] = i < n ? i : -1;   // every page
+    pdl_wait_primary();                              // (this grid ends no earlier than the scores')
     return;
   }
   const int words = (n + 31) / 32;
@@ -382,156 +420,196 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
   const int lo = p.first, hi = n - p.last;           // pages chosen by score: [lo, hi)
   const uint32_t want = p.top - p.first - p.last;    // (n > top, so hi - lo > want)
 
-  float above = INFINITY, below = INFINITY;          // scores beyond decide; [below, above] is open
+  // the largest |q|_1 of the group's heads (before the scores are waited for)
+  float q1 = 0.f;
+  for (int j = warp; j < p.group; j += W) {
+    const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
+                        static_cast<int64_t>(kvh * p.group + j) * p.q_stride_head;
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) sum += fabsf(bf16_to_f32(q[lane + 32 * e]));
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    q1 = sum <= FLT_MAX ? fmaxf(q1, sum) : INFINITY;
+  }
+  for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
+  if (tid == 0) s.infs = s.decided = s.n_open = 0;
+  __syncthreads();
+  pdl_wait_primary();
+
+  // scores of pages that are not chosen by score read as -infinity, which none has
+  float first_v[kPer];
+  auto load = [&](int i) { return i >= lo && i < hi ? score[i] : -INFINITY; };
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) first_v[j] = load(j * T + tid);
+  auto each = [&](auto f) {                          // f(page, score): whole warps on 32 neighbours
+    for (int base = 0; base < n; base += kPer * T) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int i = base + j * T + tid;
+        if (i - lane < n) f(i, base == 0 ? first_v[j] : load(i));
+      }
+    }
+  };
+
+  float above = INFINITY, below = INFINITY;
   bool all_open = false, ties = true;                // ties: what is open is exactly equal
   if (want > 0) {
-    // eps of this row
-    float q1 = 0.f;
-    for (int j = warp; j < p.group; j += kSelWarps) {
-      const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
-                          static_cast<int64_t>(kvh * p.group + j) * p.q_stride_head;
-      float sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) sum += fabsf(bf16_to_f32(q[lane + 32 * e]));
-#pragma unroll
-      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-      q1 = sum > q1 || sum != sum ? sum : q1;
-    }
-    // (non-negative floats order as integers, a NaN above them all)
-    q1 = __uint_as_float(block_max(__float_as_uint(q1) & 0x7fffffffu, s.warp_a));
-    float am = 0.f;
+    float v[4] = {-INFINITY, -INFINITY, 0.f, q1};    // largest and -smallest finite score, A, |q|_1
+    uint32_t infs = 0;
+    each([&](int, float x) {
+      infs += x == INFINITY;
+      if (fabsf(x) <= FLT_MAX) {
+        v[0] = fmaxf(v[0], x);
+        v[1] = fmaxf(v[1], -x);
+      }
+    });
     const int chunks = (hi + p.chunk_pages - 1) / p.chunk_pages;
-    for (int i = tid; i < chunks; i += kSelThreads) am = fmaxf(am, p.amax[cell * p.n_chunks + i]);
-    am = __uint_as_float(block_max(__float_as_uint(am), s.warp_b));
+    for (int i = tid; i < chunks; i += T) v[2] = fmaxf(v[2], p.amax[cell * p.n_chunks + i]);
+    if (infs != 0) atomicAdd(&s.infs, infs);
+    block_max<T>(v, s);                              // (its barrier publishes s.infs)
+    infs = s.infs;
+    const float top = v[0], low = -v[1], am = v[2];
     // |q|_1 itself is summed in 32 bits: a hundredth more covers it; sums below
     // the normal range may be flushed: 2 D times the smallest normal covers them.
     // A q that is not finite gives every page +infinity, a zero one zero: exact.
-    const float size = q1 * am;
-    const float eps = !(q1 <= FLT_MAX) || q1 == 0.f || am == 0.f ? 0.f
-                      : size <= FLT_MAX ? 1.01f * (D * 0x1p-21f) * size + 2 * D * FLT_MIN : INFINITY;
-
-    const uint32_t kth = kth_largest(s, hi - lo, want, [&](int i, uint32_t* key) {
-      *key = key32(score[lo + i]);
-      return true;
-    });
-    const float t = from_key32(kth);
+    const float size = v[3] * am;
+    const float eps = !(v[3] <= FLT_MAX) || v[3] == 0.f || am == 0.f ? 0.f
+                      : size <= FLT_MAX ? 1.01f * (D * 0x1p-22f) * size + 2 * D * FLT_MIN : INFINITY;
     all_open = !(eps <= FLT_MAX);
-    ties = !all_open && (eps == 0.f || t == INFINITY);
-    above = __fadd_ru(t, 2.f * eps);
-    below = __fadd_rd(t, -2.f * eps);
+    ties = !all_open;
+    if (infs >= want && !all_open) {
+      above = below = INFINITY;                      // infinities alone, all alike
+    } else if (!all_open) {
+      ties = eps == 0.f && top == low;
+      float t_lo = low, t_hi = top;
+      const float half = 0.5f * top - 0.5f * low;    // (does not overflow)
+      const float step = kBins / half;
+      if (half > 0.f && step <= FLT_MAX) {
+        auto bin = [&](float x) { return min(kBins - 1, static_cast<int>((0.5f * x - 0.5f * low) * step)); };
+        each([&](int, float x) {
+          if (fabsf(x) <= FLT_MAX) atomicAdd(&s.hist[bin(x)], 1u);
+        });
+        __syncthreads();
+        find_bin<T>(s, kBins, want - infs);
+        // the step's edges, with room for the roundings of bin() and of this
+        const float width = 2.f * (half / kBins), slop = 0x1p-20f * (fabsf(top) + fabsf(low));
+        t_lo = fmaxf(low, low + s.digit * width - slop);
+        t_hi = fminf(top, low + (s.digit + 1) * width + slop);
+      }
+      above = __fadd_ru(t_hi, 2.f * eps);
+      below = __fadd_rd(t_lo, -2.f * eps);
+    }
   }
 
   // decide what 32 bits can
-  if (tid == 0) s.n_list = 0;
-  __syncthreads();
-  uint32_t decided = 0, n_open = 0;
-  for (int w = warp; w < words; w += kSelWarps) {
-    const int i = w * 32 + lane;
-    bool in = i < n && (i < lo || i >= hi), maybe = false;
-    bool scored = false;
-    if (want > 0 && i >= lo && i < hi) {
-      const float x = score[i];
-      scored = !all_open && x > above;
-      maybe = all_open || (!scored && x >= below);
-      in |= scored;
-    }
-    const uint32_t in_w = __ballot_sync(0xffffffffu, in), open_w = __ballot_sync(0xffffffffu, maybe);
-    const uint32_t scored_w = __ballot_sync(0xffffffffu, scored);
+  each([&](int i, float x) {
+    const bool cand = want > 0 && x != -INFINITY;
+    const bool sure = cand && !all_open && x > above;
+    const bool maybe = cand && !sure && (all_open || x >= below);
+    const uint32_t in_w = __ballot_sync(0xffffffffu, sure || (i < n && (i < lo || i >= hi)));
+    const uint32_t open_w = __ballot_sync(0xffffffffu, maybe);
+    const uint32_t sure_w = __ballot_sync(0xffffffffu, sure);
+    uint32_t at_list = 0;
     if (lane == 0) {
-      chosen[w] = in_w;
-      open[w] = open_w;
-      decided += __popc(scored_w);
-      n_open += __popc(open_w);
+      chosen[i >> 5] = in_w;
+      open[i >> 5] = open_w;
+      if (sure_w != 0) atomicAdd(&s.decided, __popc(sure_w));
+      if (open_w != 0) at_list = atomicAdd(&s.n_open, __popc(open_w));
     }
-  }
-  decided = block_sum(decided, s.warp_a);
-  n_open = block_sum(n_open, s.warp_b);
-  uint32_t need = want - decided;                    // to take from the open ones
+    if (open_w != 0) {                               // (the same for the warp)
+      at_list = __shfl_sync(0xffffffffu, at_list, 0) + __popc(open_w & ((1u << lane) - 1u));
+      if (maybe && at_list < kListCap) s.index[at_list] = i;
+    }
+  });
+  __syncthreads();
+  const uint32_t n_open = s.n_open;
+  uint32_t need = want - s.decided;                  // to take from the open ones
 
   if (need > 0 && need < n_open && !ties) {
     if (n_open <= kListCap) {
       // rank them by their exact scores
-      for (int w = tid; w < words; w += kSelThreads)
-        for (uint32_t m = open[w]; m != 0; m &= m - 1) s.index[atomicAdd(&s.n_list, 1)] = w * 32 + __ffs(m) - 1;
-      __syncthreads();
-      for (int i = warp; i < static_cast<int>(n_open); i += kSelWarps) {
+      for (uint32_t i = warp; i < n_open; i += W) {
         const double v = exact_score<D>(p, bt, row, kvh, s.index[i]);
         if (lane == 0) s.value[i] = v;
       }
       __syncthreads();
-      for (int i = tid; i < static_cast<int>(n_open); i += kSelThreads) {
+      for (uint32_t i = tid; i < n_open; i += T) {
         const double v = s.value[i];
         const int page = s.index[i];
         uint32_t better = 0;
-        for (int j = 0; j < static_cast<int>(n_open); ++j)
-          better += s.value[j] > v || (s.value[j] == v && s.index[j] < page);
+        for (uint32_t j = 0; j < n_open; ++j) better += s.value[j] > v || (s.value[j] == v && s.index[j] < page);
         if (better < need) atomicOr(&chosen[page >> 5], 1u << (page & 31));
       }
       need = 0;
     } else {
       // too many to rank: the need-th largest exact score by its upper, then its
       // lower 32 bits, kept in place of the 32-bit scores
+      uint32_t* keys = reinterpret_cast<uint32_t*>(score);
       for (int half = 0; half < 2 && need > 0; ++half) {
-        for (int w = warp; w < words; w += kSelWarps)
+        for (int w = warp; w < words; w += W)
           for (uint32_t m = open[w]; m != 0; m &= m - 1) {
             const int i = w * 32 + __ffs(m) - 1;
             const uint64_t k = key64(exact_score<D>(p, bt, row, kvh, i));
-            if (lane == 0) score[i] = __uint_as_float(static_cast<uint32_t>(half == 0 ? k >> 32 : k));
+            if (lane == 0) keys[i] = static_cast<uint32_t>(half == 0 ? k >> 32 : k);
           }
         __syncthreads();
-        const uint32_t kth = kth_largest(s, n, need, [&](int i, uint32_t* key) {
-          *key = __float_as_uint(score[i]);
-          return (open[i >> 5] >> (i & 31) & 1u) != 0;
-        });
+        const uint32_t kth = kth_largest<T>(s, keys, open, n, need);
         uint32_t taken = 0;
+        if (tid == 0) s.decided = 0;
         __syncthreads();
-        for (int w = tid; w < words; w += kSelThreads) {
+        for (int w = tid; w < words; w += T) {
           uint32_t win = 0, stay = 0;
           for (uint32_t m = open[w]; m != 0; m &= m - 1) {
             const int b = __ffs(m) - 1;
-            const uint32_t key = __float_as_uint(score[w * 32 + b]);
-            win |= (key > kth ? 1u : 0u) << b;
-            stay |= (key == kth ? 1u : 0u) << b;
+            win |= (keys[w * 32 + b] > kth ? 1u : 0u) << b;
+            stay |= (keys[w * 32 + b] == kth ? 1u : 0u) << b;
           }
           chosen[w] |= win;
           open[w] = stay;
           taken += __popc(win);
         }
-        need -= block_sum(taken, s.warp_a);
+        if (taken != 0) atomicAdd(&s.decided, taken);
+        __syncthreads();
+        need -= s.decided;
+        __syncthreads();
       }
     }
   }
   __syncthreads();
 
-  // the lowest `need` of what is still open are equal to the border: take them;
-  // then write the chosen pages in order.  Thread t holds words [t per, (t+1) per).
-  const int per = (words + kSelThreads - 1) / kSelThreads;
-  auto scan = [&](uint32_t v) {                      // sum over the threads before this one
-    uint32_t sum = v;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, sum, m);
-      if (lane >= m) sum += x;
-    }
-    __syncthreads();
-    if (lane == 31) s.warp_a[warp] = sum;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) sum += s.warp_a[w];
-    return sum - v;
-  };
+  // the lowest `need` of what is still open equal the border: take them; then
+  // write the chosen pages in order.  Thread t holds words [t per, (t + 1) per).
+  const int per = (words + T - 1) / T;
+  const int w0 = tid * per, w1 = min(w0 + per, words);
   if (need > 0) {
     uint32_t mine = 0;
-    for (int w = tid * per; w < min((tid + 1) * per, words); ++w) mine += __popc(open[w]);
-    uint32_t before = scan(mine);
-    for (int w = tid * per; w < min((tid + 1) * per, words); ++w)
+    for (int w = w0; w < w1; ++w) mine += __popc(open[w]);
+    uint32_t before = sum_before<T>(mine, s);
+    for (int w = w0; w < w1; ++w)
       for (uint32_t m = open[w]; m != 0 && before < need; m &= m - 1, ++before) chosen[w] |= m & (0u - m);
   }
   uint32_t mine = 0;
-  for (int w = tid * per; w < min((tid + 1) * per, words); ++w) mine += __popc(chosen[w]);
-  uint32_t at_out = scan(mine);
-  for (int w = tid * per; w < min((tid + 1) * per, words); ++w)
+  for (int w = w0; w < w1; ++w) mine += __popc(chosen[w]);
+  uint32_t at_out = sum_before<T>(mine, s);
+  for (int w = w0; w < w1; ++w)
     for (uint32_t m = chosen[w]; m != 0 && at_out < static_cast<uint32_t>(p.top); m &= m - 1)
       out[at_out++] = w * 32 + __ffs(m) - 1;
+}
+
+template <int D, int T>
+cudaError_t launch_select(const SelectParams& p, bool scored, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.rows, p.num_kv_heads);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = p.row_pages / 32 * 8;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = scored ? 1 : 0;   // overlaps the score kernel's end, and waits for its scores
+  return cudaLaunchKernelEx(&cfg, select_kernel<D, T>, p);
 }
 
 template <int D>
@@ -545,9 +623,11 @@ cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
     score_kernel<D><<<grid, kScoreThreads, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const dim3 grid(p.rows, p.num_kv_heads);
-  select_kernel<D><<<grid, kSelThreads, p.row_pages / 32 * 8, st>>>(p);
-  return cudaGetLastError();
+  // threads per row: so many that the longest row's scores stay in registers
+  if (p.row_pages <= 128 * kPer) return launch_select<D, 128>(p, chunks > 0, st);
+  if (p.row_pages <= 256 * kPer) return launch_select<D, 256>(p, chunks > 0, st);
+  if (p.row_pages <= 512 * kPer) return launch_select<D, 512>(p, chunks > 0, st);
+  return launch_select<D, 1024>(p, chunks > 0, st);
 }
 
 }  // namespace
@@ -611,7 +691,7 @@ extern "C" pa_status pa_select_pages(const pa_sparse_plan_t* plan, const void* q
   const int64_t blocks = static_cast<int64_t>((std::min(total_q, plan->score_rows) + block - 1) / block);
   const int64_t pages_all = blocks * s.num_kv_heads * p.row_pages;
   int64_t chunk = kScorePagesMin;
-  while (chunk * 2 <= 1024 && pages_all / (chunk * 2) >= static_cast<int64_t>(s.num_sms) * 8) chunk *= 2;
+  while (chunk * 2 <= 1024 && pages_all / (chunk * 2) >= static_cast<int64_t>(s.num_sms) * kScoreCtas) chunk *= 2;
   p.chunk_pages = static_cast<int>(chunk);
   // a capacity of no more than top_pages pages needs no scores
   const int chunks = s.max_pages_per_seq <= s.top_pages || s.top_pages == s.first_pages + s.last_pages
