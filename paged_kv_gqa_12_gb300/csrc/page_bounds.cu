@@ -158,45 +158,50 @@ __global__ void __launch_bounds__(kThreads) page_bounds_kernel(const BoundsParam
         const int filled = min(ps, s_len[lo] - pg * ps);
         const uint8_t* src = p.k_cache + id * p.stride_page + h * p.stride_head + part * 16;
         uint16_t* dst = p.bounds + id * p.bounds_stride_page + h * p.bounds_stride_head + part * NE;
+        // Batches of kUnroll slots, the next one's loads ahead of this one's
+        // comparisons; beyond the filled slots the last of them is read again.
         uint32_t mn[16 / E / 2], mx[16 / E / 2];
-        {
-          const uint4 w = *reinterpret_cast<const uint4*>(src);   // slot 0: filled, as the page is
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        uint4 w[2][kUnroll];
+        auto load = [&](uint4 (&x)[kUnroll], int s0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (E == 2) {
-              mn[i] = mx[i] = x[i];
-            } else {
-              mn[2 * i] = mx[2 * i] = e4m3x2_f16x2<0>(x[i]);
-              mn[2 * i + 1] = mx[2 * i + 1] = e4m3x2_f16x2<1>(x[i]);
-            }
-          }
-        }
-        // (a slot beyond the filled ones reads slot 0 once more)
-        for (int s0 = 1; s0 < filled; s0 += kUnroll) {
-          uint4 w[kUnroll];
+          for (int k = 0; k < kUnroll; ++k)
+            x[k] = *reinterpret_cast<const uint4*>(src + min(s0 + k, filled - 1) * p.stride_tok);
+        };
+        auto fold = [&](const uint4 (&x)[kUnroll]) {
 #pragma unroll
-          for (int k = 0; k < kUnroll; ++k) {
-            const int s = s0 + k < filled ? s0 + k : 0;
-            w[k] = *reinterpret_cast<const uint4*>(src + s * p.stride_tok);
-          }
-#pragma unroll
-          for (int k = 0; k < kUnroll; ++k) {
-            const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          for (int k = 0; k < kUnroll; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const uint32_t v = (&x[k].x)[i];
               if constexpr (E == 2) {
-                mn[i] = min_bf16x2(mn[i], x[i]);
-                mx[i] = max_bf16x2(mx[i], x[i]);
+                mn[i] = min_bf16x2(mn[i], v);
+                mx[i] = max_bf16x2(mx[i], v);
               } else {
-                const uint32_t y0 = e4m3x2_f16x2<0>(x[i]), y1 = e4m3x2_f16x2<1>(x[i]);
+                const uint32_t y0 = e4m3x2_f16x2<0>(v), y1 = e4m3x2_f16x2<1>(v);
                 mn[2 * i] = min_f16x2(mn[2 * i], y0);
                 mx[2 * i] = max_f16x2(mx[2 * i], y0);
                 mn[2 * i + 1] = min_f16x2(mn[2 * i + 1], y1);
                 mx[2 * i + 1] = max_f16x2(mx[2 * i + 1], y1);
               }
             }
+        };
+        load(w[0], 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = (&w[0][0].x)[i];
+          if constexpr (E == 2) {
+            mn[i] = mx[i] = v;
+          } else {
+            mn[2 * i] = mx[2 * i] = e4m3x2_f16x2<0>(v);
+            mn[2 * i + 1] = mx[2 * i + 1] = e4m3x2_f16x2<1>(v);
           }
+        }
+        for (int s0 = 0; s0 < filled; s0 += 2 * kUnroll) {
+          if (s0 + kUnroll < filled) load(w[1], s0 + kUnroll);
+          fold(w[0]);
+          if (s0 + kUnroll >= filled) break;
+          if (s0 + 2 * kUnroll < filled) load(w[0], s0 + 2 * kUnroll);
+          fold(w[1]);
         }
         if constexpr (E == 2) {
           *reinterpret_cast<uint4*>(dst) = make_uint4(mn[0], mn[1], mn[2], mn[3]);

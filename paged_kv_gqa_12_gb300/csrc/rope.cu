@@ -47,7 +47,7 @@ struct RopeParams {
   uint8_t* k_cache;
   uint8_t* v_cache;
   int64_t stride_page, stride_tok, stride_head;   // bytes
-  int num_pages, page_size, num_q_heads, num_kv_heads, num_tokens;
+  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;   // ps_log2: -1, no power of two
   int half;              // rot_dim / 2
   int interleaved, num_axes, max_position;
   int axis_end[4];       // first pair behind each axis
@@ -71,19 +71,45 @@ __device__ __forceinline__ uint32_t quant4(const float* x, float scale) {
   return lo | (hi << 16);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int U>
 __global__ void __launch_bounds__(kThreads) append_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 8;                  // lanes per row
   constexpr int ROWS = kThreads / LPR;        // rows a CTA holds at a time
   const int t = blockIdx.x;
   const int lane = threadIdx.x % LPR;
   const int sub = threadIdx.x / LPR;
+  // this lane's two 4-element vectors of a row
+  const bool turns = 4 * lane < p.half;
+  const bool apart = turns && !p.interleaved;
+  const int da = apart ? 4 * lane : 8 * lane;
+  const int db = apart ? p.half + 4 * lane : 8 * lane + 4;
+
+  // U rows at a time, their loads ahead of everything else
+  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
+  uint2 wa[U], wb[U];
+  auto kind_of = [&](int r) { return r < p.num_q_heads ? 0 : (r < p.num_q_heads + p.num_kv_heads ? 1 : 2); };   // q, k, v
+  auto head_of = [&](int r, int kind) { return kind == 0 ? r : r - p.num_q_heads - (kind - 1) * p.num_kv_heads; };
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * ROWS + sub;
+      wa[u] = wb[u] = make_uint2(0u, 0u);
+      if (r < rows) {
+        const int kind = kind_of(r), h = head_of(r, kind);
+        const uint16_t* src = kind == 0 ? p.q + t * p.q_stride_tok + h * p.q_stride_head
+                              : (kind == 1 ? p.k_new : p.v_new) + t * p.new_stride_tok + h * p.new_stride_head;
+        wa[u] = *reinterpret_cast<const uint2*>(src + da);
+        wb[u] = *reinterpret_cast<const uint2*>(src + db);
+      }
+    }
+  };
+  load(0);
 
   const int64_t slot = p.slot_mapping[t];
   if (slot < 0) return;                       // padding token
-  const int64_t page = slot / p.page_size;
+  const int64_t page = p.ps_log2 >= 0 ? slot >> p.ps_log2 : slot / p.page_size;
   if (page >= p.num_pages) {                  // outside the pool: nothing written
-    if (p.err != nullptr && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, kErrPageId);
+    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, kErrPageId);
     return;
   }
   int pos[4] = {0, 0, 0, 0};
@@ -97,21 +123,15 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const RopeParams 
       }
   }
   if (bad) {
-    if (p.err != nullptr && threadIdx.x == 0 && blockIdx.y == 0) atomicOr(p.err, PA_DEVICE_POSITION);
+    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, PA_DEVICE_POSITION);
     return;
   }
 
-  // this lane's two 4-element vectors and the cosines and sines of its four pairs
-  const bool turns = 4 * lane < p.half;
-  int da = 8 * lane, db = 8 * lane + 4;
+  // the cosines and sines of this lane's four pairs
   float cs[4], sn[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) cs[e] = 1.f, sn[e] = 0.f;
   if (turns) {
-    if (!p.interleaved) {
-      da = 4 * lane;
-      db = p.half + 4 * lane;
-    }
     if (p.num_axes == 1) {
       const float* row = p.cos_sin + pos[0] * p.cos_sin_stride + 4 * lane;
       const float4 c = __ldg(reinterpret_cast<const float4*>(row));
@@ -131,91 +151,88 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const RopeParams 
     }
   }
 
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
   const int64_t cell = page * p.stride_page + (slot - page * p.page_size) * p.stride_tok;
   const bool norms = p.q_norm != nullptr || p.k_norm != nullptr;
-  for (int r0 = blockIdx.y * ROWS; r0 < rows; r0 += gridDim.y * ROWS) {
-    const int r = r0 + sub;
-    const bool on = r < rows;
-    const int kind = r < p.num_q_heads ? 0 : (r < p.num_q_heads + p.num_kv_heads ? 1 : 2);   // q, k, v
-    const int h = kind == 0 ? r : r - p.num_q_heads - (kind - 1) * p.num_kv_heads;
-    uint2 wa = make_uint2(0u, 0u), wb = make_uint2(0u, 0u);
-    if (on) {
-      const uint16_t* src = kind == 0 ? p.q + t * p.q_stride_tok + h * p.q_stride_head
-                            : (kind == 1 ? p.k_new : p.v_new) + t * p.new_stride_tok + h * p.new_stride_head;
-      wa = *reinterpret_cast<const uint2*>(src + da);
-      wb = *reinterpret_cast<const uint2*>(src + db);
-    }
-    float a[4], b[4];
-    unpack4(wa, a);
-    unpack4(wb, b);
-    if (norms) {   // (the same for the whole CTA: every lane of the warp shuffles)
-      float ss = 0.f;
+  for (int r0 = 0; r0 < rows; r0 += U * ROWS) {
+    if (r0 > 0) load(r0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) ss += a[e] * a[e] + b[e] * b[e];
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * ROWS + sub;
+      const int kind = kind_of(r), h = head_of(r, kind);
+      float a[4], b[4];
+      unpack4(wa[u], a);
+      unpack4(wb[u], b);
+      if (norms) {   // (the same for the whole CTA: every lane of the warp shuffles)
+        float ss = 0.f;
 #pragma unroll
-      for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      const uint16_t* w = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : nullptr);
-      if (w != nullptr) {
-        const float rs = rsqrtf(ss * (1.f / D) + p.norm_eps);
-        float u[4], v[4];
-        unpack4(__ldg(reinterpret_cast<const uint2*>(w + da)), u);
-        unpack4(__ldg(reinterpret_cast<const uint2*>(w + db)), v);
+        for (int e = 0; e < 4; ++e) ss += a[e] * a[e] + b[e] * b[e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          a[e] *= rs * (u[e] + p.norm_offset);
-          b[e] *= rs * (v[e] + p.norm_offset);
+        for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+        const uint16_t* w = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : nullptr);
+        if (w != nullptr) {
+          const float rs = rsqrtf(ss * (1.f / D) + p.norm_eps);
+          float x[4], y[4];
+          unpack4(__ldg(reinterpret_cast<const uint2*>(w + da)), x);
+          unpack4(__ldg(reinterpret_cast<const uint2*>(w + db)), y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a[e] *= rs * (x[e] + p.norm_offset);
+            b[e] *= rs * (y[e] + p.norm_offset);
+          }
         }
       }
-    }
-    if (turns && kind != 2) {
-      if (p.interleaved) {   // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
+      if (r >= rows) continue;
+      if (turns && kind != 2) {
+        if (p.interleaved) {   // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const float x = a[e], y = b[e];
-          a[e] = x * cs[e / 2] - a[e + 1] * sn[e / 2];
-          a[e + 1] = a[e + 1] * cs[e / 2] + x * sn[e / 2];
-          b[e] = y * cs[2 + e / 2] - b[e + 1] * sn[2 + e / 2];
-          b[e + 1] = b[e + 1] * cs[2 + e / 2] + y * sn[2 + e / 2];
-        }
-      } else {               // pairs (a_e, b_e)
+          for (int e = 0; e < 4; e += 2) {
+            const float x = a[e], y = b[e];
+            a[e] = x * cs[e / 2] - a[e + 1] * sn[e / 2];
+            a[e + 1] = a[e + 1] * cs[e / 2] + x * sn[e / 2];
+            b[e] = y * cs[2 + e / 2] - b[e + 1] * sn[2 + e / 2];
+            b[e + 1] = b[e + 1] * cs[2 + e / 2] + y * sn[2 + e / 2];
+          }
+        } else {               // pairs (a_e, b_e)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = a[e];
-          a[e] = x * cs[e] - b[e] * sn[e];
-          b[e] = b[e] * cs[e] + x * sn[e];
+          for (int e = 0; e < 4; ++e) {
+            const float x = a[e];
+            a[e] = x * cs[e] - b[e] * sn[e];
+            b[e] = b[e] * cs[e] + x * sn[e];
+          }
         }
       }
-    }
-    if (!on) continue;
-    if (FP8 && kind != 0) {
-      uint8_t* dst = (kind == 1 ? p.k_cache : p.v_cache) + cell + h * p.stride_head;
-      const float scale = kind == 1 ? p.k_scale : p.v_scale;
-      *reinterpret_cast<uint32_t*>(dst + da) = quant4(a, scale);
-      *reinterpret_cast<uint32_t*>(dst + db) = quant4(b, scale);
-    } else {
-      uint16_t* dst = kind == 0 ? p.q_out + t * p.qo_stride_tok + h * p.qo_stride_head
-                                : reinterpret_cast<uint16_t*>((kind == 1 ? p.k_cache : p.v_cache) + cell +
-                                                              h * p.stride_head);
-      if (kind != 2) {   // (values keep their bits)
-        wa = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-        wb = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+      if (FP8 && kind != 0) {
+        uint8_t* dst = (kind == 1 ? p.k_cache : p.v_cache) + cell + h * p.stride_head;
+        const float scale = kind == 1 ? p.k_scale : p.v_scale;
+        *reinterpret_cast<uint32_t*>(dst + da) = quant4(a, scale);
+        *reinterpret_cast<uint32_t*>(dst + db) = quant4(b, scale);
+      } else {
+        uint16_t* dst = kind == 0 ? p.q_out + t * p.qo_stride_tok + h * p.qo_stride_head
+                                  : reinterpret_cast<uint16_t*>((kind == 1 ? p.k_cache : p.v_cache) + cell +
+                                                                h * p.stride_head);
+        if (kind != 2) {       // (values keep their bits)
+          wa[u] = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
+          wb[u] = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
+        }
+        *reinterpret_cast<uint2*>(dst + da) = wa[u];
+        *reinterpret_cast<uint2*>(dst + db) = wb[u];
       }
-      *reinterpret_cast<uint2*>(dst + da) = wa;
-      *reinterpret_cast<uint2*>(dst + db) = wb;
     }
   }
 }
 
+template <int D, bool FP8>
+cudaError_t launch_rows(const RopeParams& p, cudaStream_t st) {
+  const int passes = (p.num_q_heads + 2 * p.num_kv_heads + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
+  auto kern = passes == 1 ? append_rope_kernel<D, FP8, 1> : passes == 2 ? append_rope_kernel<D, FP8, 2>
+              : passes == 3 ? append_rope_kernel<D, FP8, 3> : append_rope_kernel<D, FP8, 4>;
+  kern<<<p.num_tokens, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch(const RopeParams& p, bool fp8, cudaStream_t st) {
-  const dim3 grid(p.num_tokens);
-  if (fp8) {
-    append_rope_kernel<D, true><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    append_rope_kernel<D, false><<<grid, kThreads, 0, st>>>(p);
-  }
-  return cudaGetLastError();
+  return fp8 ? launch_rows<D, true>(p, st) : launch_rows<D, false>(p, st);
 }
 
 }  // namespace
@@ -307,6 +324,7 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   p.stride_head = kv_stride_head * e;
   p.num_pages = num_pages;
   p.page_size = page_size;
+  p.ps_log2 = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(page_size)) : -1;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
   p.num_tokens = num_tokens;

@@ -29,10 +29,10 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScoreCtas = 8;          // per SM, at least, while a chunk keeps kScorePagesMin pages
-constexpr int kPer = 8;                // scores a selection thread keeps in registers
-constexpr int kBins = 2048;            // steps of the score histogram
-constexpr int kListCap = 512;          // undecided pages ranked in shared memory
+
+// Selection by T threads a row: scores kept per thread, steps of the score
+// histogram, undecided pages ranked in shared memory.
+template <int T> struct Sel { static constexpr int kPer = 8, kBins = T <= 256 ? 4 * T : 2048, kListCap = 2 * T < 512 ? 2 * T : 512; };
 
 struct SelectParams {
   const uint16_t* q;
@@ -44,7 +44,7 @@ struct SelectParams {
   int64_t bt_stride;
   const int32_t* seq_lens;
   const int32_t* qsl;
-  int batch, num_kv_heads, group, cols, ps_log2;   // cols: score columns per token (>= group)
+  int batch, num_kv_heads, group, hpt, ps_log2;   // hpt: heads of a token in a score tile (1, 2, 4, 8)
   int64_t max_len;
   int top, first, last;
   int row0, rows;             // query rows of this pass
@@ -62,16 +62,55 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {   //
   asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ float finite_or_inf(float s) { return fabsf(s) <= FLT_MAX ? s : INFINITY; }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// A sum that is not finite becomes NaN, which max_nan carries to the end.
+__device__ __forceinline__ float nan_if_infinite(float s) { return fmaf(s, 0.f, s); }
+__device__ __forceinline__ float inf_if_nan(float s) { return s == s ? s : INFINITY; }
+
+// 16 bytes of bounds: read once by this kernel, neighbours soon
+__device__ __forceinline__ uint4 load_bounds(const uint16_t* src) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(src));
+  return v;
+}
+
+// Two bf16 split by sign bit into the factors of the lower and of the upper
+// bounds; a NaN of either sign spoils its own half, which is enough.
+__device__ __forceinline__ uint32_t sign_mask(uint32_t x) {   // 0xffff where a bf16 is negative
+  uint32_t m;
+  asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(m) : "r"(x));
+  return m;
+}
+__device__ __forceinline__ uint32_t negatives(uint32_t x) { return x & sign_mask(x); }
+__device__ __forceinline__ uint32_t positives(uint32_t x) { return x & ~sign_mask(x); }
+__device__ __forceinline__ uint4 negatives(uint4 x) {
+  return make_uint4(negatives(x.x), negatives(x.y), negatives(x.z), negatives(x.w));
+}
+__device__ __forceinline__ uint4 positives(uint4 x) {
+  return make_uint4(positives(x.x), positives(x.y), positives(x.z), positives(x.w));
+}
 
 // ---- scores -------------------------------------------------------------------
-// One CTA = (page chunk, kv head, block of query rows).  A warp takes 16 pages as
+// One CTA = (kv head, page chunk, block of query rows).  A warp takes 16 pages as
 // the M rows of its MMAs, their 2 D bounds loaded straight from global memory
 // into A fragments: thread (g, c) of the fragment holds any four k-pairs of rows
 // g and g + 8 as long as B agrees, so it takes 16 contiguous bytes for two
-// k-steps, and the query coefficients in shared memory are read the same way.
-template <int D>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams p) {
+// k-steps, and the query factors are read the same way.
+//
+// ONE: a block of one row of at most 8 heads (decode).  The query factors stay in
+// registers, no warp waits for another, and the kernel is the stream of the
+// bounds.  Otherwise the factors of the block's rows lie in shared memory: a
+// tile of 8 columns holds `hpt` heads of 8 / hpt tokens, the group's heads run
+// over the tiles of a token group, and their maximum is taken in registers (and
+// over the hpt columns by shuffles, none for blocks of 8 tokens and more).
+template <int D, bool ONE>
+__global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(const SelectParams p) {
   constexpr int K2 = 2 * D;
   constexpr int NP = K2 / 32;                 // 16-byte pieces per thread and row
   constexpr int QROW = K2 * 2 + 64;           // bytes of a query column: rows 64 bytes apart in the banks
@@ -79,11 +118,12 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
   __shared__ float s_a[kScoreWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int kvh = blockIdx.y;
-  const int chunk0 = blockIdx.z * p.chunk_pages;
-  const int r_begin = p.row0 + blockIdx.x * p.block_rows;
+  const int block = blockIdx.x / p.num_kv_heads;
+  const int kvh = blockIdx.x - block * p.num_kv_heads;
+  const int chunk0 = blockIdx.y * p.chunk_pages;
+  const int r_begin = p.row0 + block * p.block_rows;
   const int r_end = min(r_begin + p.block_rows, p.row0 + p.rows);
-  const int G = p.group, C = p.cols;
+  const int G = p.group;
   pdl_launch_dependents();   // the selection may start up; it waits for this grid's scores
 
   int row = r_begin;
@@ -99,78 +139,60 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     const int n = at.pos + m - 1 < 0 ? 0 : ((at.pos + m - 1) >> p.ps_log2) + 1;
     if (n <= p.top || chunk0 >= n - p.last) continue;
     const int end = min(chunk0 + p.chunk_pages, n - p.last);
-
-    // [q- | q+] of every column (token, head); heads beyond the group repeat head
-    // 0, which changes no maximum
-    const int tiles = (m * C + 7) / 8;
-    __syncthreads();
-    for (int i = tid; i < tiles * 8 * (D / 8); i += kScoreThreads) {
-      const int col = i / (D / 8), d = (i % (D / 8)) * 8;
-      const int tok = col / C, j = col - tok * C;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (tok < m)
-        w = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(first_row + tok) * p.q_stride_tok +
-                                            static_cast<int64_t>(kvh * G + (j < G ? j : 0)) * p.q_stride_head + d);
-      uint32_t x[4] = {w.x, w.y, w.z, w.w}, lo[4], hi[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // by sign bit; a NaN of either sign spoils its own half, which is enough
-        const uint32_t neg = ((x[e] >> 15) & 0x00010001u) * 0xffffu;
-        lo[e] = x[e] & neg;
-        hi[e] = x[e] & ~neg;
-      }
-      uint8_t* dst = qs + col * QROW + d * 2;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(dst + D * 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    }
-    __syncthreads();
-
     const int32_t* bt = p.block_table + at.b * p.bt_stride;
+    const uint16_t* q0 = p.q + static_cast<int64_t>(first_row) * p.q_stride_tok +
+                         static_cast<int64_t>(kvh * G) * p.q_stride_head;
+
+    // pool pages of fragment rows g and g + 8; pages behind the chunk's end repeat
+    // its last one, a page outside the pool reads page 0 (and scores 0 below)
+    int id[2];
+    bool lost[2];
+    auto page_ids = [&](int p0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) id[h] = bt[min(p0 + g + 8 * h, end - 1)];
+    };
+    page_ids(chunk0 + warp * 16);
+
+    uint4 q_one[ONE ? NP / 2 : 1];
+    const int tpt = 8 / p.hpt;
+    const int groups = (m + tpt - 1) / tpt, head_tiles = (G + p.hpt - 1) / p.hpt;
+    if constexpr (ONE) {                      // column g is head g (or head 0 again)
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i)
+        q_one[i] = *reinterpret_cast<const uint4*>(q0 + static_cast<int64_t>(g < G ? g : 0) * p.q_stride_head +
+                                                   32 * i + 8 * c);
+    } else {
+      __syncthreads();
+      for (int i = tid; i < groups * head_tiles * 8 * (D / 8); i += kScoreThreads) {
+        const int col = i / (D / 8), d = (i % (D / 8)) * 8;
+        const int tile = col >> 3, tg = tile / head_tiles;
+        const int tok = tg * tpt + (col & 7) / p.hpt;
+        const int head = (tile - tg * head_tiles) * p.hpt + (col & (p.hpt - 1));
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < m)                          // heads beyond the group repeat head 0: the same maximum
+          x = *reinterpret_cast<const uint4*>(q0 + tok * p.q_stride_tok +
+                                              static_cast<int64_t>(head < G ? head : 0) * p.q_stride_head + d);
+        *reinterpret_cast<uint4*>(qs + col * QROW + d * 2) = negatives(x);
+        *reinterpret_cast<uint4*>(qs + col * QROW + (D + d) * 2) = positives(x);
+      }
+      __syncthreads();
+    }
+
     const int64_t out_row0 = (static_cast<int64_t>(first_row - p.row0) * p.num_kv_heads + kvh) * p.row_pages;
     const int64_t tok_stride = static_cast<int64_t>(p.num_kv_heads) * p.row_pages;
     float a_max = 0.f;
-    // the 16 pages at p0: pool pages of rows g and g + 8 (-1: none), their bounds
-    auto page_ids = [&](int p0, int (&id)[2]) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int pg = p0 + g + 8 * h;
-        id[h] = pg < end ? bt[pg] : -1;
-      }
-    };
-    auto fetch = [&](int p0, const int (&id)[2], auto& a) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool ok = static_cast<unsigned>(id[h]) < static_cast<unsigned>(p.num_pages);
-        if (!ok && p0 + g + 8 * h < end && c == 0) atomicOr(p.err, kErrPageId);
-        const uint16_t* src = p.bounds + id[h] * p.bounds_stride_page + kvh * p.bounds_stride_head + 8 * c;
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-          a[h][i] = ok ? __ldg(reinterpret_cast<const uint4*>(src + 32 * i)) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    constexpr int kStep = kScoreWarps * 16;
-    constexpr bool kAhead = D <= 128;  // a second set of fragments fits the registers
-    int id[2];
-    uint4 next[kAhead ? 2 : 1][kAhead ? NP : 1];
-    int p0 = chunk0 + warp * 16;
-    page_ids(p0, id);
-    if constexpr (kAhead) {
-      if (p0 < end) fetch(p0, id, next);
-      page_ids(p0 + kStep, id);
-    }
-    for (; p0 < end; p0 += kStep) {
+    for (int p0 = chunk0 + warp * 16; p0 < end; p0 += kScoreWarps * 16) {
       uint4 a[2][NP];
-      if constexpr (kAhead) {          // the next pages' bounds, and the ids of those behind them
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        lost[h] = static_cast<unsigned>(id[h]) >= static_cast<unsigned>(p.num_pages);
+        const uint16_t* src = p.bounds + (lost[h] ? 0 : id[h]) * p.bounds_stride_page +
+                              kvh * p.bounds_stride_head + 8 * c;
 #pragma unroll
-          for (int i = 0; i < NP; ++i) a[h][i] = next[h][i];
-        if (p0 + kStep < end) fetch(p0 + kStep, id, next);
-        page_ids(p0 + 2 * kStep, id);
-      } else {
-        fetch(p0, id, a);
-        page_ids(p0 + kStep, id);
+        for (int i = 0; i < NP; ++i) a[h][i] = load_bounds(src + 32 * i);
       }
+      if (lost[0] || lost[1]) atomicOr(p.err, kErrPageId);
+      page_ids(p0 + kScoreWarps * 16);        // (of the next pages)
       // the largest finite bound (a page with another one has no finite score)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -185,52 +207,65 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
         const float f = __uint_as_float((v & 0x7fffu) << 16);
         if (f <= FLT_MAX) a_max = fmaxf(a_max, f);
       }
-      float best[4];
-      int tile_in_token = 0;
-      for (int t = 0; t < tiles; ++t) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint8_t* src = qs + (t * 8 + g) * QROW + 16 * c;
+      for (int tg = 0; tg < groups; ++tg) {
+        // columns 2c, 2c + 1 of pages g (0, 1) and g + 8 (2, 3)
+        float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto take = [&](float (&d)[4]) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-          const uint4 b = *reinterpret_cast<const uint4*>(src + 64 * i);
-          const uint32_t f0[4] = {a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y};
-          const uint32_t f1[4] = {a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w};
-          mma_bf16(d, f0, b.x, b.y);
-          mma_bf16(d, f1, b.z, b.w);
-        }
+          for (int e = 0; e < 4; ++e) best[e] = max_nan(best[e], nan_if_infinite(d[e]));
+        };
+        // (independent sums side by side: one after the other they would wait on
+        // each MMA's latency)
+        if constexpr (ONE) {
+          float d[2][4] = {};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = finite_or_inf(d[e]);
-        // columns 2c, 2c + 1 of pages g (d0, d1) and g + 8 (d2, d3)
-        if (C == 1) {                          // every column is a token
+          for (int i = 0; i < NP / 2; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pg = p0 + g + 8 * (e >> 1), tok = t * 8 + 2 * c + (e & 1);
-            if (pg < end && tok < m) p.scores[out_row0 + tok * tok_stride + pg] = d[e];
+            for (int s = 0; s < 2; ++s) {
+              const uint4 b = s == 0 ? negatives(q_one[i]) : positives(q_one[i]);
+              const uint4 &x = a[0][s * (NP / 2) + i], &y = a[1][s * (NP / 2) + i];
+              const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+              mma_bf16(d[s], f0, b.x, b.y);
+              mma_bf16(d[s], f1, b.z, b.w);
+            }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[0][e] += d[1][e];
+          take(d[0]);
+        } else {
+          constexpr int U = 4;
+          const uint8_t* src0 = qs + (tg * head_tiles * 8 + g) * QROW + 16 * c;
+          for (int ht = 0; ht < head_tiles; ht += U) {
+            float d[U][4] = {};
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              const uint32_t f0[4] = {a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y};
+              const uint32_t f1[4] = {a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w};
+#pragma unroll
+              for (int u = 0; u < U; ++u) {   // (tiles beyond the last repeat it)
+                const uint4 b = *reinterpret_cast<const uint4*>(src0 + min(ht + u, head_tiles - 1) * 8 * QROW + 64 * i);
+                mma_bf16(d[u], f0, b.x, b.y);
+                mma_bf16(d[u], f1, b.z, b.w);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) take(d[u]);
           }
-          continue;
         }
-        float x = fmaxf(d[0], d[1]), y = fmaxf(d[2], d[3]);
-        if (C >= 4) {
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
-        }
-        if (C >= 8) {
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
-        }
-        if (C > 8) {                           // a token of several tiles
-          best[0] = tile_in_token == 0 ? x : fmaxf(best[0], x);
-          best[1] = tile_in_token == 0 ? y : fmaxf(best[1], y);
-          x = best[0];
-          y = best[1];
-          tile_in_token = tile_in_token + 1 == C / 8 ? 0 : tile_in_token + 1;
-          if (tile_in_token != 0) continue;
-        }
-        const int tok = (t * 8 + 2 * c) / C;
-        if (tok < m && (2 * c) % C == 0) {
-          float* dst = p.scores + out_row0 + tok * tok_stride + p0 + g;
-          if (p0 + g < end) dst[0] = x;
-          if (p0 + g + 8 < end) dst[8] = y;
+        auto store = [&](int tok, int h, float s) {
+          const int pg = p0 + g + 8 * h;
+          if (tok < m && pg < end) p.scores[out_row0 + tok * tok_stride + pg] = lost[h] ? 0.f : inf_if_nan(s);
+        };
+        if (p.hpt == 1) {                     // a column is a token
+#pragma unroll
+          for (int e = 0; e < 4; ++e) store(tg * 8 + 2 * c + (e & 1), e >> 1, best[e]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float x = max_nan(best[2 * h], best[2 * h + 1]);
+            if (p.hpt >= 4) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            if (p.hpt >= 8) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            if ((2 * c & (p.hpt - 1)) == 0) store(tg * tpt + 2 * c / p.hpt, h, x);
+          }
         }
       }
     }
@@ -241,7 +276,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const SelectParams
     if (tid < m) {
       float v = 0.f;
       for (int w = 0; w < kScoreWarps; ++w) v = fmaxf(v, s_a[w]);
-      p.amax[(static_cast<int64_t>(first_row + tid - p.row0) * p.num_kv_heads + kvh) * p.n_chunks + blockIdx.z] = v;
+      p.amax[(static_cast<int64_t>(first_row + tid - p.row0) * p.num_kv_heads + kvh) * p.n_chunks + blockIdx.y] = v;
     }
   }
 }
@@ -253,7 +288,16 @@ __device__ __forceinline__ uint64_t key64(double f) {   // order-preserving; -0 
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
+// The power of two that brings a positive finite x into [1, 2), within the normal
+// range (a zero or infinite x: any).
+__device__ __forceinline__ float inverse_power(float x) {
+  const int e = static_cast<int>(__float_as_uint(x) >> 23);          // biased exponent
+  return __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 254)) << 23);
+}
+
+template <int T>
 struct SelShared {
+  static constexpr int kBins = Sel<T>::kBins, kListCap = Sel<T>::kListCap;
   uint32_t hist[kBins];
   float red[4][32];
   uint32_t warp_sum[32];
@@ -264,7 +308,7 @@ struct SelShared {
 
 // Over the CTA: the maximum of each of N values (T threads; every thread gets it).
 template <int T, int N>
-__device__ __forceinline__ void block_max(float (&v)[N], SelShared& s) {
+__device__ __forceinline__ void block_max(float (&v)[N], SelShared<T>& s) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < N; ++i)
@@ -285,7 +329,7 @@ __device__ __forceinline__ void block_max(float (&v)[N], SelShared& s) {
 
 // Sum of v over the threads before this one.
 template <int T>
-__device__ __forceinline__ uint32_t sum_before(uint32_t v, SelShared& s) {
+__device__ __forceinline__ uint32_t sum_before(uint32_t v, SelShared<T>& s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t sum = v;
 #pragma unroll
@@ -305,7 +349,7 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, SelShared& s) {
 // The bin of s.hist[0 .. n_bins) (n_bins a multiple of T or half of it) that
 // holds the k-th largest, into s.digit, and its rank within the bin, into s.left.
 template <int T>
-__device__ __forceinline__ void find_bin(SelShared& s, int n_bins, uint32_t k) {
+__device__ __forceinline__ void find_bin(SelShared<T>& s, int n_bins, uint32_t k) {
   const int per = n_bins > T ? n_bins / T : 1;
   const int first = n_bins - 1 - static_cast<int>(threadIdx.x) * per;   // this thread's highest bin
   uint32_t mine = 0;
@@ -327,7 +371,7 @@ __device__ __forceinline__ void find_bin(SelShared& s, int n_bins, uint32_t k) {
 
 // The k-th largest of the 32-bit keys in `keys` of the pages marked in `open`.
 template <int T>
-__device__ uint32_t kth_largest(SelShared& s, const uint32_t* keys, const uint32_t* open, int n, uint32_t k) {
+__device__ uint32_t kth_largest(SelShared<T>& s, const uint32_t* keys, const uint32_t* open, int n, uint32_t k) {
   uint32_t prefix = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = threadIdx.x; i < 256; i += T) s.hist[i] = 0;
@@ -344,60 +388,87 @@ __device__ uint32_t kth_largest(SelShared& s, const uint32_t* keys, const uint32
   return prefix;
 }
 
-// Exact score of a page for the group, in 64 bits, by one warp.  Four heads at a
-// time: their sums are independent, the 64-bit pipe is slow.
+// a + b = s + e exactly (Knuth's two-sum).
+__device__ __forceinline__ void two_sum(float& a, float b, float& e) {
+  const float s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  a = s;
+}
+
+// Exact score of a page for the group by one warp, scaled by the powers of two
+// sq sa (which bring q and the bounds to about 1, so that products stay in
+// range).  A product of two bf16 is exact in 32 bits and the sums are kept in
+// three floats each, s + t + u: what is lost is below 2^-53 of the largest, and
+// the slow 64-bit pipe only joins the three.  Eight lanes take a head.
 template <int D>
-__device__ double exact_score(const SelectParams& p, const int32_t* bt, int row, int kvh, int page) {
-  constexpr int V = D / 32;                          // dims per lane
-  const int lane = threadIdx.x & 31;
+__device__ double exact_score(const SelectParams& p, const int32_t* bt, int row, int kvh, int page, float sq,
+                              float sa) {
+  const int lane = threadIdx.x & 31, slot = lane >> 3, sub = lane & 7;
   const int id = bt[page];
   if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) return 0.0;
-  const uint16_t* lo = p.bounds + id * p.bounds_stride_page + kvh * p.bounds_stride_head + lane * V;
-  float l[V], h[V];
-  bool odd = false;
+  const uint16_t* src = p.bounds + id * p.bounds_stride_page + kvh * p.bounds_stride_head + 8 * sub;
+  uint4 lo[D / 64], hi[D / 64];
+  uint32_t big = 0u;
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    l[e] = bf16_to_f32(lo[e]);
-    h[e] = bf16_to_f32(lo[D + e]);
-    odd |= !(fabsf(l[e]) <= FLT_MAX) || !(fabsf(h[e]) <= FLT_MAX);
+  for (int i = 0; i < D / 64; ++i) {
+    lo[i] = *reinterpret_cast<const uint4*>(src + 64 * i);
+    hi[i] = *reinterpret_cast<const uint4*>(src + D + 64 * i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      big = absmax_bf16x2(absmax_bf16x2(big, (&lo[i].x)[e]), (&hi[i].x)[e]);
   }
-  if (__any_sync(0xffffffffu, odd)) return INFINITY;
+  big = absmax_bf16x2(big, big >> 16) & 0x7fffu;
+  if (__any_sync(0xffffffffu, big > 0x7f7fu)) return INFINITY;   // an infinity or NaN
   double best = -INFINITY;
-  for (int j0 = 0; j0 < p.group; j0 += 4) {
-    double sum[4];
+  for (int j = slot; j - slot < p.group; j += 4) {
+    const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +   // (heads beyond the group repeat its last)
+                        static_cast<int64_t>(kvh * p.group + min(j, p.group - 1)) * p.q_stride_head + 8 * sub;
+    float s = 0.f, t = 0.f, u = 0.f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {                    // (heads beyond the group repeat its last one)
-      const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
-                          static_cast<int64_t>(kvh * p.group + min(j0 + u, p.group - 1)) * p.q_stride_head + lane * V;
-      sum[u] = 0.0;
+    for (int i = 0; i < D / 64; ++i) {
+      const uint4 qv = *reinterpret_cast<const uint4*>(q + 64 * i);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float x = bf16_to_f32(q[e]);
-        sum[u] += static_cast<double>(x) * static_cast<double>(x < 0.f ? l[e] : h[e]);
+      for (int e = 0; e < 8; ++e) {
+        const int shift = (e & 1) * 16;
+        const float x = bf16_to_f32(static_cast<uint16_t>((&qv.x)[e >> 1] >> shift));
+        const uint32_t w = x < 0.f ? (&lo[i].x)[e >> 1] : (&hi[i].x)[e >> 1];
+        float err;
+        two_sum(s, __fmul_rn(x * sq, bf16_to_f32(static_cast<uint16_t>(w >> shift)) * sa), err);
+        two_sum(t, err, err);
+        u += err;
       }
     }
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1)
-#pragma unroll
-      for (int u = 0; u < 4; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], k);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) best = fmax(best, fabs(sum[u]) <= DBL_MAX ? sum[u] : INFINITY);
+    for (int k = 4; k > 0; k >>= 1) {
+      const float s2 = __shfl_xor_sync(0xffffffffu, s, k), t2 = __shfl_xor_sync(0xffffffffu, t, k);
+      const float u2 = __shfl_xor_sync(0xffffffffu, u, k);
+      float e1, e2;
+      two_sum(s, s2, e1);
+      two_sum(t, t2, e2);
+      u += u2 + e2;
+      two_sum(t, e1, e1);
+      u += e1;
+    }
+    best = fmax(best, static_cast<double>(s) + (static_cast<double>(t) + static_cast<double>(u)));
   }
-  return best;
+  best = fmax(best, __shfl_xor_sync(0xffffffffu, best, 8));
+  return fmax(best, __shfl_xor_sync(0xffffffffu, best, 16));
 }
 
 // One CTA = one (query row, kv head); a thread keeps kPer of the row's scores in
 // registers (rows of more than kPer T pages read them again).  The K-th largest
 // is located by one histogram over kBins equal steps between the smallest and
-// the largest score: its step's two edges take the place of t, so a page is in
-// above the upper edge + 2 eps and out below the lower edge - 2 eps.  What is
-// chosen and what is open is kept as bit maps in shared memory, and the chosen
-// pages are written in ascending order at the end.
+// the largest score, and ranked among the few of its step; of a crowded step the
+// two edges take the place of t: in above the upper edge + 2 eps, out below the
+// lower edge - 2 eps.  What is chosen and what is open is kept as bit maps in
+// shared memory, and the chosen pages are written in ascending order at the end.
 template <int D, int T>
 __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
   constexpr int W = T / 32;
+  constexpr int kPer = Sel<T>::kPer, kBins = Sel<T>::kBins, kListCap = Sel<T>::kListCap;
   extern __shared__ uint32_t bits[];                 // chosen, then open
-  __shared__ SelShared s;
+  __shared__ SelShared<T> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int row = p.row0 + blockIdx.x;
   const int kvh = blockIdx.y;
@@ -454,6 +525,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
 
   float above = INFINITY, below = INFINITY;
   bool all_open = false, ties = true;                // ties: what is open is exactly equal
+  float sq = 1.f, sa = 1.f;                          // 1 / |q|_1 and 1 / A, as powers of two
   if (want > 0) {
     float v[4] = {-INFINITY, -INFINITY, 0.f, q1};    // largest and -smallest finite score, A, |q|_1
     uint32_t infs = 0;
@@ -474,6 +546,8 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
     // the normal range may be flushed: 2 D times the smallest normal covers them.
     // A q that is not finite gives every page +infinity, a zero one zero: exact.
     const float size = v[3] * am;
+    sq = inverse_power(v[3]);
+    sa = inverse_power(am);
     const float eps = !(v[3] <= FLT_MAX) || v[3] == 0.f || am == 0.f ? 0.f
                       : size <= FLT_MAX ? 1.01f * (D * 0x1p-22f) * size + 2 * D * FLT_MIN : INFINITY;
     all_open = !(eps <= FLT_MAX);
@@ -492,10 +566,26 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
         });
         __syncthreads();
         find_bin<T>(s, kBins, want - infs);
-        // the step's edges, with room for the roundings of bin() and of this
-        const float width = 2.f * (half / kBins), slop = 0x1p-20f * (fabsf(top) + fabsf(low));
-        t_lo = fmaxf(low, low + s.digit * width - slop);
-        t_hi = fminf(top, low + (s.digit + 1) * width + slop);
+        const int digit = s.digit;
+        const uint32_t in_bin = s.hist[digit], left = s.left;
+        if (in_bin <= 32) {                          // the K-th itself: rank the step's few
+          each([&](int i, float x) {
+            if (fabsf(x) <= FLT_MAX && bin(x) == digit) s.index[atomicAdd(&s.infs, 1u) - infs] = __float_as_int(x);
+          });
+          __syncthreads();
+          const float x = lane < static_cast<int>(in_bin) ? __int_as_float(s.index[lane]) : -INFINITY;
+          uint32_t larger = 0;
+          for (uint32_t j = 0; j < in_bin; ++j) {
+            const float y = __shfl_sync(0xffffffffu, x, j);
+            larger += y > x || (y == x && static_cast<int>(j) < lane);
+          }
+          t_lo = t_hi = __shfl_sync(0xffffffffu, x, __ffs(__ballot_sync(0xffffffffu, larger == left - 1)) - 1);
+          __syncthreads();                           // (the list is used again)
+        } else {                                     // the step's edges, with room for the roundings of bin() and of this
+          const float width = 2.f * (half / kBins), slop = 0x1p-20f * (fabsf(top) + fabsf(low));
+          t_lo = fmaxf(low, low + digit * width - slop);
+          t_hi = fminf(top, low + (digit + 1) * width + slop);
+        }
       }
       above = __fadd_ru(t_hi, 2.f * eps);
       below = __fadd_rd(t_lo, -2.f * eps);
@@ -530,7 +620,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
     if (n_open <= kListCap) {
       // rank them by their exact scores
       for (uint32_t i = warp; i < n_open; i += W) {
-        const double v = exact_score<D>(p, bt, row, kvh, s.index[i]);
+        const double v = exact_score<D>(p, bt, row, kvh, s.index[i], sq, sa);
         if (lane == 0) s.value[i] = v;
       }
       __syncthreads();
@@ -550,7 +640,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
         for (int w = warp; w < words; w += W)
           for (uint32_t m = open[w]; m != 0; m &= m - 1) {
             const int i = w * 32 + __ffs(m) - 1;
-            const uint64_t k = key64(exact_score<D>(p, bt, row, kvh, i));
+            const uint64_t k = key64(exact_score<D>(p, bt, row, kvh, i, sq, sa));
             if (lane == 0) keys[i] = static_cast<uint32_t>(half == 0 ? k >> 32 : k);
           }
         __syncthreads();
@@ -612,21 +702,33 @@ cudaError_t launch_select(const SelectParams& p, bool scored, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, select_kernel<D, T>, p);
 }
 
+// Shared memory of a score CTA of `rows` rows.
+int score_smem(const SelectParams& p, int D, int rows) {
+  const int tpt = 8 / p.hpt;
+  return (rows + tpt - 1) / tpt * ((p.group + p.hpt - 1) / p.hpt) * 8 * (4 * D + 64);
+}
+
+template <int D, bool ONE>
+cudaError_t launch_score(const SelectParams& p, int chunks, cudaStream_t st) {
+  const int smem = ONE ? 0 : score_smem(p, D, p.block_rows);
+  const cudaError_t e = cudaFuncSetAttribute(score_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows * p.num_kv_heads, chunks);
+  score_kernel<D, ONE><<<grid, kScoreThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
-  const int tiles = (p.block_rows * p.cols + 7) / 8;
-  const int smem = tiles * 8 * (4 * D + 64);
-  cudaError_t e = cudaFuncSetAttribute(score_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   if (chunks > 0) {
-    const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows, p.num_kv_heads, chunks);
-    score_kernel<D><<<grid, kScoreThreads, smem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const cudaError_t e = p.block_rows == 1 && p.group <= 8 ? launch_score<D, true>(p, chunks, st)
+                                                            : launch_score<D, false>(p, chunks, st);
+    if (e != cudaSuccess) return e;
   }
   // threads per row: so many that the longest row's scores stay in registers
-  if (p.row_pages <= 128 * kPer) return launch_select<D, 128>(p, chunks > 0, st);
-  if (p.row_pages <= 256 * kPer) return launch_select<D, 256>(p, chunks > 0, st);
-  if (p.row_pages <= 512 * kPer) return launch_select<D, 512>(p, chunks > 0, st);
+  if (p.row_pages <= 128 * Sel<128>::kPer) return launch_select<D, 128>(p, chunks > 0, st);
+  if (p.row_pages <= 256 * Sel<256>::kPer) return launch_select<D, 256>(p, chunks > 0, st);
+  if (p.row_pages <= 512 * Sel<512>::kPer) return launch_select<D, 512>(p, chunks > 0, st);
   return launch_select<D, 1024>(p, chunks > 0, st);
 }
 
@@ -668,8 +770,6 @@ extern "C" pa_status pa_select_pages(const pa_sparse_plan_t* plan, const void* q
   p.batch = batch;
   p.num_kv_heads = s.num_kv_heads;
   p.group = s.num_q_heads / s.num_kv_heads;
-  // columns per token: the group rounded up to a divisor or a multiple of 8
-  p.cols = p.group > 8 ? (p.group + 7) / 8 * 8 : p.group > 4 ? 8 : p.group > 2 ? 4 : p.group;
   p.ps_log2 = __builtin_ctz(static_cast<unsigned>(s.page_size));
   p.max_len = static_cast<int64_t>(s.max_pages_per_seq) * s.page_size;
   p.top = s.top_pages;
@@ -680,18 +780,35 @@ extern "C" pa_status pa_select_pages(const pa_sparse_plan_t* plan, const void* q
   p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + kScratchHeaderBytes);
   p.err = static_cast<uint32_t*>(scratch);
   // rows per score CTA: one for decode; for chunks as many as a request brings on
-  // average, up to 64 columns
-  int block = 1;
+  // average, as far as their factors take 48 KB of shared memory
+  auto heads_per_tile = [&](int rows) {
+    int h = 8;
+    while (h > 1 && (h / 2 >= p.group || 8 / h < rows)) h /= 2;
+    return h;
+  };
+  p.block_rows = 1;
+  p.hpt = heads_per_tile(1);
   if (query_start_loc != nullptr) {
     const int each = (total_q + batch - 1) / batch;
-    while (block < each && block * 2 * p.cols <= 64) block *= 2;
+    while (p.block_rows < each) {
+      SelectParams next = p;
+      next.block_rows *= 2;
+      next.hpt = heads_per_tile(next.block_rows);
+      if (next.block_rows > kScoreThreads || score_smem(next, s.head_dim, next.block_rows) > 48 * 1024) break;
+      p = next;
+    }
   }
-  p.block_rows = block;
-  // pages per score CTA: as many as leave about eight CTAs per SM
-  const int64_t blocks = static_cast<int64_t>((std::min(total_q, plan->score_rows) + block - 1) / block);
+  // Pages per score CTA: one wave of the four CTAs an SM holds while that leaves
+  // at most 256 pages each (contexts differ in length: shorter chunks balance);
+  // blocks of several rows, whose CTAs also stage queries, two waves of at most
+  // 512.  Measured: one 131071-token context 64 pages 23.3 us, 128 pages 21.8;
+  // 64 requests of 4 to 32 K tokens 128 / 256 / 512 pages 70.2 / 69.0 / 75.8 us;
+  // 400 rows of 4 requests 64 / 128 / 256 pages 42.1 / 37.7 / 41.6 us.
+  const int64_t blocks = (std::min(total_q, plan->score_rows) + p.block_rows - 1) / p.block_rows;
   const int64_t pages_all = blocks * s.num_kv_heads * p.row_pages;
-  int64_t chunk = kScorePagesMin;
-  while (chunk * 2 <= 1024 && pages_all / (chunk * 2) >= static_cast<int64_t>(s.num_sms) * kScoreCtas) chunk *= 2;
+  const int64_t slots = static_cast<int64_t>(s.num_sms) * (p.block_rows == 1 ? 4 : 8);
+  const int64_t even = (pages_all / slots + kScorePagesMin - 1) / kScorePagesMin * kScorePagesMin;
+  const int64_t chunk = std::min<int64_t>(std::max<int64_t>(even, kScorePagesMin), p.block_rows == 1 ? 256 : 512);
   p.chunk_pages = static_cast<int>(chunk);
   // a capacity of no more than top_pages pages needs no scores
   const int chunks = s.max_pages_per_seq <= s.top_pages || s.top_pages == s.first_pages + s.last_pages
