@@ -14,6 +14,7 @@
 // pair's two elements are therefore always in one lane and the rotation needs
 // no exchange; the norm needs log2(D / 8) shuffles.  A CTA takes one token's
 // rows: cosines and sines are read once per lane and used for all its rows.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -29,25 +30,24 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Strides are in bytes and below 2^32: an address is one 32 x 32 + 64 bit product.
 struct RopeParams {
-  const uint16_t* q;
-  int64_t q_stride_tok, q_stride_head;
-  uint16_t* q_out;
-  int64_t qo_stride_tok, qo_stride_head;
-  const uint16_t* k_new;
-  const uint16_t* v_new;
-  int64_t new_stride_tok, new_stride_head;
+  const uint8_t* q;
+  uint8_t* q_out;
+  const uint8_t* k_new;
+  const uint8_t* v_new;
+  uint32_t q_tok, q_head, qo_tok, qo_head, new_tok, new_head;
   const int32_t* positions;
   int64_t positions_stride;
   const float* cos_sin;
-  int64_t cos_sin_stride;
+  uint32_t cos_sin_row;
   const uint16_t* q_norm;
   const uint16_t* k_norm;
   float norm_eps, norm_offset;
   uint8_t* k_cache;
   uint8_t* v_cache;
-  int64_t stride_page, stride_tok, stride_head;   // bytes
-  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;   // ps_log2: -1, no power of two
+  uint32_t page_bytes, tok_bytes, head_bytes;
+  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads;   // ps_log2: -1, no power of two
   int half;              // rot_dim / 2
   int interleaved, num_axes, max_position;
   int axis_end[4];       // first pair behind each axis
@@ -56,62 +56,96 @@ struct RopeParams {
   uint32_t* err;         // optional error word
 };
 
-__device__ __forceinline__ void unpack4(uint2 w, float* x) {
-  x[0] = __uint_as_float(w.x << 16);
-  x[1] = __uint_as_float(w.x & 0xffff0000u);
-  x[2] = __uint_as_float(w.y << 16);
-  x[3] = __uint_as_float(w.y & 0xffff0000u);
+__device__ __forceinline__ uint64_t offset(uint32_t i, uint32_t stride) { return static_cast<uint64_t>(i) * stride; }
+
+// Two floats as one operand of the packed fp32 instructions: half as many issue
+// slots as single ones.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 floats(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 bf16x2_floats(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t floats_bf16x2(F2 a) {
+  const float2 f = floats(a);
+  return pack_bf16x2(f.x, f.y);
 }
 
-__device__ __forceinline__ uint32_t quant4(const float* x, float scale) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)),
-                                               __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)),
-                                               __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+__device__ __forceinline__ uint32_t quant4(F2 lo, F2 hi, float scale) {
+  const float2 a = floats(lo), b = floats(hi);
+  const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(a.x, scale), __fdiv_rn(a.y, scale)),
+                                              __NV_SATFINITE, __NV_E4M3);
+  const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(b.x, scale), __fdiv_rn(b.y, scale)),
+                                              __NV_SATFINITE, __NV_E4M3);
+  return l | (h << 16);
 }
 
-template <int D, bool FP8, int U>
-__global__ void __launch_bounds__(kThreads) append_rope_kernel(const RopeParams p) {
+// One CTA = one token.  UQ query rows and UKV key or value rows per lane group are
+// in flight at a time, their loads ahead of the token's slot and positions, and
+// those of the norm weights and the angles; longer tokens loop.
+template <int D, bool FP8, int UQ>
+__global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 8;                  // lanes per row
   constexpr int ROWS = kThreads / LPR;        // rows a CTA holds at a time
+  constexpr int UKV = D == 256 ? 2 : 1;
   const int t = blockIdx.x;
   const int lane = threadIdx.x % LPR;
   const int sub = threadIdx.x / LPR;
-  // this lane's two 4-element vectors of a row
+  // this lane's two 4-element vectors of a row, as bytes of a bf16 row
   const bool turns = 4 * lane < p.half;
   const bool apart = turns && !p.interleaved;
-  const int da = apart ? 4 * lane : 8 * lane;
-  const int db = apart ? p.half + 4 * lane : 8 * lane + 4;
+  const uint32_t da = apart ? 8 * lane : 16 * lane;
+  const uint32_t db = apart ? 2 * p.half + 8 * lane : 16 * lane + 8;
+  const int nq = p.num_q_heads, nk = p.num_kv_heads;
 
-  // U rows at a time, their loads ahead of everything else
-  const int rows = p.num_q_heads + 2 * p.num_kv_heads;
-  uint2 wa[U], wb[U];
-  auto kind_of = [&](int r) { return r < p.num_q_heads ? 0 : (r < p.num_q_heads + p.num_kv_heads ? 1 : 2); };   // q, k, v
-  auto head_of = [&](int r, int kind) { return kind == 0 ? r : r - p.num_q_heads - (kind - 1) * p.num_kv_heads; };
-  auto load = [&](int r0) {
+  const uint8_t* q_src = p.q + offset(t, p.q_tok);
+  const uint64_t new_at = offset(t, p.new_tok);
+  uint2 qa[UQ], qb[UQ], na[UKV], nb[UKV];
+  auto load_q = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * ROWS + sub;
-      wa[u] = wb[u] = make_uint2(0u, 0u);
-      if (r < rows) {
-        const int kind = kind_of(r), h = head_of(r, kind);
-        const uint16_t* src = kind == 0 ? p.q + t * p.q_stride_tok + h * p.q_stride_head
-                              : (kind == 1 ? p.k_new : p.v_new) + t * p.new_stride_tok + h * p.new_stride_head;
-        wa[u] = *reinterpret_cast<const uint2*>(src + da);
-        wb[u] = *reinterpret_cast<const uint2*>(src + db);
+    for (int u = 0; u < UQ; ++u) {
+      const int h = r0 + u * ROWS + sub;
+      if (h < nq) {
+        qa[u] = *reinterpret_cast<const uint2*>(q_src + da + offset(h, p.q_head));
+        qb[u] = *reinterpret_cast<const uint2*>(q_src + db + offset(h, p.q_head));
       }
     }
   };
-  load(0);
+  auto load_kv = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < UKV; ++u) {
+      const int r = r0 + u * ROWS + sub;
+      if (r < 2 * nk) {
+        const uint8_t* x = (r < nk ? p.k_new : p.v_new) + new_at + offset(r < nk ? r : r - nk, p.new_head);
+        na[u] = *reinterpret_cast<const uint2*>(x + da);
+        nb[u] = *reinterpret_cast<const uint2*>(x + db);
+      }
+    }
+  };
+  load_q(0);
+  load_kv(0);
 
   const int64_t slot = p.slot_mapping[t];
-  if (slot < 0) return;                       // padding token
-  const int64_t page = p.ps_log2 >= 0 ? slot >> p.ps_log2 : slot / p.page_size;
-  if (page >= p.num_pages) {                  // outside the pool: nothing written
-    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, kErrPageId);
-    return;
-  }
   int pos[4] = {0, 0, 0, 0};
   bool bad = false;
   if (p.half > 0) {
@@ -122,117 +156,143 @@ __global__ void __launch_bounds__(kThreads) append_rope_kernel(const RopeParams 
         bad |= static_cast<unsigned>(pos[a]) >= static_cast<unsigned>(p.max_position);
       }
   }
-  if (bad) {
-    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, PA_DEVICE_POSITION);
+  if (slot < 0) return;                       // padding token
+  const int64_t page = p.ps_log2 >= 0 ? slot >> p.ps_log2 : slot / p.page_size;
+  if (page >= p.num_pages || bad) {           // outside the pool or the table: nothing written
+    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, page >= p.num_pages ? kErrPageId : PA_DEVICE_POSITION);
     return;
   }
 
   // the cosines and sines of this lane's four pairs
-  float cs[4], sn[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = 1.f, sn[e] = 0.f;
+  float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turns) {
-    if (p.num_axes == 1) {
-      const float* row = p.cos_sin + pos[0] * p.cos_sin_stride + 4 * lane;
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + p.half));
-      cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-      sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+    const int pair = 4 * lane;
+    auto at = [&](int i) {
+      return i < p.axis_end[0] ? pos[0] : i < p.axis_end[1] ? pos[1] : i < p.axis_end[2] ? pos[2] : pos[3];
+    };
+    auto end = [&](int i) {
+      return i < p.axis_end[0] ? p.axis_end[0] : i < p.axis_end[1] ? p.axis_end[1]
+             : i < p.axis_end[2] ? p.axis_end[2] : p.axis_end[3];
+    };
+    const float* row = p.cos_sin + offset(at(pair), p.cos_sin_row) + pair;
+    if (end(pair) >= pair + 4) {              // all on one axis
+      cs = __ldg(reinterpret_cast<const float4*>(row));
+      sn = __ldg(reinterpret_cast<const float4*>(row + p.half));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int pair = 4 * lane + e;
-        const int ps = pair < p.axis_end[0] ? pos[0]
-                       : pair < p.axis_end[1] ? pos[1] : pair < p.axis_end[2] ? pos[2] : pos[3];
-        const float* row = p.cos_sin + ps * p.cos_sin_stride + pair;
-        cs[e] = __ldg(row);
-        sn[e] = __ldg(row + p.half);
+        row = p.cos_sin + offset(at(pair + e), p.cos_sin_row) + pair + e;
+        (&cs.x)[e] = __ldg(row);
+        (&sn.x)[e] = __ldg(row + p.half);
       }
     }
   }
 
-  const int64_t cell = page * p.stride_page + (slot - page * p.page_size) * p.stride_tok;
-  const bool norms = p.q_norm != nullptr || p.k_norm != nullptr;
-  for (int r0 = 0; r0 < rows; r0 += U * ROWS) {
-    if (r0 > 0) load(r0);
+  // norm (where the head kind has weights: x, y) and rotation of one row
+  auto turn = [&](uint2 wa, uint2 wb, bool norm, uint2 x, uint2 y, F2 (&a)[2], F2 (&b)[2]) {
+    a[0] = bf16x2_floats(wa.x), a[1] = bf16x2_floats(wa.y);
+    b[0] = bf16x2_floats(wb.x), b[1] = bf16x2_floats(wb.y);
+    if (norm) {
+      const float2 s2 = floats(fma2(a[0], a[0], fma2(a[1], a[1], fma2(b[0], b[0], b[1] * b[1]))));
+      float ss = s2.x + s2.y;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+      for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+      const float rs = rsqrtf(ss * (1.f / D) + p.norm_eps);
+      const F2 r2 = f2(rs, rs), off = f2(rs * p.norm_offset, rs * p.norm_offset);   // rs (w + offset)
+      a[0] = a[0] * fma2(r2, bf16x2_floats(x.x), off);
+      a[1] = a[1] * fma2(r2, bf16x2_floats(x.y), off);
+      b[0] = b[0] * fma2(r2, bf16x2_floats(y.x), off);
+      b[1] = b[1] * fma2(r2, bf16x2_floats(y.y), off);
+    }
+    if (!turns) return;
+    if (p.interleaved) {                      // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
+      auto one = [](F2 v, float c, float s) {
+        const float2 f = floats(v);
+        return fma2(v, f2(c, c), f2(f.y, f.x) * f2(-s, s));
+      };
+      a[0] = one(a[0], cs.x, sn.x);
+      a[1] = one(a[1], cs.y, sn.y);
+      b[0] = one(b[0], cs.z, sn.z);
+      b[1] = one(b[1], cs.w, sn.w);
+    } else {                                  // pairs (a_e, b_e)
+      const F2 c[2] = {f2(cs.x, cs.y), f2(cs.z, cs.w)}, s[2] = {f2(sn.x, sn.y), f2(sn.z, sn.w)};
+      const F2 n[2] = {f2(-sn.x, -sn.y), f2(-sn.z, -sn.w)};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const F2 v = a[i];
+        a[i] = fma2(v, c[i], b[i] * n[i]);
+        b[i] = fma2(b[i], c[i], v * s[i]);
+      }
+    }
+  };
+  auto weights = [&](const uint16_t* w, uint2& x, uint2& y) {
+    if (w == nullptr) return;
+    x = __ldg(reinterpret_cast<const uint2*>(w + da / 2));
+    y = __ldg(reinterpret_cast<const uint2*>(w + db / 2));
+  };
+  uint2 qx = make_uint2(0u, 0u), qy = qx, kx = qx, ky = qx;
+  weights(p.q_norm, qx, qy);
+  weights(p.k_norm, kx, ky);
+
+  uint8_t* q_dst = p.q_out + offset(t, p.qo_tok);
+  for (int r0 = 0; r0 < nq; r0 += UQ * ROWS) {
+    if (r0 > 0) load_q(r0);
+#pragma unroll
+    for (int u = 0; u < UQ; ++u) {
+      const int h = r0 + u * ROWS + sub;
+      if (r0 + u * ROWS >= nq) break;         // (the same for the CTA: whole warps shuffle)
+      F2 a[2], b[2];
+      turn(qa[u], qb[u], p.q_norm != nullptr, qx, qy, a, b);
+      if (h < nq) {
+        *reinterpret_cast<uint2*>(q_dst + da + offset(h, p.qo_head)) =
+            make_uint2(floats_bf16x2(a[0]), floats_bf16x2(a[1]));
+        *reinterpret_cast<uint2*>(q_dst + db + offset(h, p.qo_head)) =
+            make_uint2(floats_bf16x2(b[0]), floats_bf16x2(b[1]));
+      }
+    }
+  }
+  const uint64_t cell = offset(static_cast<uint32_t>(page), p.page_bytes) +
+                        offset(static_cast<uint32_t>(slot - page * p.page_size), p.tok_bytes);
+  for (int r0 = 0; r0 < 2 * nk; r0 += UKV * ROWS) {
+    if (r0 > 0) load_kv(r0);
+#pragma unroll
+    for (int u = 0; u < UKV; ++u) {
       const int r = r0 + u * ROWS + sub;
-      const int kind = kind_of(r), h = head_of(r, kind);
-      float a[4], b[4];
-      unpack4(wa[u], a);
-      unpack4(wb[u], b);
-      if (norms) {   // (the same for the whole CTA: every lane of the warp shuffles)
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ss += a[e] * a[e] + b[e] * b[e];
-#pragma unroll
-        for (int m = 1; m < LPR; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const uint16_t* w = kind == 0 ? p.q_norm : (kind == 1 ? p.k_norm : nullptr);
-        if (w != nullptr) {
-          const float rs = rsqrtf(ss * (1.f / D) + p.norm_eps);
-          float x[4], y[4];
-          unpack4(__ldg(reinterpret_cast<const uint2*>(w + da)), x);
-          unpack4(__ldg(reinterpret_cast<const uint2*>(w + db)), y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a[e] *= rs * (x[e] + p.norm_offset);
-            b[e] *= rs * (y[e] + p.norm_offset);
-          }
+      const bool k = r < nk;
+      F2 a[2], b[2];
+      turn(na[u], nb[u], p.k_norm != nullptr, kx, ky, a, b);
+      if (r >= 2 * nk) continue;
+      uint8_t* dst = (k ? p.k_cache : p.v_cache) + cell + offset(k ? r : r - nk, p.head_bytes);
+      if constexpr (FP8) {
+        if (!k) {                             // values go as they are
+          a[0] = bf16x2_floats(na[u].x), a[1] = bf16x2_floats(na[u].y);
+          b[0] = bf16x2_floats(nb[u].x), b[1] = bf16x2_floats(nb[u].y);
         }
-      }
-      if (r >= rows) continue;
-      if (turns && kind != 2) {
-        if (p.interleaved) {   // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float x = a[e], y = b[e];
-            a[e] = x * cs[e / 2] - a[e + 1] * sn[e / 2];
-            a[e + 1] = a[e + 1] * cs[e / 2] + x * sn[e / 2];
-            b[e] = y * cs[2 + e / 2] - b[e + 1] * sn[2 + e / 2];
-            b[e + 1] = b[e + 1] * cs[2 + e / 2] + y * sn[2 + e / 2];
-          }
-        } else {               // pairs (a_e, b_e)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = a[e];
-            a[e] = x * cs[e] - b[e] * sn[e];
-            b[e] = b[e] * cs[e] + x * sn[e];
-          }
-        }
-      }
-      if (FP8 && kind != 0) {
-        uint8_t* dst = (kind == 1 ? p.k_cache : p.v_cache) + cell + h * p.stride_head;
-        const float scale = kind == 1 ? p.k_scale : p.v_scale;
-        *reinterpret_cast<uint32_t*>(dst + da) = quant4(a, scale);
-        *reinterpret_cast<uint32_t*>(dst + db) = quant4(b, scale);
+        const float scale = k ? p.k_scale : p.v_scale;
+        *reinterpret_cast<uint32_t*>(dst + da / 2) = quant4(a[0], a[1], scale);
+        *reinterpret_cast<uint32_t*>(dst + db / 2) = quant4(b[0], b[1], scale);
       } else {
-        uint16_t* dst = kind == 0 ? p.q_out + t * p.qo_stride_tok + h * p.qo_stride_head
-                                  : reinterpret_cast<uint16_t*>((kind == 1 ? p.k_cache : p.v_cache) + cell +
-                                                                h * p.stride_head);
-        if (kind != 2) {       // (values keep their bits)
-          wa[u] = make_uint2(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]));
-          wb[u] = make_uint2(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]));
-        }
-        *reinterpret_cast<uint2*>(dst + da) = wa[u];
-        *reinterpret_cast<uint2*>(dst + db) = wb[u];
+        const uint2 wa = k ? make_uint2(floats_bf16x2(a[0]), floats_bf16x2(a[1])) : na[u];
+        const uint2 wb = k ? make_uint2(floats_bf16x2(b[0]), floats_bf16x2(b[1])) : nb[u];
+        *reinterpret_cast<uint2*>(dst + da) = wa;
+        *reinterpret_cast<uint2*>(dst + db) = wb;
       }
     }
   }
 }
 
 template <int D, bool FP8>
-cudaError_t launch_rows(const RopeParams& p, cudaStream_t st) {
-  const int passes = (p.num_q_heads + 2 * p.num_kv_heads + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
-  auto kern = passes == 1 ? append_rope_kernel<D, FP8, 1> : passes == 2 ? append_rope_kernel<D, FP8, 2>
-              : passes == 3 ? append_rope_kernel<D, FP8, 3> : append_rope_kernel<D, FP8, 4>;
-  kern<<<p.num_tokens, kThreads, 0, st>>>(p);
+cudaError_t launch_rows(const RopeParams& p, int tokens, cudaStream_t st) {
+  constexpr int kRows = kThreads / (D / 8);
+  auto kern = p.num_q_heads <= kRows ? append_rope_kernel<D, FP8, 1>
+              : p.num_q_heads <= 2 * kRows ? append_rope_kernel<D, FP8, 2> : append_rope_kernel<D, FP8, 4>;
+  kern<<<tokens, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch(const RopeParams& p, bool fp8, cudaStream_t st) {
-  return fp8 ? launch_rows<D, true>(p, st) : launch_rows<D, false>(p, st);
+cudaError_t launch(const RopeParams& p, bool fp8, int tokens, cudaStream_t st) {
+  return fp8 ? launch_rows<D, true>(p, tokens, st) : launch_rows<D, false>(p, tokens, st);
 }
 
 }  // namespace
@@ -253,7 +313,7 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
     return PA_ERR_INVALID_ARG;
   if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return PA_ERR_UNSUPPORTED;
-  if (static_cast<int64_t>(num_q_heads) + 2 * static_cast<int64_t>(num_kv_heads) > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_q_heads) + 2 * static_cast<int64_t>(num_kv_heads) > (1 << 16)) return PA_ERR_UNSUPPORTED;
   const bool fp8 = kv_dtype == PA_KV_FP8_E4M3;
   if (fp8 && !(k_scale > 0.f && v_scale > 0.f)) return PA_ERR_INVALID_ARG;
   if ((q != nullptr) != (q_out != nullptr) || (q != nullptr) != (num_q_heads > 0)) {
@@ -298,40 +358,48 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   if (!at(k_cache, 16) || !at(v_cache, 16) || (kv_stride_page * e) % 16 || (kv_stride_tok * e) % 16 ||
       (kv_stride_head * e) % 16)
     return PA_ERR_UNSUPPORTED;
+  // strides below 2^32 bytes (a token's and a page's own; whole arrays may be larger)
+  const int64_t widest = std::max({q ? std::max(std::max(q_stride_tok, q_stride_head),
+                                                std::max(q_out_stride_tok, q_out_stride_head)) : int64_t{0},
+                                   new_stride_tok, new_stride_head});
+  if (widest > (UINT32_MAX >> 1) || std::max({kv_stride_page, kv_stride_tok, kv_stride_head}) > UINT32_MAX / e ||
+      rope->cos_sin_stride > UINT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   RopeParams p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.q_stride_tok = q_stride_tok;
-  p.q_stride_head = q_stride_head;
-  p.q_out = static_cast<uint16_t*>(q_out);
-  p.qo_stride_tok = q_out_stride_tok;
-  p.qo_stride_head = q_out_stride_head;
-  p.k_new = static_cast<const uint16_t*>(k_new);
-  p.v_new = static_cast<const uint16_t*>(v_new);
-  p.new_stride_tok = new_stride_tok;
-  p.new_stride_head = new_stride_head;
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_out = static_cast<uint8_t*>(q_out);
+  p.k_new = static_cast<const uint8_t*>(k_new);
+  p.v_new = static_cast<const uint8_t*>(v_new);
+  if (q) {
+    p.q_tok = static_cast<uint32_t>(q_stride_tok * 2);
+    p.q_head = static_cast<uint32_t>(q_stride_head * 2);
+    p.qo_tok = static_cast<uint32_t>(q_out_stride_tok * 2);
+    p.qo_head = static_cast<uint32_t>(q_out_stride_head * 2);
+  }
+  p.new_tok = static_cast<uint32_t>(new_stride_tok * 2);
+  p.new_head = static_cast<uint32_t>(new_stride_head * 2);
   p.positions = positions;
   p.positions_stride = positions_stride;
   p.cos_sin = rope->cos_sin;
-  p.cos_sin_stride = rope->cos_sin_stride;
+  p.cos_sin_row = static_cast<uint32_t>(rope->cos_sin_stride);
   p.q_norm = q ? static_cast<const uint16_t*>(rope->q_norm) : nullptr;
   p.k_norm = static_cast<const uint16_t*>(rope->k_norm);
   p.norm_eps = rope->norm_eps;
   p.norm_offset = rope->norm_offset;
   p.k_cache = static_cast<uint8_t*>(k_cache);
   p.v_cache = static_cast<uint8_t*>(v_cache);
-  p.stride_page = kv_stride_page * e;
-  p.stride_tok = kv_stride_tok * e;
-  p.stride_head = kv_stride_head * e;
+  p.page_bytes = static_cast<uint32_t>(kv_stride_page * e);
+  p.tok_bytes = static_cast<uint32_t>(kv_stride_tok * e);
+  p.head_bytes = static_cast<uint32_t>(kv_stride_head * e);
   p.num_pages = num_pages;
   p.page_size = page_size;
   p.ps_log2 = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(page_size)) : -1;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = num_kv_heads;
-  p.num_tokens = num_tokens;
   p.half = rot / 2;
   p.interleaved = rope->interleaved;
   p.num_axes = rope->num_axes;
-  p.max_position = rope->max_position;
+  p.max_position = rot > 0 ? rope->max_position : 1;
   for (int a = 0, end = 0; a < 4; ++a) {
     if (a < rope->num_axes) end += rope->num_axes == 1 ? rot / 2 : rope->sections[a];
     p.axis_end[a] = end;
@@ -341,7 +409,8 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   p.v_scale = v_scale;
   p.err = static_cast<uint32_t*>(scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, st)
-                        : head_dim == 128 ? launch<128>(p, fp8, st) : launch<256>(p, fp8, st);
+  const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, num_tokens, st)
+                        : head_dim == 128 ? launch<128>(p, fp8, num_tokens, st)
+                                          : launch<256>(p, fp8, num_tokens, st);
   return r == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
