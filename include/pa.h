@@ -313,7 +313,8 @@ typedef struct {
  *   q, q_out       device bf16 [num_tokens, num_q_heads, head_dim] with their strides, or
  *                  both NULL (num_q_heads 0: keys and values alone); q_out may be q itself
  *   k_new, v_new   device bf16 [num_tokens, num_kv_heads, head_dim], one pair of strides
- *                  (views of one projection output will do); all rows 8-byte aligned
+ *                  (views of one projection output will do); all rows 8-byte aligned, all
+ *                  strides below 2^32 bytes (the arrays may be larger)
  *   positions      device int32 [num_axes, positions_stride]: each token's position on each axis
  *                  (may be NULL when rot_dim is 0)
  *   k_cache .. slot_mapping, k_scale, v_scale, scratch   as for pa_append_kv; the slots of a

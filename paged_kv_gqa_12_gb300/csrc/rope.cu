@@ -7,13 +7,21 @@
 //   (a, b) <- (a cos - b sin, b cos + a sin)                   per rotated pair
 // and one rounding at the end, to bf16 or to e4m3(y / scale).
 //
-// Every byte is touched once (read q, k, v; write q_out and two slots), so the
-// kernel is an HBM stream.  D / 8 lanes share a row; lane j holds the four
+// Every byte is touched once (read q, k, v and the angles; write q_out and two
+// slots): the floor is HBM's.  D / 8 lanes share a row; lane j holds the four
 // pairs 4j .. 4j+3, i.e. two 4-element vectors: the two halves' when pairs lie
 // rot_dim / 2 apart, neighbours when they are interleaved or do not rotate.  A
 // pair's two elements are therefore always in one lane and the rotation needs
 // no exchange; the norm needs log2(D / 8) shuffles.  A CTA takes one token's
 // rows: cosines and sines are read once per lane and used for all its rows.
+//
+// Measured (411 MB: 16381 tokens, 32 + 2 x 8 heads of 128, norms, three axes):
+// 85 us, 4.8 TB/s, 71 % of the copy bandwidth; the same rows without rotation and
+// norm 63 us.  What is left is issue slots (547 warp instructions a token's three
+// rows per lane; packed fp32 arithmetic and 32-bit strides took 245 off) and the
+// position -> angle chain.  Slower: one persistent CTA loop with hoisted rows
+// (register spills, 120 us), the rows through a cp.async ring (141 us), 16-byte
+// vectors (spills, 134 us), rows prefetched into L2 (84 us: nothing).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -29,6 +37,10 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
+// Tokens ahead whose angles are asked for: a little more than an SM's six CTAs on
+// all SMs hold at a time (16381 tokens at random positions: none 91.9 us, 1024
+// 85.0, 1536 86.0, 3000 89.6).
+constexpr int kAhead = 1024;
 
 // Strides are in bytes and below 2^32: an address is one 32 x 32 + 64 bit product.
 struct RopeParams {
@@ -47,7 +59,7 @@ struct RopeParams {
   uint8_t* k_cache;
   uint8_t* v_cache;
   uint32_t page_bytes, tok_bytes, head_bytes;
-  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads;   // ps_log2: -1, no power of two
+  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;   // ps_log2: -1, no power of two
   int half;              // rot_dim / 2
   int interleaved, num_axes, max_position;
   int axis_end[4];       // first pair behind each axis
@@ -103,8 +115,8 @@ __device__ __forceinline__ uint32_t quant4(F2 lo, F2 hi, float scale) {
 // One CTA = one token.  UQ query rows and UKV key or value rows per lane group are
 // in flight at a time, their loads ahead of the token's slot and positions, and
 // those of the norm weights and the angles; longer tokens loop.
-template <int D, bool FP8, int UQ>
-__global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(const RopeParams p) {
+template <int D, bool FP8, bool INTERLEAVED, int UQ>
+__global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) append_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 8;                  // lanes per row
   constexpr int ROWS = kThreads / LPR;        // rows a CTA holds at a time
   constexpr int UKV = D == 256 ? 2 : 1;
@@ -113,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
   const int sub = threadIdx.x / LPR;
   // this lane's two 4-element vectors of a row, as bytes of a bf16 row
   const bool turns = 4 * lane < p.half;
-  const bool apart = turns && !p.interleaved;
+  const bool apart = turns && !INTERLEAVED;
   const uint32_t da = apart ? 8 * lane : 16 * lane;
   const uint32_t db = apart ? 2 * p.half + 8 * lane : 16 * lane + 8;
   const int nq = p.num_q_heads, nk = p.num_kv_heads;
@@ -188,6 +200,20 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
     }
   }
 
+  // A token's angles are two dependent loads away (position, then a row of the
+  // table, from HBM if no token near has been there): the first row's lanes ask L2
+  // for those of the token kAhead further on.
+  if (threadIdx.x < LPR && turns && t + kAhead < p.num_tokens && (lane & 1) == 0) {
+    const int i = 4 * lane;
+    const int a = i < p.axis_end[0] ? 0 : i < p.axis_end[1] ? 1 : i < p.axis_end[2] ? 2 : 3;
+    const int ahead = p.positions[a * p.positions_stride + t + kAhead];
+    if (static_cast<unsigned>(ahead) < static_cast<unsigned>(p.max_position)) {
+      const float* row = p.cos_sin + offset(ahead, p.cos_sin_row) + i;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + p.half));
+    }
+  }
+
   // norm (where the head kind has weights: x, y) and rotation of one row
   auto turn = [&](uint2 wa, uint2 wb, bool norm, uint2 x, uint2 y, F2 (&a)[2], F2 (&b)[2]) {
     a[0] = bf16x2_floats(wa.x), a[1] = bf16x2_floats(wa.y);
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
       b[1] = b[1] * fma2(r2, bf16x2_floats(y.y), off);
     }
     if (!turns) return;
-    if (p.interleaved) {                      // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
+    if constexpr (INTERLEAVED) {              // pairs (a0, a1), (a2, a3), (b0, b1), (b2, b3)
       auto one = [](F2 v, float c, float s) {
         const float2 f = floats(v);
         return fma2(v, f2(c, c), f2(f.y, f.x) * f2(-s, s));
@@ -230,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
     x = __ldg(reinterpret_cast<const uint2*>(w + da / 2));
     y = __ldg(reinterpret_cast<const uint2*>(w + db / 2));
   };
-  uint2 qx = make_uint2(0u, 0u), qy = qx, kx = qx, ky = qx;
-  weights(p.q_norm, qx, qy);
-  weights(p.k_norm, kx, ky);
+  uint2 x = make_uint2(0u, 0u), y = x;
+  weights(p.q_norm, x, y);
+  const int lead = (threadIdx.x & ~31) / LPR;   // first row of the warp: whole warps shuffle, and skip
 
   uint8_t* q_dst = p.q_out + offset(t, p.qo_tok);
   for (int r0 = 0; r0 < nq; r0 += UQ * ROWS) {
@@ -240,9 +266,9 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
 #pragma unroll
     for (int u = 0; u < UQ; ++u) {
       const int h = r0 + u * ROWS + sub;
-      if (r0 + u * ROWS >= nq) break;         // (the same for the CTA: whole warps shuffle)
+      if (r0 + u * ROWS + lead >= nq) break;
       F2 a[2], b[2];
-      turn(qa[u], qb[u], p.q_norm != nullptr, qx, qy, a, b);
+      turn(qa[u], qb[u], p.q_norm != nullptr, x, y, a, b);
       if (h < nq) {
         *reinterpret_cast<uint2*>(q_dst + da + offset(h, p.qo_head)) =
             make_uint2(floats_bf16x2(a[0]), floats_bf16x2(a[1]));
@@ -253,14 +279,17 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
   }
   const uint64_t cell = offset(static_cast<uint32_t>(page), p.page_bytes) +
                         offset(static_cast<uint32_t>(slot - page * p.page_size), p.tok_bytes);
+  weights(p.k_norm, x, y);
   for (int r0 = 0; r0 < 2 * nk; r0 += UKV * ROWS) {
     if (r0 > 0) load_kv(r0);
 #pragma unroll
     for (int u = 0; u < UKV; ++u) {
       const int r = r0 + u * ROWS + sub;
+      if (r0 + u * ROWS + lead >= 2 * nk) break;
       const bool k = r < nk;
       F2 a[2], b[2];
-      turn(na[u], nb[u], p.k_norm != nullptr, kx, ky, a, b);
+      // (a warp of values alone has nothing to turn)
+      if (FP8 || r0 + u * ROWS + lead < nk) turn(na[u], nb[u], p.k_norm != nullptr, x, y, a, b);
       if (r >= 2 * nk) continue;
       uint8_t* dst = (k ? p.k_cache : p.v_cache) + cell + offset(k ? r : r - nk, p.head_bytes);
       if constexpr (FP8) {
@@ -272,27 +301,32 @@ __global__ void __launch_bounds__(kThreads, UQ <= 2 ? 5 : 4) append_rope_kernel(
         *reinterpret_cast<uint32_t*>(dst + da / 2) = quant4(a[0], a[1], scale);
         *reinterpret_cast<uint32_t*>(dst + db / 2) = quant4(b[0], b[1], scale);
       } else {
-        const uint2 wa = k ? make_uint2(floats_bf16x2(a[0]), floats_bf16x2(a[1])) : na[u];
-        const uint2 wb = k ? make_uint2(floats_bf16x2(b[0]), floats_bf16x2(b[1])) : nb[u];
-        *reinterpret_cast<uint2*>(dst + da) = wa;
-        *reinterpret_cast<uint2*>(dst + db) = wb;
+        if (k) {
+          na[u] = make_uint2(floats_bf16x2(a[0]), floats_bf16x2(a[1]));
+          nb[u] = make_uint2(floats_bf16x2(b[0]), floats_bf16x2(b[1]));
+        }
+        *reinterpret_cast<uint2*>(dst + da) = na[u];
+        *reinterpret_cast<uint2*>(dst + db) = nb[u];
       }
     }
   }
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool INTERLEAVED>
 cudaError_t launch_rows(const RopeParams& p, int tokens, cudaStream_t st) {
   constexpr int kRows = kThreads / (D / 8);
-  auto kern = p.num_q_heads <= kRows ? append_rope_kernel<D, FP8, 1>
-              : p.num_q_heads <= 2 * kRows ? append_rope_kernel<D, FP8, 2> : append_rope_kernel<D, FP8, 4>;
+  auto kern = p.num_q_heads <= kRows ? append_rope_kernel<D, FP8, INTERLEAVED, 1>
+              : p.num_q_heads <= 2 * kRows ? append_rope_kernel<D, FP8, INTERLEAVED, 2>
+                                           : append_rope_kernel<D, FP8, INTERLEAVED, 4>;
   kern<<<tokens, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch(const RopeParams& p, bool fp8, int tokens, cudaStream_t st) {
-  return fp8 ? launch_rows<D, true>(p, tokens, st) : launch_rows<D, false>(p, tokens, st);
+  if (p.interleaved)
+    return fp8 ? launch_rows<D, true, true>(p, tokens, st) : launch_rows<D, false, true>(p, tokens, st);
+  return fp8 ? launch_rows<D, true, false>(p, tokens, st) : launch_rows<D, false, false>(p, tokens, st);
 }
 
 }  // namespace
@@ -404,6 +438,7 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
     if (a < rope->num_axes) end += rope->num_axes == 1 ? rot / 2 : rope->sections[a];
     p.axis_end[a] = end;
   }
+  p.num_tokens = num_tokens;
   p.slot_mapping = slot_mapping;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
