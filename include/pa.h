@@ -427,8 +427,8 @@ pa_status pa_select_pages(const pa_sparse_plan_t* plan,
 /* Attention over chosen pages: as pa_decode / pa_extend, with the keys of query
  * row r and kv head g being { j <= pos : j / page_size in pages[r][g][:] }.
  *   pages          device int32 [total_q, Hkv, K] contiguous, as pa_select_pages writes them or the
- *                  caller's own: page indices of the request in any order, each at most once,
- *                  ended by the first negative one.  Pages behind the query hold no key j <= pos
+ *                  caller's own: page indices of the request in any order, each at most once.
+ *                  Negative ones are passed over; pages behind the query hold no key j <= pos
  *                  and add nothing.  No page: out = 0, lse = the sink or -infinity.
  * Rows, positions, errors and untouched rows as for pa_select_pages; the other arguments as for
  * pa_extend.  Asynchronous on `stream`; one kernel launch. */

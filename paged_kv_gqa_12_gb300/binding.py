@@ -322,18 +322,27 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
                sections=(ctypes.c_int32 * 4)(*sec), max_position=0 if cos_sin is None else cos_sin.shape[0],
                cos_sin=_ptr(cos_sin), cos_sin_stride=0 if cos_sin is None else cos_sin.stride(0), q_norm=_ptr(q_norm),
                k_norm=_ptr(k_norm), norm_eps=float(norm_eps), norm_offset=float(norm_offset))
+    dims = {t.shape[0] for t in (q_norm, k_norm) if t is not None}
+    if len(dims) > 1:
+        raise ValueError("q_norm and k_norm must be [head_dim]")
     r.tensors = (cos_sin, q_norm, k_norm)
+    if dims:
+        r.norm_dim = dims.pop()
     return r
 
 
-# A call of a few microseconds on the GPU should not wait for its checks: they
-# take each property once and raise from _typed alone.
+# A call of a few microseconds on the GPU should not wait for its checks: each
+# function compares a tensor's type, device and strides in place and leaves what
+# does not look as usual to _typed, which decides and words the error.
+
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
 
 def _device(*tensors) -> int:
     """The current CUDA device, which the first tensor (or none) has to be on."""
     if tensors and tensors[0].get_device() < 0:
         raise ValueError("tensors must be on the current CUDA device")
-    return torch.cuda.current_device() if tensors else -1
+    return torch._C._cuda_getDevice() if tensors else -1
 
 
 def _typed(name, t, dtype, dims, dev):
@@ -352,16 +361,18 @@ def _raw_stream(stream, dev) -> int:
 
 def _pair(k_name, k, v_name, v, dtype, dims, dev):
     """Two tensors of one type, shape and strides; returns both tuples."""
-    _typed(k_name, k, dtype, dims, dev)
-    _typed(v_name, v, dtype, dims, dev)
     shape, stride = k.shape, k.stride()
-    if v.shape != shape or v.stride() != stride:
+    if k.dtype is not dtype or v.dtype is not dtype or k.get_device() != dev or v.get_device() != dev \
+            or len(stride) != dims or stride[-1] != 1:
+        _typed(k_name, k, dtype, dims, dev)
+        _typed(v_name, v, dtype, dims, dev)
+    if v.stride() != stride or v.shape != shape:
         raise ValueError(f"{k_name} and {v_name} must share shape and strides")
     return shape, stride
 
 
 def _cache_type(kv_dtype):
-    return torch.uint8 if kv_dtype == KV_FP8_E4M3 else torch.bfloat16
+    return torch.uint8 if kv_dtype == KV_FP8_E4M3 else _BF16
 
 
 def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_mapping, *, q=None, q_out=None,
@@ -369,60 +380,67 @@ def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_ma
     """pa_append_rope_kv: norm and rotate q (bf16 [T, Hq, D], into q_out) and k_new (bf16 [T, Hkv, D]), write k_new
     and v_new into the paged caches at slot_mapping (int64 [T]).  positions: int32 [T], or [axes, T]."""
     dev = _device(k_new)
-    (T, hkv, D), ns = _pair("k_new", k_new, "v_new", v_new, torch.bfloat16, 3, dev)
+    (T, hkv, D), ns = _pair("k_new", k_new, "v_new", v_new, _BF16, 3, dev)
     cs, kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _cache_type(kv_dtype), 4, dev)
-    _typed("slot_mapping", slot_mapping, torch.int64, 1, dev)
+    if slot_mapping.dtype is not _I64 or slot_mapping.get_device() != dev or slot_mapping.stride() != (1,):
+        _typed("slot_mapping", slot_mapping, _I64, 1, dev)
     if cs[2] != hkv or cs[3] != D or slot_mapping.shape[0] != T:
         raise ValueError("k_new must be [tokens, kv_heads, head_dim] of the cache, slot_mapping [tokens]")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     hq, qp, qs, op, os_ = 0, None, (0, 0), None, (0, 0)
     if q is not None:
-        _typed("q", q, torch.bfloat16, 3, dev)
-        _typed("q_out", q_out, torch.bfloat16, 3, dev)
-        shape = q.shape
+        shape, qs, os_ = q.shape, q.stride(), q_out.stride()
+        if q.dtype is not _BF16 or q_out.dtype is not _BF16 or q.get_device() != dev or q_out.get_device() != dev \
+                or len(qs) != 3 or qs[-1] != 1 or len(os_) != 3 or os_[-1] != 1:
+            _typed("q", q, _BF16, 3, dev)
+            _typed("q_out", q_out, _BF16, 3, dev)
         if q_out.shape != shape or shape[0] != T or shape[2] != D:
             raise ValueError("q and q_out must be [tokens, q_heads, head_dim]")
-        hq, qp, qs, op, os_ = shape[1], q.data_ptr(), q.stride(), q_out.data_ptr(), q_out.stride()
-    for w in getattr(r, "tensors", (None,))[1:]:
-        if w is not None and w.shape[0] != D:
-            raise ValueError("q_norm and k_norm must be [head_dim]")
+        hq, qp, op = shape[1], q.data_ptr(), q_out.data_ptr()
+    if getattr(r, "norm_dim", D) != D:
+        raise ValueError("q_norm and k_norm must be [head_dim]")
     pp, ps = None, 0
     if r.rot_dim > 0:
         if positions is None:
             raise ValueError("a rotation needs positions")
-        dims, axes = positions.dim(), r.num_axes
-        _typed("positions", positions, torch.int32, dims, dev)
-        shape = positions.shape
-        if not (dims == 2 and shape[0] == axes and shape[1] == T or dims == 1 and axes == 1 and shape[0] == T):
+        shape, stride, axes = positions.shape, positions.stride(), r.num_axes
+        if positions.dtype is not _I32 or positions.get_device() != dev or stride[-1] != 1:
+            _typed("positions", positions, _I32, len(shape), dev)
+        if shape != (axes, T) and not (axes == 1 and shape == (T,)):
             raise ValueError("positions must be [axes, tokens] ([tokens] for one axis)")
-        pp, ps = positions.data_ptr(), positions.stride(0) if dims == 2 else T
+        pp, ps = positions.data_ptr(), stride[0] if len(stride) == 2 else T
     status = load().pa_append_rope_kv(
         ctypes.byref(r), qp, qs[0], qs[1], op, os_[0], os_[1], hq, k_new.data_ptr(), v_new.data_ptr(), ns[0], ns[1], pp,
         ps, k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2], cs[0], cs[1], hkv, D, kv_dtype,
         slot_mapping.data_ptr(), T, k_scale, v_scale, None if scratch is None else scratch.data_ptr(),
         _raw_stream(stream, dev))
-    _check(status, "pa_append_rope_kv")
+    if status != PA_OK:
+        raise PaError(status, "pa_append_rope_kv")
 
 
 def _requests(block_table, seq_lens, query_start_loc, dev):
-    """Checks of the request metadata; returns the batch size."""
-    _typed("block_table", block_table, torch.int32, 2, dev)
-    _typed("seq_lens", seq_lens, torch.int32, 1, dev)
-    batch = seq_lens.shape[0]
-    if block_table.shape[0] < batch:
+    """Checks of the request metadata; returns (batch, block-table row stride and width)."""
+    batch, bts, (rows, width) = seq_lens.shape[0], block_table.stride(), block_table.shape
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or bts[-1] != 1:
+        _typed("block_table", block_table, _I32, 2, dev)
+    if seq_lens.dtype is not _I32 or seq_lens.get_device() != dev or seq_lens.stride() != (1,):
+        _typed("seq_lens", seq_lens, _I32, 1, dev)
+    if rows < batch:
         raise ValueError("block_table must have a row per request")
     if query_start_loc is not None:
-        _typed("query_start_loc", query_start_loc, torch.int32, 1, dev)
+        if query_start_loc.dtype is not _I32 or query_start_loc.get_device() != dev or query_start_loc.stride() != (1,):
+            _typed("query_start_loc", query_start_loc, _I32, 1, dev)
         if query_start_loc.shape[0] != batch + 1:
             raise ValueError("query_start_loc must be [batch + 1]")
-    return batch
+    return batch, bts[0], width
 
 
 def _bounds(bounds, pages, kv_heads, head_dim, dev):
     """Checks of a bounds tensor; returns its strides."""
-    _typed("bounds", bounds, torch.bfloat16, 4, dev)
     s = bounds.stride()
+    if bounds.dtype is not _BF16 or bounds.get_device() != dev or len(s) != 4 or s[-1] != 1:
+        _typed("bounds", bounds, _BF16, 4, dev)
     if bounds.shape != (pages, kv_heads, 2, head_dim) or s[2] != head_dim:
         raise ValueError("bounds must be [pages, kv_heads, 2, head_dim], the last two dimensions contiguous")
     return s
@@ -432,7 +450,7 @@ def _floats(name, t, n, dev):
     """Pointer of an optional fp32 [n] tensor."""
     if t is None:
         return None
-    _typed(name, t, torch.float32, 1, dev)
+    _typed(name, t, _F32, 1, dev)
     if t.shape[0] != n:
         raise ValueError(f"{name} must be [{n}]")
     return t.data_ptr()
@@ -443,17 +461,19 @@ def page_bounds(k_cache, block_table, seq_lens, bounds, *, query_start_loc=None,
     """pa_page_bounds: refresh bounds (bf16 [pages, kv_heads, 2, head_dim]: smallest, largest key value per dim) of
     the pages that hold new tokens (query_start_loc), or of every page of the requests (None)."""
     dev = _device(k_cache)
-    _typed("k_cache", k_cache, _cache_type(kv_dtype), 4, dev)
-    batch = _requests(block_table, seq_lens, query_start_loc, dev)
-    (pages, ps, hkv, D), ks = k_cache.shape, k_cache.stride()
+    ks, dtype = k_cache.stride(), _cache_type(kv_dtype)
+    if k_cache.dtype is not dtype or k_cache.get_device() != dev or len(ks) != 4 or ks[-1] != 1:
+        _typed("k_cache", k_cache, dtype, 4, dev)
+    batch, bts, width = _requests(block_table, seq_lens, query_start_loc, dev)
+    pages, ps, hkv, D = k_cache.shape
     bs = _bounds(bounds, pages, hkv, D, dev)
     status = load().pa_page_bounds(
-        k_cache.data_ptr(), ks[0], ks[1], ks[2], pages, ps, hkv, D, kv_dtype, block_table.data_ptr(),
-        block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
-        None if query_start_loc is None else query_start_loc.data_ptr(), batch, k_scale,
+        k_cache.data_ptr(), ks[0], ks[1], ks[2], pages, ps, hkv, D, kv_dtype, block_table.data_ptr(), bts, width,
+        seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(), batch, k_scale,
         _floats("k_scales", k_scales, batch, dev), bounds.data_ptr(), bs[0], bs[1],
         None if scratch is None else scratch.data_ptr(), _raw_stream(stream, dev))
-    _check(status, "pa_page_bounds")
+    if status != PA_OK:
+        raise PaError(status, "pa_page_bounds")
 
 
 def sparse_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, kv_dtype: int = KV_BF16,
@@ -471,16 +491,22 @@ def sparse_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size
 
 
 def _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev):
-    """Checks of query rows and their page lists against a plan's shape; returns (rows, batch)."""
-    _typed("q", q, torch.bfloat16, 3, dev)
-    _typed("pages", pages, torch.int32, 3, dev)
-    batch = _requests(block_table, seq_lens, query_start_loc, dev)
+    """Checks of query rows and their page lists against a plan's shape; returns (rows, q strides, batch, block-table
+    row stride)."""
+    hkv, top, qs = s.num_kv_heads, s.top_pages, q.stride()
+    if q.dtype is not _BF16 or q.get_device() != dev or len(qs) != 3 or qs[-1] != 1:
+        _typed("q", q, _BF16, 3, dev)
+    if pages.dtype is not _I32 or pages.get_device() != dev or len(pages.shape) != 3:
+        _typed("pages", pages, _I32, 3, dev)
+    batch, bts, width = _requests(block_table, seq_lens, query_start_loc, dev)
     rows, hq, D = q.shape
     if hq != s.num_q_heads or D != s.head_dim:
         raise ValueError("q must be [rows, q_heads, head_dim] of the plan")
-    if pages.shape != (rows, s.num_kv_heads, s.top_pages) or not pages.is_contiguous():
+    if pages.shape != (rows, hkv, top) or (pages.stride() != (hkv * top, top, 1) and not pages.is_contiguous()):
         raise ValueError("pages must be contiguous [rows, kv_heads, top_pages] of the plan")
-    return rows, batch
+    if width < s.max_pages_per_seq:
+        raise ValueError("block_table must be max_pages_per_seq of the plan wide")
+    return rows, qs, batch, bts
 
 
 def select_pages(p: PaSparsePlan, q, bounds, block_table, seq_lens, pages, *, query_start_loc=None, scratch,
@@ -488,15 +514,15 @@ def select_pages(p: PaSparsePlan, q, bounds, block_table, seq_lens, pages, *, qu
     """pa_select_pages: pages (int32 [rows, kv_heads, top_pages]) of each query row (bf16 q [rows, Hq, D]) by the key
     bounds page_bounds wrote.  One row per request without query_start_loc, packed rows with it."""
     dev, s = _device(q), p.shape
-    rows, batch = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
+    rows, qs, batch, bts = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
     pool = bounds.shape[0]
     bs = _bounds(bounds, pool, s.num_kv_heads, s.head_dim, dev)
-    qs = q.stride()
     status = load().pa_select_pages(
-        ctypes.byref(p), q.data_ptr(), qs[0], qs[1], bounds.data_ptr(), bs[0], bs[1], pool, block_table.data_ptr(),
-        block_table.stride(0), seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(),
-        batch, rows, pages.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
-    _check(status, "pa_select_pages")
+        ctypes.byref(p), q.data_ptr(), qs[0], qs[1], bounds.data_ptr(), bs[0], bs[1], pool, block_table.data_ptr(), bts,
+        seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows,
+        pages.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
+    if status != PA_OK:
+        raise PaError(status, "pa_select_pages")
 
 
 def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, pages, *, query_start_loc=None,
@@ -505,26 +531,30 @@ def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, p
     """pa_sparse_attend: attention of each query row over the pages chosen for it (q / out bf16 [rows, Hq, D], lse
     fp32 [rows, Hq])."""
     dev, s = _device(q), p.shape
-    rows, batch = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
+    rows, qs, batch, bts = _sparse_rows(s, q, pages, block_table, seq_lens, query_start_loc, dev)
     (pool, ps, hkv, D), kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _cache_type(s.kv_dtype), 4, dev)
     if ps != s.page_size or hkv != s.num_kv_heads or D != s.head_dim:
         raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] of the plan")
-    _typed("out", out, torch.bfloat16, 3, dev)
+    os_ = out.stride()
+    if out.dtype is not _BF16 or out.get_device() != dev or len(os_) != 3 or os_[-1] != 1:
+        _typed("out", out, _BF16, 3, dev)
     if out.shape != q.shape:
         raise ValueError("out must be [rows, q_heads, head_dim]")
     if lse is not None:
-        _typed("lse", lse, torch.float32, 2, dev)
-        if lse.shape != (rows, s.num_q_heads) or not lse.is_contiguous():
+        hq = s.num_q_heads
+        if lse.dtype is not _F32 or lse.get_device() != dev or len(lse.shape) != 2:
+            _typed("lse", lse, _F32, 2, dev)
+        if lse.shape != (rows, hq) or (lse.stride() != (hq, 1) and not lse.is_contiguous()):
             raise ValueError("lse must be contiguous [rows, q_heads]")
-    qs, os_ = q.stride(), out.stride()
     status = load().pa_sparse_attend(
         ctypes.byref(p), q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2],
-        pool, block_table.data_ptr(), block_table.stride(0), seq_lens.data_ptr(),
+        pool, block_table.data_ptr(), bts, seq_lens.data_ptr(),
         None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows, pages.data_ptr(), scale,
         _floats("sinks", sinks, s.num_q_heads, dev), k_scale, v_scale, _floats("k_scales", k_scales, batch, dev),
         _floats("v_scales", v_scales, batch, dev), out.data_ptr(), os_[0], os_[1],
         None if lse is None else lse.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
-    _check(status, "pa_sparse_attend")
+    if status != PA_OK:
+        raise PaError(status, "pa_sparse_attend")
 
 
 def debug_wait_expiry(scratch, which: int, limit_ns: int, stream=None):

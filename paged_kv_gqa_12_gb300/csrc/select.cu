@@ -711,8 +711,10 @@ int score_smem(const SelectParams& p, int D, int rows) {
 template <int D, bool ONE>
 cudaError_t launch_score(const SelectParams& p, int chunks, cudaStream_t st) {
   const int smem = ONE ? 0 : score_smem(p, D, p.block_rows);
-  const cudaError_t e = cudaFuncSetAttribute(score_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(score_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows * p.num_kv_heads, chunks);
   score_kernel<D, ONE><<<grid, kScoreThreads, smem, st>>>(p);
   return cudaGetLastError();

@@ -11,11 +11,12 @@
 //   * One CTA = one (row, split of its pages, kv head [, 16 heads of a large
 //     group]), 4 warps, each with a private ring of stages that its lane 0
 //     refills by TMA from the pages; no barrier between warps in the loop.
-//   * The chosen pages are laid side by side: key x of the row is slot x % ps
-//     of its page x / ps.  The list entry, resolved through the block table,
-//     and the number of keys of the page at or before pos (`lim`) are staged in
-//     shared memory once, so the loop is that of a dense sequence and only
-//     tiles with lim < their keys are masked.
+//   * A split takes an equal share of the list's entries, whatever they hold, so
+//     that its first loads (list, then block table) wait for nothing else.  Its
+//     pages are laid side by side: key x is slot x % ps of entry x / ps.  Each
+//     entry's pool page and the number of its keys at or before pos (`lim`) are
+//     staged in shared memory once, so the loop is that of a dense sequence and
+//     only tiles with lim < their keys are masked.
 //   * S^T = K Q^T and O^T += V^T P^T on warp-level bf16 MMAs, the group's heads
 //     as N = 8: with 8 query rows a 128-row tcgen05 tile would be 1/16 used.
 //   * Splits are merged by the CTA that finishes last (arrival counters in the
@@ -51,6 +52,7 @@ struct SparseParams {
   const int32_t* qsl;
   int batch, num_q_heads, num_kv_heads, group, ps_log2, num_pages;
   int64_t max_len;
+  int max_pages;
   const int32_t* pages;       // [rows, Hkv, top]
   int top;
   float scale_log2, cap_log2, scale_over_cap;
@@ -192,70 +194,61 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   const int g = lane >> 2, c = lane & 3;
   const int ps = 1 << p.ps_log2;
 
+  // entries [e0, e1) of the row's list are this split's; the first of each thread
+  // leaves before the row's place is known
+  const int e0 = split * p.list_cap;
+  const int entries = min(p.top - e0, p.list_cap);
+  const int32_t* list = p.pages + (static_cast<int64_t>(row) * p.num_kv_heads + kvh) * p.top + e0;
+  int entry = tid < entries ? list[tid] : -1;
+
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int s_used;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * T::WARP);
+  int32_t* ids = reinterpret_cast<int32_t*>(bars + kWarps * NS);
+  int32_t* lims = ids + p.list_cap;
+  if (tid == 0) {
+    s_used = 0;
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
+    for (int i = 0; i < kWarps * NS; ++i) mbar_init(&bars[i], 1);
+    fence_mbar_init();
+  }
   const RowPlace at = find_row<kThreads>(p.seq_lens, p.qsl, p.batch, row, p.max_len);
   if (at.b < 0) return;                                    // behind the last request
   if (at.bad) {
     if (tid == 0) atomicOr(p.err, kErrCapacity);
     return;
   }
-  // pages of the row: up to the first negative entry
-  const int32_t* list = p.pages + (static_cast<int64_t>(row) * p.num_kv_heads + kvh) * p.top;
-  __shared__ int s_end;
-  if (tid == 0) s_end = at.pos >= 0 ? p.top : 0;
-  __syncthreads();
-  if (at.pos >= 0) {
-    for (int i = tid; i < p.top; i += kThreads)
-      if (list[i] < 0) {
-        atomicMin(&s_end, i);
-        break;
-      }
-  }
-  __syncthreads();
-  const int n_pages = s_end;
-  const int n_keys = n_pages << p.ps_log2;                 // laid side by side
-  const int n_tiles = (n_keys + TS - 1) / TS;
-  if (n_tiles == 0) {
+  if (at.pos < 0) {                                        // a request without keys
     if (split == 0) write_empty(p, D, row, head0, heads);
     return;
   }
-  const int per = (n_tiles + p.splits - 1) / p.splits;     // tiles of a split
-  const int n_splits = (n_tiles + per - 1) / per;          // none empty
-  if (split >= n_splits) return;
-  const int tile0 = split * per;
-  const int tiles = min(per, n_tiles - tile0);
-  const int key_end = min((tile0 + tiles) * TS, n_keys);
-  const int e0 = (tile0 * TS) >> p.ps_log2;                // list entries [e0, e1)
-  const int e1 = (key_end + ps - 1) >> p.ps_log2;
-
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * T::WARP);
-  int32_t* ids = reinterpret_cast<int32_t*>(bars + kWarps * NS);
-  int32_t* lims = ids + p.list_cap;
-
   const int32_t* bt = p.block_table + at.b * p.bt_stride;
-  for (int i = tid; i < e1 - e0; i += kThreads) {
-    const int64_t first_key = static_cast<int64_t>(list[e0 + i]) << p.ps_log2;
-    const int64_t left = at.pos + 1 - first_key;           // keys of the page at or before pos
-    const int lim = left <= 0 ? 0 : static_cast<int>(left < ps ? left : ps);
-    int id = p.num_pages;                                  // an out-of-range box: zeros
-    if (lim > 0) {
-      id = bt[list[e0 + i]];
+  __syncthreads();                                         // s_used
+  int used = 0;
+  for (int i = tid; i < entries; i += kThreads) {
+    if (i != tid) entry = list[i];
+    int id = p.num_pages, lim = 0;                         // an out-of-range box: zeros
+    if (entry >= 0 && entry < p.max_pages) {
+      id = bt[entry];
+      const int left = at.pos + 1 - (entry << p.ps_log2);  // keys of the page at or before pos
+      lim = min(max(left, 0), ps);
       if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-        atomicOr(p.err, kErrPageId);
+        if (lim > 0) atomicOr(p.err, kErrPageId);
         id = p.num_pages;
       }
     }
     ids[i] = id;
     lims[i] = lim;
+    if (lim > 0) used = i + 1;
   }
-  if (tid == 0) {
-    prefetch_tensormap(&tmk);
-    prefetch_tensormap(&tmv);
-    for (int i = 0; i < kWarps * NS; ++i) mbar_init(&bars[i], 1);
-    fence_mbar_init();
-  }
+  used = __reduce_max_sync(0xffffffffu, used);
+  if (lane == 0 && used > 0) atomicMax(&s_used, used);
   __syncthreads();
+  // keys of the listed pages, side by side: x is slot x % ps of entry x / ps
+  const int key_end = s_used << p.ps_log2;
+  const int tiles = (key_end + TS - 1) / TS;
 
   uint8_t* ring = smem + warp * T::WARP;
   uint64_t* bar = bars + warp * NS;
@@ -264,19 +257,19 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   // Lane 0: fetch local tile k into `stage`; boxes without an attended key are
   // left out (their rows are masked).
   auto fetch = [&](int k, int stage) {
-    const int x0 = (tile0 + k) * TS;
+    const int x0 = k * TS;
     uint8_t* ks = ring + stage * T::STAGE;
     uint8_t* vs = ks + T::BYTES;
     uint32_t want = 0;
     for (int j = 0; j < TS / br; ++j) {
       const int x = x0 + j * br;
-      if (x < key_end && (x & (ps - 1)) < lims[(x >> p.ps_log2) - e0]) want |= 1u << j;
+      if (x < key_end && (x & (ps - 1)) < lims[x >> p.ps_log2]) want |= 1u << j;
     }
     mbar_arrive_expect_tx(&bar[stage], static_cast<uint32_t>(__popc(want) * br * T::ROW * 2));
     for (int j = 0; j < TS / br; ++j) {
       if (!(want >> j & 1u)) continue;
       const int x = x0 + j * br;
-      const int id = ids[(x >> p.ps_log2) - e0];
+      const int id = ids[x >> p.ps_log2];
 #pragma unroll
       for (int cc = 0; cc < T::NCC; ++cc) {
         const int dst = cc * TS * T::RB + j * br * T::RB;
@@ -334,14 +327,14 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     const uint8_t* kst = ring + stage * T::STAGE;
     const uint8_t* vst = kst + T::BYTES;
     const uint32_t ku = smem_u32(kst), vu = smem_u32(vst);
-    const int x0 = (tile0 + k) * TS;
+    const int x0 = k * TS;
     // attended keys of each 16-key group: those before `left` (a group lies in one page)
     int left[T::MT];
     bool partial = false;
 #pragma unroll
     for (int mt = 0; mt < T::MT; ++mt) {
       const int x = x0 + mt * 16;
-      left[mt] = x < key_end ? lims[(x >> p.ps_log2) - e0] - (x & (ps - 1)) : 0;
+      left[mt] = x < key_end ? lims[x >> p.ps_log2] - (x & (ps - 1)) : 0;
       partial |= left[mt] < 16;
     }
 
@@ -597,7 +590,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       den += ws[HW * D + HW + h] * f;
     }
     const int hq = head0 + h;
-    if (n_splits == 1) {
+    if (p.splits == 1) {
       float Z = den, f = 1.f, top = M0;
       if (p.sinks != nullptr) {
         const float sk = p.sinks[hq] * kLog2e;
@@ -616,7 +609,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       if (d == 0) p.lse_part[r] = (M0 + lg2(den)) * kLn2;
     }
   }
-  if (n_splits == 1) return;
+  if (p.splits == 1) return;
 
   // ---- the split that finishes last merges ---------------------------------------
   // Partials, a fence, then the arrival; whoever completes the count acquires
@@ -626,7 +619,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   if (tid == 0) {
     uint32_t* cnt = p.counters + static_cast<int64_t>(row) * gridDim.y + blockIdx.y;
     __threadfence();
-    const bool done = atomicAdd(cnt, 1u) + 1 == static_cast<uint32_t>(n_splits);
+    const bool done = atomicAdd(cnt, 1u) + 1 == static_cast<uint32_t>(p.splits);
     if (done) {
       atomicExch(cnt, 0u);
       __threadfence();
@@ -634,7 +627,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     *last = done;
   }
   __syncthreads();
-  if (*last) merge<D>(p, n_splits, row, head0, heads);
+  if (*last) merge<D>(p, p.splits, row, head0, heads);
 }
 
 template <int D, bool FP8>
@@ -671,14 +664,8 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const SparseP
 
 int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// List entries a split of `splits` can need: its share of the tiles, and one
-// page more at either end.
-int list_entries(const pa_sparse_shape& s, int splits) {
-  const int ts = variant(s.head_dim, s.kv_dtype == PA_KV_FP8_E4M3).tile_tokens;
-  const int64_t tiles = (static_cast<int64_t>(s.top_pages) * s.page_size + ts - 1) / ts;
-  const int64_t per = (tiles + splits - 1) / splits;
-  return static_cast<int>(std::min<int64_t>(s.top_pages, per * ts / s.page_size + 2));
-}
+// List entries of a split.
+int list_entries(const pa_sparse_shape& s, int splits) { return (s.top_pages + splits - 1) / splits; }
 
 }  // namespace
 
@@ -708,16 +695,14 @@ pa_status validate_sparse(const pa_sparse_shape& s) {
 int sparse_splits(const pa_sparse_shape& s, int64_t rows) {
   const int64_t pairs = rows * s.num_kv_heads * sparse_head_groups(s);
   if (pairs <= 0 || pairs > kMergeCounters) return 1;
-  const Variant v = variant(s.head_dim, s.kv_dtype == PA_KV_FP8_E4M3);
   const int64_t keys = static_cast<int64_t>(s.top_pages) * s.page_size;
-  const int64_t tiles = (keys + v.tile_tokens - 1) / v.tile_tokens;
-  if (s.num_splits > 0) return static_cast<int>(std::min<int64_t>(s.num_splits, tiles));
+  if (s.num_splits > 0) return std::min(s.num_splits, s.top_pages);
   const int64_t slots = static_cast<int64_t>(s.num_sms) * 2;
   const bool wave = pairs >= slots;
   const int64_t target = slots * (wave ? 8 : 4);
   const int64_t least = wave ? 1024 : 128;
   const int64_t n = std::min((target + pairs - 1) / pairs, keys / least);
-  return static_cast<int>(std::max<int64_t>(1, std::min(n, tiles)));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, s.top_pages)));
 }
 
 int64_t sparse_partial_bytes(const pa_sparse_shape& s, int64_t partial_rows) {
@@ -855,6 +840,7 @@ extern "C" pa_status pa_sparse_attend(const pa_sparse_plan_t* plan, const void* 
   p.ps_log2 = __builtin_ctz(static_cast<unsigned>(s.page_size));
   p.num_pages = num_pages;
   p.max_len = static_cast<int64_t>(s.max_pages_per_seq) * s.page_size;
+  p.max_pages = s.max_pages_per_seq;
   p.pages = pages;
   p.top = s.top_pages;
   p.scale_log2 = scale * kLog2e;

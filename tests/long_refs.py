@@ -105,7 +105,7 @@ def attend(q, k_cache, v_cache, block_table, seq_lens, pages, *, page_size, scal
             ks, vs = [], []
             for page in pages[row, h].tolist():
                 if page < 0:
-                    break
+                    continue
                 there = min(page_size, pos + 1 - page * page_size)
                 if there <= 0:
                     continue

@@ -128,7 +128,7 @@ def test_rows_without_pages(pb):
         check(p, d, run(pb, p, d, num_splits=4))
 
 
-def test_list_ends_at_the_first_negative_entry(pb):
+def test_negative_entries_are_passed_over(pb):
     p, d = make([300, 400], 8, 2, 128, 16, top=10, seed=2)
     d["pages"][:, :, 4] = -1
     check(p, d, run(pb, p, d))
