@@ -70,28 +70,37 @@ struct SparseParams {
   uint32_t* err;
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NH8>
 struct Cfg;
-// Keys per stage and stages per warp, as measured for the decode kernel: small
-// bf16 stages so that three CTAs share an SM, four over e4m3 caches.
-template <> struct Cfg<64, false> { static constexpr int TS = 16, NS = 4; };
-template <> struct Cfg<128, false> { static constexpr int TS = 16, NS = 2; };
-template <> struct Cfg<256, false> { static constexpr int TS = 16, NS = 3; };
-template <> struct Cfg<64, true> { static constexpr int TS = 32, NS = 3; };
-template <> struct Cfg<128, true> { static constexpr int TS = 16, NS = 3; };
-template <> struct Cfg<256, true> { static constexpr int TS = 16, NS = 3; };
+// Keys per stage and stages per warp.  The rings are small, so that many CTAs
+// share an SM and a call of a few hundred rows is one wave of them; a warp that
+// waits for its one stage is covered by the others.  Measured, 64 rows of 2048
+// keys over 8 kv heads (us; TS x NS):
+//   bf16  D 64: 16x2 62.3, 32x1 62.8, 16x1 66.9, 64x1 75.7, 16x4 86.3
+//   bf16 D 128: 16x1 86.6, 32x1 102, 16x2 108; 16 heads a kv head: 16x2 53.1, 32x1 54.6, 16x1 64.8
+//   bf16 D 256: 16x1 170, 32x1 181, 16x2 188
+//   e4m3  D 64: 64x1 51.8, 32x1 53.0, 16x2 53.1, 16x1 64.2
+//   e4m3 D 128: 16x2 75.9, 16x3 75.8, 16x1 80.4, 32x2 98.9; D 256: 32x1 137, 16x2 148, 16x1 157
+template <int NH8> struct Cfg<64, false, NH8> { static constexpr int TS = 16, NS = 2; };
+template <int NH8> struct Cfg<128, false, NH8> { static constexpr int TS = 16, NS = NH8 == 1 ? 1 : 2; };
+template <int NH8> struct Cfg<256, false, NH8> { static constexpr int TS = 16, NS = 1; };
+template <int NH8> struct Cfg<64, true, NH8> { static constexpr int TS = 64, NS = 1; };
+template <int NH8> struct Cfg<128, true, NH8> { static constexpr int TS = 16, NS = 2; };
+template <int NH8> struct Cfg<256, true, NH8> { static constexpr int TS = 32, NS = 1; };
 
-template <int D, bool FP8>
+template <int D, bool FP8, int NH8>
 struct Tile {
-  static constexpr int TS = Cfg<D, FP8>::TS;
-  static constexpr int NS = Cfg<D, FP8>::NS;
+  static constexpr int TS = Cfg<D, FP8, NH8>::TS;
+  static constexpr int NS = Cfg<D, FP8, NH8>::NS;
   static constexpr int E = FP8 ? 1 : 2;
   static constexpr int ROW = D * E;                     // bytes of a key of one head
   static constexpr int RB = ROW < 128 ? ROW : 128;      // bytes per TMA box row
   static constexpr int NCC = ROW / RB;                  // column chunks
   static constexpr int BYTES = TS * ROW;                // K (or V) of a stage
   static constexpr int STAGE = 2 * BYTES;
-  static constexpr int WARP = NS * STAGE;
+  // a warp's ring; at the end it holds the warp's state, [8 NH8][D] and two [8 NH8] floats
+  static constexpr int STATE = (8 * NH8 * (D + 2) * 4 + 1023) / 1024 * 1024;
+  static constexpr int WARP = NS * STAGE > STATE ? NS * STAGE : STATE;
   static constexpr int MT = TS / 16;
   static constexpr int KS = D / 16;
 
@@ -181,7 +190,7 @@ template <int D, bool FP8, int NH8, bool CAP>
 __global__ void __launch_bounds__(kThreads)
 sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const SparseParams p) {
-  using T = Tile<D, FP8>;
+  using T = Tile<D, FP8, NH8>;
   constexpr int TS = T::TS, NS = T::NS;
   const int row = blockIdx.x / p.splits;
   const int split = blockIdx.x - row * p.splits;
@@ -630,24 +639,32 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   if (*last) merge<D>(p, p.splits, row, head0, heads);
 }
 
-template <int D, bool FP8>
-int smem_bytes(int list_cap) {
-  using T = Tile<D, FP8>;
-  return 1024 + kWarps * T::WARP + kWarps * T::NS * 8 + list_cap * 8;
-}
-
 struct Variant {
   int tile_tokens, stages, smem0;   // smem0: without the page list
+  int ctas;                         // that share an SM (by the registers of 128 threads, and shared memory)
 };
 
-Variant variant(int D, bool fp8) {
-#define PA_V(DD, F) Variant{Tile<DD, F>::TS, Tile<DD, F>::NS, smem_bytes<DD, F>(0)}
-  switch (D) {
-    case 64: return fp8 ? PA_V(64, true) : PA_V(64, false);
-    case 128: return fp8 ? PA_V(128, true) : PA_V(128, false);
-    default: return fp8 ? PA_V(256, true) : PA_V(256, false);
+template <int D, bool FP8, int NH8, int REGS>
+Variant variant_of() {
+  using T = Tile<D, FP8, NH8>;
+  const int smem = 1024 + kWarps * T::WARP + kWarps * T::NS * 8;
+  return Variant{T::TS, T::NS, smem, std::min(65536 / (kThreads * REGS), kMaxSmem / (smem + 2048))};
+}
+
+// (the registers as the compiler reports them, rounded up to their allocation)
+Variant variant(const pa_sparse_shape& s) {
+  const bool fp8 = s.kv_dtype == PA_KV_FP8_E4M3, wide = std::min(s.num_q_heads / s.num_kv_heads, 16) > 8;
+  switch (s.head_dim) {
+    case 64:
+      return fp8 ? (wide ? variant_of<64, true, 2, 168>() : variant_of<64, true, 1, 128>())
+                 : (wide ? variant_of<64, false, 2, 128>() : variant_of<64, false, 1, 96>());
+    case 128:
+      return fp8 ? (wide ? variant_of<128, true, 2, 168>() : variant_of<128, true, 1, 128>())
+                 : (wide ? variant_of<128, false, 2, 168>() : variant_of<128, false, 1, 96>());
+    default:
+      return fp8 ? (wide ? variant_of<256, true, 2, 256>() : variant_of<256, true, 1, 256>())
+                 : (wide ? variant_of<256, false, 2, 256>() : variant_of<256, false, 1, 168>());
   }
-#undef PA_V
 }
 
 template <int D, bool FP8>
@@ -687,21 +704,22 @@ pa_status validate_sparse(const pa_sparse_shape& s) {
   return PA_OK;
 }
 
-// Splits of each row.  The counts follow the decode planner's measured ones:
-// about four CTAs per CTA slot of the machine while the (row, kv head) pairs
-// alone do not fill it, with at least 128 keys each; then at most eight, with at
-// least 1024 keys.  The arrival counters of the scratch header bound the rows
-// that may be split at all (a call beyond them has work enough).
+// Splits of each row: as many as keep the call one wave of the CTAs that the SMs
+// hold, with at least 32 keys each, and 256 beyond sixteen (whose merging costs
+// more than it gains).  Just above one wave three splits fill the second one.
+// Measured, rows of 2048 keys, 8 kv heads, head_dim 128 bf16 (us by splits): 1 row
+// 1: 35.2, 8: 10.6, 16: 8.8, 32: 10.0, 64: 12.7; 16 rows 1: 50.9, 5: 30.7, 8: 35.3;
+// 64 rows (512 pairs on 760 slots) 1: 86.6, 2: 96.5; 100 rows 1: 162, 3: 146; 128
+// rows 1: 174, 2: 170, 3: 182.  The arrival counters of the scratch header bound the
+// rows that may be split at all (a call beyond them has work enough).
 int sparse_splits(const pa_sparse_shape& s, int64_t rows) {
   const int64_t pairs = rows * s.num_kv_heads * sparse_head_groups(s);
   if (pairs <= 0 || pairs > kMergeCounters) return 1;
   const int64_t keys = static_cast<int64_t>(s.top_pages) * s.page_size;
   if (s.num_splits > 0) return std::min(s.num_splits, s.top_pages);
-  const int64_t slots = static_cast<int64_t>(s.num_sms) * 2;
-  const bool wave = pairs >= slots;
-  const int64_t target = slots * (wave ? 8 : 4);
-  const int64_t least = wave ? 1024 : 128;
-  const int64_t n = std::min((target + pairs - 1) / pairs, keys / least);
+  const int64_t slots = static_cast<int64_t>(s.num_sms) * variant(s).ctas;
+  int64_t n = std::min({slots / pairs, keys / 32, std::max<int64_t>(16, keys / 256)});
+  if (pairs > slots && 4 * pairs <= 5 * slots) n = std::min<int64_t>(3, keys / 256);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, s.top_pages)));
 }
 
@@ -754,7 +772,7 @@ extern "C" pa_status pa_sparse_plan(const pa_sparse_shape* shape, pa_sparse_plan
       return PA_ERR_CUDA;
   }
   const pa_sparse_shape& s = p.shape;
-  const Variant v = variant(s.head_dim, s.kv_dtype == PA_KV_FP8_E4M3);
+  const Variant v = variant(s);
   int64_t partial = 0;
   int fewest = 0;   // splits of the call that splits least: the longest page list of a CTA
   const int64_t split_rows =
@@ -813,7 +831,7 @@ extern "C" pa_status pa_sparse_attend(const pa_sparse_plan_t* plan, const void* 
   const int splits = sparse_splits(s, total_q);
   if (splits > 1 && static_cast<int64_t>(total_q) * splits > plan->partial_rows) return PA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(total_q) * splits > INT32_MAX) return PA_ERR_UNSUPPORTED;
-  const Variant v = variant(s.head_dim, fp8);
+  const Variant v = variant(s);
   const int cap = list_entries(s, splits);
   const int smem = v.smem0 + cap * 8;
   if (plan->tile_tokens != v.tile_tokens || smem > kMaxSmem) return PA_ERR_INVALID_ARG;
