@@ -32,7 +32,12 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 
 // Selection by T threads a row: scores kept per thread, steps of the score
 // histogram, undecided pages ranked in shared memory.
-template <int T> struct Sel { static constexpr int kPer = 8, kBins = T <= 256 ? 4 * T : 2048, kListCap = 2 * T < 512 ? 2 * T : 512; };
+template <int T>
+struct Sel {
+  static constexpr int kPer = T == 1024 ? 8 : 16;
+  static constexpr int kBins = T <= 64 ? 512 : T == 128 ? 1024 : 2048;
+  static constexpr int kListCap = 2 * T < 512 ? 2 * T : 512;
+};
 
 struct SelectParams {
   const uint16_t* q;
@@ -48,6 +53,7 @@ struct SelectParams {
   int64_t max_len;
   int top, first, last;
   int row0, rows;             // query rows of this pass
+  int num_sms;
   int block_rows;             // rows per score CTA
   int chunk_pages, n_chunks;  // pages per score CTA; chunk maxima per (row, kv head)
   float* scores;              // [rows of the pass, Hkv, row_pages]
@@ -314,16 +320,19 @@ __device__ __forceinline__ void block_max(float (&v)[N], SelShared<T>& s) {
   for (int i = 0; i < N; ++i)
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], k));
-  if (lane == 0)
+  if constexpr (T == 32) {
+    __syncthreads();
+  } else {
+    if (lane == 0)
 #pragma unroll
-    for (int i = 0; i < N; ++i) s.red[i][threadIdx.x >> 5] = v[i];
-  __syncthreads();
+      for (int i = 0; i < N; ++i) s.red[i][threadIdx.x >> 5] = v[i];
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = s.red[i][lane < T / 32 ? lane : 0];
+    for (int i = 0; i < N; ++i) {
+      v[i] = s.red[i][lane & (T / 32 - 1)];
 #pragma unroll
-    for (int k = T / 64; k > 0; k >>= 1) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], k));
-    v[i] = __shfl_sync(0xffffffffu, v[i], 0);
+      for (int k = T / 64; k > 0; k >>= 1) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], k));
+    }
   }
 }
 
@@ -337,13 +346,12 @@ __device__ __forceinline__ uint32_t sum_before(uint32_t v, SelShared<T>& s) {
     const uint32_t x = __shfl_up_sync(0xffffffffu, sum, m);
     if (lane >= m) sum += x;
   }
+  if constexpr (T == 32) return sum - v;
   __syncthreads();
   if (lane == 31) s.warp_sum[warp] = sum;
   __syncthreads();
-  uint32_t w = lane < warp ? s.warp_sum[lane] : 0u;
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) w += __shfl_xor_sync(0xffffffffu, w, k);
-  return w + sum - v;
+  for (int w = 0; w < warp; ++w) sum += s.warp_sum[w];
+  return sum - v;
 }
 
 // The bin of s.hist[0 .. n_bins) (n_bins a multiple of T or half of it) that
@@ -491,16 +499,20 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
   const int lo = p.first, hi = n - p.last;           // pages chosen by score: [lo, hi)
   const uint32_t want = p.top - p.first - p.last;    // (n > top, so hi - lo > want)
 
-  // the largest |q|_1 of the group's heads (before the scores are waited for)
+  // the largest |q|_1 of the group's heads (before the scores are waited for):
+  // D / 8 lanes a head
   float q1 = 0.f;
-  for (int j = warp; j < p.group; j += W) {
-    const uint16_t* q = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
-                        static_cast<int64_t>(kvh * p.group + j) * p.q_stride_head;
+  for (int j0 = 0; j0 < p.group; j0 += W * (256 / D)) {
+    const int j = min(j0 + tid / (D / 8), p.group - 1);
+    const uint4 x = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(row) * p.q_stride_tok +
+                                                    static_cast<int64_t>(kvh * p.group + j) * p.q_stride_head +
+                                                    tid % (D / 8) * 8);
     float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) sum += fabsf(bf16_to_f32(q[lane + 32 * e]));
+    for (int e = 0; e < 4; ++e)
+      sum += fabsf(__uint_as_float((&x.x)[e] << 16)) + fabsf(__uint_as_float((&x.x)[e] & 0xffff0000u));
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    for (int k = D / 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     q1 = sum <= FLT_MAX ? fmaxf(q1, sum) : INFINITY;
   }
   for (int i = tid; i < kBins; i += T) s.hist[i] = 0;
@@ -593,28 +605,29 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
   }
 
   // decide what 32 bits can
+  uint32_t n_in = 0;
   each([&](int i, float x) {
     const bool cand = want > 0 && x != -INFINITY;
     const bool sure = cand && !all_open && x > above;
     const bool maybe = cand && !sure && (all_open || x >= below);
     const uint32_t in_w = __ballot_sync(0xffffffffu, sure || (i < n && (i < lo || i >= hi)));
     const uint32_t open_w = __ballot_sync(0xffffffffu, maybe);
-    const uint32_t sure_w = __ballot_sync(0xffffffffu, sure);
-    uint32_t at_list = 0;
+    n_in += __popc(in_w);
     if (lane == 0) {
       chosen[i >> 5] = in_w;
       open[i >> 5] = open_w;
-      if (sure_w != 0) atomicAdd(&s.decided, __popc(sure_w));
-      if (open_w != 0) at_list = atomicAdd(&s.n_open, __popc(open_w));
     }
     if (open_w != 0) {                               // (the same for the warp)
+      uint32_t at_list = 0;
+      if (lane == 0) at_list = atomicAdd(&s.n_open, __popc(open_w));
       at_list = __shfl_sync(0xffffffffu, at_list, 0) + __popc(open_w & ((1u << lane) - 1u));
       if (maybe && at_list < kListCap) s.index[at_list] = i;
     }
   });
+  if (lane == 0) atomicAdd(&s.decided, n_in);
   __syncthreads();
   const uint32_t n_open = s.n_open;
-  uint32_t need = want - s.decided;                  // to take from the open ones
+  uint32_t need = p.top - s.decided;                 // to take from the open ones
 
   if (need > 0 && need < n_open && !ties) {
     if (n_open <= kListCap) {
@@ -727,10 +740,15 @@ cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
                                                             : launch_score<D, false>(p, chunks, st);
     if (e != cudaSuccess) return e;
   }
-  // threads per row: so many that the longest row's scores stay in registers
-  if (p.row_pages <= 128 * Sel<128>::kPer) return launch_select<D, 128>(p, chunks > 0, st);
-  if (p.row_pages <= 256 * Sel<256>::kPer) return launch_select<D, 256>(p, chunks > 0, st);
-  if (p.row_pages <= 512 * Sel<512>::kPer) return launch_select<D, 512>(p, chunks > 0, st);
+  // Threads per row: sixteen scores each where rows are many (the fixed work of a
+  // row is per warp), eight where they are few and the time of one row counts; at
+  // most 1024 (longer rows read their scores again).
+  const int each = static_cast<int64_t>(p.rows) * p.num_kv_heads >= 8 * p.num_sms ? 16 : 8;
+  if (p.row_pages <= 32 * each) return launch_select<D, 32>(p, chunks > 0, st);
+  if (p.row_pages <= 64 * each) return launch_select<D, 64>(p, chunks > 0, st);
+  if (p.row_pages <= 128 * each) return launch_select<D, 128>(p, chunks > 0, st);
+  if (p.row_pages <= 256 * each) return launch_select<D, 256>(p, chunks > 0, st);
+  if (p.row_pages <= 512 * each) return launch_select<D, 512>(p, chunks > 0, st);
   return launch_select<D, 1024>(p, chunks > 0, st);
 }
 
@@ -774,6 +792,7 @@ extern "C" pa_status pa_select_pages(const pa_sparse_plan_t* plan, const void* q
   p.group = s.num_q_heads / s.num_kv_heads;
   p.ps_log2 = __builtin_ctz(static_cast<unsigned>(s.page_size));
   p.max_len = static_cast<int64_t>(s.max_pages_per_seq) * s.page_size;
+  p.num_sms = s.num_sms;
   p.top = s.top_pages;
   p.first = s.first_pages;
   p.last = s.last_pages;
