@@ -77,15 +77,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float nan_if_infinite(float s) { return fmaf(s, 0.f, s); }
 __device__ __forceinline__ float inf_if_nan(float s) { return s == s ? s : INFINITY; }
 
-// 16 bytes of bounds: read once by this kernel, neighbours soon
-__device__ __forceinline__ uint4 load_bounds(const uint16_t* src) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(src));
-  return v;
-}
-
 // Two bf16 split by sign bit into the factors of the lower and of the upper
 // bounds; a NaN of either sign spoils its own half, which is enough.
 __device__ __forceinline__ uint32_t sign_mask(uint32_t x) {   // 0xffff where a bf16 is negative
@@ -103,20 +94,161 @@ __device__ __forceinline__ uint4 positives(uint4 x) {
 }
 
 // ---- scores -------------------------------------------------------------------
-// One CTA = (kv head, page chunk, block of query rows).  A warp takes 16 pages as
-// the M rows of its MMAs, their 2 D bounds loaded straight from global memory
-// into A fragments: thread (g, c) of the fragment holds any four k-pairs of rows
-// g and g + 8 as long as B agrees, so it takes 16 contiguous bytes for two
-// k-steps, and the query factors are read the same way.
-//
-// ONE: a block of one row of at most 8 heads (decode).  The query factors stay in
-// registers, no warp waits for another, and the kernel is the stream of the
-// bounds.  Otherwise the factors of the block's rows lie in shared memory: a
-// tile of 8 columns holds `hpt` heads of 8 / hpt tokens, the group's heads run
-// over the tiles of a token group, and their maximum is taken in registers (and
-// over the hpt columns by shuffles, none for blocks of 8 tokens and more).
-template <int D, bool ONE>
-__global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(const SelectParams p) {
+// A warp takes 16 pages as the M rows of its MMAs and up to 8 query columns as N.
+// Thread (g, c) of an A fragment holds any four k-pairs of pages g and g + 8 as
+// long as B agrees, so it takes 16 contiguous bytes of bounds for two k-steps, and
+// the query factors are read the same way.
+
+// The largest magnitude of a page's bounds over the four lanes of its row (0 where
+// one is not finite: such a page has no finite score).
+__device__ __forceinline__ float row_amax(uint32_t v) {
+  v = absmax_bf16x2(v, v >> 16);
+  v = absmax_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = absmax_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  const float f = __uint_as_float((v & 0x7fffu) << 16);
+  return f <= FLT_MAX ? f : 0.f;
+}
+__device__ __forceinline__ uint32_t fold_abs(uint32_t v, const uint4& x) {
+  return absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(v, x.x), x.y), x.z), x.w);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// One query row of at most 8 heads (decode): one CTA = (row, kv head, page chunk).
+// The kernel is the stream of the bounds: a page's 4 D bytes of a kv head are one
+// bulk copy, 16 of them a stage, each warp with a ring of its own, so that an SM
+// has some 200 KB on the way and no warp waits for another.  Query column g (head
+// g, or head 0 again: the same maximum) stays in registers.
+template <int D>
+struct One {
+  static constexpr int NS = D == 64 ? 2 : 1;          // stages a warp
+  static constexpr int ROW = 4 * D + 64;              // bytes from page to page: free of bank conflicts
+  static constexpr int STAGE = 16 * ROW;
+  static constexpr int SMEM = kScoreWarps * NS * (STAGE + 8);
+};
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) score_one_kernel(const SelectParams p) {
+  using O = One<D>;
+  constexpr int NP = 2 * D / 32;              // 16-byte pieces per thread and row
+  constexpr int kStep = kScoreWarps * 16;
+  extern __shared__ __align__(16) uint8_t rings[];
+  __shared__ float s_a[kScoreWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int r = blockIdx.x / p.num_kv_heads;
+  const int kvh = blockIdx.x - r * p.num_kv_heads;
+  const int chunk0 = blockIdx.y * p.chunk_pages;
+  const int row = p.row0 + r;
+  pdl_launch_dependents();   // the selection may start up; it waits for this grid's scores
+
+  uint64_t* bar = reinterpret_cast<uint64_t*>(rings + kScoreWarps * O::NS * O::STAGE) + warp * O::NS;
+  const uint32_t ring = smem_u32(rings + warp * O::NS * O::STAGE);
+  if (lane == 0) {
+    for (int s = 0; s < O::NS; ++s) mbar_init(&bar[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const RowPlace at = find_row<kScoreThreads>(p.seq_lens, p.qsl, p.batch, row, p.max_len);
+  if (at.b < 0 || at.bad) return;             // (a bad one is reported by the selection kernel)
+  const int n = at.pos < 0 ? 0 : (at.pos >> p.ps_log2) + 1;
+  if (n <= p.top || chunk0 >= n - p.last) return;
+  const int end = min(chunk0 + p.chunk_pages, n - p.last);
+
+  // lane i < 16 copies page p0 + i; one behind the chunk's end repeats its last, one
+  // outside the pool reads page 0 and scores 0
+  const int32_t* bt = p.block_table + at.b * p.bt_stride;
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(p.bounds + kvh * p.bounds_stride_head);
+  const int64_t page_bytes = p.bounds_stride_page * 2;
+  uint32_t lost[O::NS];
+  auto page_id = [&](int p0) { return bt[min(p0 + (lane & 15), end - 1)]; };
+  auto issue = [&](int id, int s) {
+    const bool out = static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages);
+    lost[s] = __ballot_sync(0xffffffffu, out);
+    if (lost[s] != 0 && lane == 0) atomicOr(p.err, kErrPageId);
+    if (lane == 0) mbar_arrive_expect_tx(&bar[s], 16 * 4 * D);
+    __syncwarp();
+    if (lane < 16)
+      bulk_load(ring + s * O::STAGE + lane * O::ROW, base + (out ? 0 : id) * page_bytes, 4 * D, &bar[s]);
+  };
+  int p_next = chunk0 + warp * 16;            // of the next stage to fill
+  int id = page_id(p_next);
+#pragma unroll
+  for (int s = 0; s < O::NS; ++s) {
+    if (p_next < end) issue(id, s);
+    p_next += kStep;
+    id = page_id(p_next);
+  }
+
+  uint4 q[NP / 2];
+  const uint16_t* qh = p.q + static_cast<int64_t>(row) * p.q_stride_tok +
+                       static_cast<int64_t>(kvh * p.group + (g < p.group ? g : 0)) * p.q_stride_head + 8 * c;
+#pragma unroll
+  for (int i = 0; i < NP / 2; ++i) q[i] = *reinterpret_cast<const uint4*>(qh + 32 * i);
+
+  float* out_row = p.scores + (static_cast<int64_t>(r) * p.num_kv_heads + kvh) * p.row_pages;
+  float a_max = 0.f;
+  int it = 0;
+  for (int p0 = chunk0 + warp * 16; p0 < end; p0 += kStep, ++it) {
+    const int s = it % O::NS;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (it / O::NS) & 1, p.err))) break;
+    const uint8_t* src = rings + (warp * O::NS + s) * O::STAGE + g * O::ROW + 16 * c;
+    // (two independent sums: one after the other they would wait on each MMA's latency)
+    float d[2][4] = {};
+    uint32_t v0 = 0u, v1 = 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < NP / 2; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + (h * (NP / 2) + i) * 64);
+        const uint4 y = *reinterpret_cast<const uint4*>(src + 8 * O::ROW + (h * (NP / 2) + i) * 64);
+        const uint4 b = h == 0 ? negatives(q[i]) : positives(q[i]);
+        const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+        mma_bf16(d[i & 1], f0, b.x, b.y);
+        mma_bf16(d[i & 1], f1, b.z, b.w);
+        v0 = fold_abs(v0, x);
+        v1 = fold_abs(v1, y);
+      }
+    const uint32_t gone = lost[O::NS == 1 ? 0 : s];
+    __syncwarp();
+    if (p_next < end) {                       // the stage is read: refill it
+      fence_proxy_async_smem();
+      issue(id, s);
+    }
+    p_next += kStep;
+    id = page_id(p_next);
+    a_max = fmaxf(a_max, fmaxf(row_amax(v0), row_amax(v1)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // columns 2c and 2c + 1 of page g + 8 h
+      float x = max_nan(nan_if_infinite(d[0][2 * h] + d[1][2 * h]), nan_if_infinite(d[0][2 * h + 1] + d[1][2 * h + 1]));
+      x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 1));
+      x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, 2));
+      const int pg = p0 + g + 8 * h;
+      if (c == 0 && pg < end) out_row[pg] = (gone >> (g + 8 * h) & 1u) ? 0.f : inf_if_nan(x);
+    }
+  }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) a_max = fmaxf(a_max, __shfl_xor_sync(0xffffffffu, a_max, k));
+  if (lane == 0) s_a[warp] = a_max;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kScoreWarps; ++w) a_max = fmaxf(a_max, s_a[w]);
+    p.amax[(static_cast<int64_t>(r) * p.num_kv_heads + kvh) * p.n_chunks + blockIdx.y] = a_max;
+  }
+}
+
+// Blocks of query rows, or rows of more heads: one CTA = (row block, kv head, page
+// chunk).  The bounds are read through L2 by every block, so they go straight
+// from global memory into A fragments; the factors of the block's rows lie in
+// shared memory: a tile of 8 columns holds `hpt` heads of 8 / hpt tokens, the
+// group's heads run over the tiles of a token group, and their maximum is taken
+// in registers (and over the hpt columns by shuffles, none from 8 tokens on).
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_block_kernel(const SelectParams p) {
   constexpr int K2 = 2 * D;
   constexpr int NP = K2 / 32;                 // 16-byte pieces per thread and row
   constexpr int QROW = K2 * 2 + 64;           // bytes of a query column: rows 64 bytes apart in the banks
@@ -130,7 +262,7 @@ __global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(
   const int r_begin = p.row0 + block * p.block_rows;
   const int r_end = min(r_begin + p.block_rows, p.row0 + p.rows);
   const int G = p.group;
-  pdl_launch_dependents();   // the selection may start up; it waits for this grid's scores
+  pdl_launch_dependents();
 
   int row = r_begin;
   while (row < r_end) {
@@ -150,7 +282,7 @@ __global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(
                          static_cast<int64_t>(kvh * G) * p.q_stride_head;
 
     // pool pages of fragment rows g and g + 8; pages behind the chunk's end repeat
-    // its last one, a page outside the pool reads page 0 (and scores 0 below)
+    // its last one, a page outside the pool reads page 0 and scores 0
     int id[2];
     bool lost[2];
     auto page_ids = [&](int p0) {
@@ -159,30 +291,22 @@ __global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(
     };
     page_ids(chunk0 + warp * 16);
 
-    uint4 q_one[ONE ? NP / 2 : 1];
     const int tpt = 8 / p.hpt;
     const int groups = (m + tpt - 1) / tpt, head_tiles = (G + p.hpt - 1) / p.hpt;
-    if constexpr (ONE) {                      // column g is head g (or head 0 again)
-#pragma unroll
-      for (int i = 0; i < NP / 2; ++i)
-        q_one[i] = *reinterpret_cast<const uint4*>(q0 + static_cast<int64_t>(g < G ? g : 0) * p.q_stride_head +
-                                                   32 * i + 8 * c);
-    } else {
-      __syncthreads();
-      for (int i = tid; i < groups * head_tiles * 8 * (D / 8); i += kScoreThreads) {
-        const int col = i / (D / 8), d = (i % (D / 8)) * 8;
-        const int tile = col >> 3, tg = tile / head_tiles;
-        const int tok = tg * tpt + (col & 7) / p.hpt;
-        const int head = (tile - tg * head_tiles) * p.hpt + (col & (p.hpt - 1));
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (tok < m)                          // heads beyond the group repeat head 0: the same maximum
-          x = *reinterpret_cast<const uint4*>(q0 + tok * p.q_stride_tok +
-                                              static_cast<int64_t>(head < G ? head : 0) * p.q_stride_head + d);
-        *reinterpret_cast<uint4*>(qs + col * QROW + d * 2) = negatives(x);
-        *reinterpret_cast<uint4*>(qs + col * QROW + (D + d) * 2) = positives(x);
-      }
-      __syncthreads();
+    __syncthreads();
+    for (int i = tid; i < groups * head_tiles * 8 * (D / 8); i += kScoreThreads) {
+      const int col = i / (D / 8), d = (i % (D / 8)) * 8;
+      const int tile = col >> 3, tg = tile / head_tiles;
+      const int tok = tg * tpt + (col & 7) / p.hpt;
+      const int head = (tile - tg * head_tiles) * p.hpt + (col & (p.hpt - 1));
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (tok < m)                            // heads beyond the group repeat head 0: the same maximum
+        x = *reinterpret_cast<const uint4*>(q0 + tok * p.q_stride_tok +
+                                            static_cast<int64_t>(head < G ? head : 0) * p.q_stride_head + d);
+      *reinterpret_cast<uint4*>(qs + col * QROW + d * 2) = negatives(x);
+      *reinterpret_cast<uint4*>(qs + col * QROW + (D + d) * 2) = positives(x);
     }
+    __syncthreads();
 
     const int64_t out_row0 = (static_cast<int64_t>(first_row - p.row0) * p.num_kv_heads + kvh) * p.row_pages;
     const int64_t tok_stride = static_cast<int64_t>(p.num_kv_heads) * p.row_pages;
@@ -195,67 +319,40 @@ __global__ void __launch_bounds__(kScoreThreads, D == 256 ? 2 : 4) score_kernel(
         const uint16_t* src = p.bounds + (lost[h] ? 0 : id[h]) * p.bounds_stride_page +
                               kvh * p.bounds_stride_head + 8 * c;
 #pragma unroll
-        for (int i = 0; i < NP; ++i) a[h][i] = load_bounds(src + 32 * i);
+        for (int i = 0; i < NP; ++i) a[h][i] = __ldg(reinterpret_cast<const uint4*>(src + 32 * i));
       }
       if (lost[0] || lost[1]) atomicOr(p.err, kErrPageId);
       page_ids(p0 + kScoreWarps * 16);        // (of the next pages)
-      // the largest finite bound (a page with another one has no finite score)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t v = 0u;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-          v = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(v, a[h][i].x), a[h][i].y), a[h][i].z),
-                            a[h][i].w);
-        v = absmax_bf16x2(v, v >> 16);
-        v = absmax_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        v = absmax_bf16x2(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        const float f = __uint_as_float((v & 0x7fffu) << 16);
-        if (f <= FLT_MAX) a_max = fmaxf(a_max, f);
+        for (int i = 0; i < NP; ++i) v = fold_abs(v, a[h][i]);
+        a_max = fmaxf(a_max, row_amax(v));
       }
       for (int tg = 0; tg < groups; ++tg) {
-        // columns 2c, 2c + 1 of pages g (0, 1) and g + 8 (2, 3)
+        // columns 2c, 2c + 1 of pages g (0, 1) and g + 8 (2, 3); several tiles side by
+        // side: one after the other their sums would wait on each MMA's latency
         float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto take = [&](float (&d)[4]) {
+        constexpr int U = 4;
+        const uint8_t* src0 = qs + (tg * head_tiles * 8 + g) * QROW + 16 * c;
+        for (int ht = 0; ht < head_tiles; ht += U) {
+          float d[U][4] = {};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) best[e] = max_nan(best[e], nan_if_infinite(d[e]));
-        };
-        // (independent sums side by side: one after the other they would wait on
-        // each MMA's latency)
-        if constexpr (ONE) {
-          float d[2][4] = {};
+          for (int i = 0; i < NP; ++i) {
+            const uint32_t f0[4] = {a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y};
+            const uint32_t f1[4] = {a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w};
 #pragma unroll
-          for (int i = 0; i < NP / 2; ++i)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint4 b = s == 0 ? negatives(q_one[i]) : positives(q_one[i]);
-              const uint4 &x = a[0][s * (NP / 2) + i], &y = a[1][s * (NP / 2) + i];
-              const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
-              mma_bf16(d[s], f0, b.x, b.y);
-              mma_bf16(d[s], f1, b.z, b.w);
+            for (int u = 0; u < U; ++u) {     // (tiles beyond the last repeat it)
+              const uint4 b = *reinterpret_cast<const uint4*>(src0 + min(ht + u, head_tiles - 1) * 8 * QROW + 64 * i);
+              mma_bf16(d[u], f0, b.x, b.y);
+              mma_bf16(d[u], f1, b.z, b.w);
             }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) d[0][e] += d[1][e];
-          take(d[0]);
-        } else {
-          constexpr int U = 4;
-          const uint8_t* src0 = qs + (tg * head_tiles * 8 + g) * QROW + 16 * c;
-          for (int ht = 0; ht < head_tiles; ht += U) {
-            float d[U][4] = {};
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              const uint32_t f0[4] = {a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y};
-              const uint32_t f1[4] = {a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w};
-#pragma unroll
-              for (int u = 0; u < U; ++u) {   // (tiles beyond the last repeat it)
-                const uint4 b = *reinterpret_cast<const uint4*>(src0 + min(ht + u, head_tiles - 1) * 8 * QROW + 64 * i);
-                mma_bf16(d[u], f0, b.x, b.y);
-                mma_bf16(d[u], f1, b.z, b.w);
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) take(d[u]);
           }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) best[e] = max_nan(best[e], nan_if_infinite(d[u][e]));
         }
         auto store = [&](int tok, int h, float s) {
           const int pg = p0 + g + 8 * h;
@@ -721,23 +818,19 @@ int score_smem(const SelectParams& p, int D, int rows) {
   return (rows + tpt - 1) / tpt * ((p.group + p.hpt - 1) / p.hpt) * 8 * (4 * D + 64);
 }
 
-template <int D, bool ONE>
-cudaError_t launch_score(const SelectParams& p, int chunks, cudaStream_t st) {
-  const int smem = ONE ? 0 : score_smem(p, D, p.block_rows);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(score_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
-  const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows * p.num_kv_heads, chunks);
-  score_kernel<D, ONE><<<grid, kScoreThreads, smem, st>>>(p);
-  return cudaGetLastError();
-}
-
 template <int D>
 cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
   if (chunks > 0) {
-    const cudaError_t e = p.block_rows == 1 && p.group <= 8 ? launch_score<D, true>(p, chunks, st)
-                                                            : launch_score<D, false>(p, chunks, st);
+    const bool one = p.block_rows == 1 && p.group <= 8;
+    const int smem = one ? One<D>::SMEM : score_smem(p, D, p.block_rows);
+    auto kern = one ? score_one_kernel<D> : score_block_kernel<D>;
+    if (smem > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
+    const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows * p.num_kv_heads, chunks);
+    kern<<<grid, kScoreThreads, smem, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   // Threads per row: sixteen scores each where rows are many (the fixed work of a
@@ -819,12 +912,11 @@ extern "C" pa_status pa_select_pages(const pa_sparse_plan_t* plan, const void* q
       p = next;
     }
   }
-  // Pages per score CTA: one wave of the four CTAs an SM holds while that leaves
-  // at most 256 pages each (contexts differ in length: shorter chunks balance);
-  // blocks of several rows, whose CTAs also stage queries, two waves of at most
-  // 512.  Measured: one 131071-token context 64 pages 23.3 us, 128 pages 21.8;
-  // 64 requests of 4 to 32 K tokens 128 / 256 / 512 pages 70.2 / 69.0 / 75.8 us;
-  // 400 rows of 4 requests 64 / 128 / 256 pages 42.1 / 37.7 / 41.6 us.
+  // Pages per score CTA: few enough that one wave of CTAs takes them all, at most
+  // 256 (contexts differ in length: shorter chunks balance; 64 requests of 4 to 32 K
+  // tokens take 64.3 us with 128, 64.6 with 256, 64.2 with 512).  Blocks of several
+  // rows also stage queries: two waves, at most 512 (400 rows of 4 requests with 64 /
+  // 128 / 256 pages: 42.1 / 37.7 / 41.6 us).
   const int64_t blocks = (std::min(total_q, plan->score_rows) + p.block_rows - 1) / p.block_rows;
   const int64_t pages_all = blocks * s.num_kv_heads * p.row_pages;
   const int64_t slots = static_cast<int64_t>(s.num_sms) * (p.block_rows == 1 ? 4 : 8);
