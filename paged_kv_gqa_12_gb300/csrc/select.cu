@@ -15,7 +15,7 @@
 // off by at most 2^-23 of the largest partial sum; that is at most |q|_1 A, A
 // the largest bound in magnitude.  So |s - u| <= eps = D 2^-22 |q|_1 A, and against
 // the K-th largest s, t, pages above t + 2 eps are in, pages below t - 2 eps are
-// out, and only those between are summed again, in 64 bits.
+// out, and only those between are summed again, to more than 64-bit precision.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -194,7 +194,11 @@ __global__ void __launch_bounds__(kScoreThreads) score_one_kernel(const SelectPa
   int it = 0;
   for (int p0 = chunk0 + warp * 16; p0 < end; p0 += kStep, ++it) {
     const int s = it % O::NS;
-    if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (it / O::NS) & 1, p.err))) break;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bar[s], (it / O::NS) & 1, p.err))) {
+      // give up (the error word says so), but not before the other stage's copies had their time to land
+      if (O::NS > 1 && p0 + kStep < end) mbar_wait(&bar[(it + 1) % O::NS], ((it + 1) / O::NS) & 1, p.err);
+      break;
+    }
     const uint8_t* src = rings + (warp * O::NS + s) * O::STAGE + g * O::ROW + 16 * c;
     // (two independent sums: one after the other they would wait on each MMA's latency)
     float d[2][4] = {};
@@ -651,14 +655,16 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
     block_max<T>(v, s);                              // (its barrier publishes s.infs)
     infs = s.infs;
     const float top = v[0], low = -v[1], am = v[2];
-    // |q|_1 itself is summed in 32 bits: a hundredth more covers it; sums below
-    // the normal range may be flushed: 2 D times the smallest normal covers them.
+    // |q|_1 itself is summed in 32 bits: a hundredth more covers it.  Factors and
+    // sums below the normal range may be flushed: (|q|_1 + D A + 2 D) times the
+    // smallest normal covers them.  Where a sum could overflow everything is open.
     // A q that is not finite gives every page +infinity, a zero one zero: exact.
     const float size = v[3] * am;
     sq = inverse_power(v[3]);
     sa = inverse_power(am);
     const float eps = !(v[3] <= FLT_MAX) || v[3] == 0.f || am == 0.f ? 0.f
-                      : size <= FLT_MAX ? 1.01f * (D * 0x1p-22f) * size + 2 * D * FLT_MIN : INFINITY;
+                      : size <= 0.5f * FLT_MAX
+                          ? 1.01f * (D * 0x1p-22f) * size + (v[3] + D * am + 2 * D) * FLT_MIN : INFINITY;
     all_open = !(eps <= FLT_MAX);
     ties = !all_open;
     if (infs >= want && !all_open) {

@@ -140,9 +140,15 @@ def test_group_maximum(pb):
 
 
 def test_scales_of_values(pb):
-    for s in (1e-30, 1e-19, 1e19, 3e37):
+    # subnormal bounds, small and large ones, and sums beyond the 32-bit range
+    for s in (1e-39, 1e-38, 1e-30, 1e-19, 1e19, 3e37):
         d = make([500 * 16, 60 * 16], 8, 2, 64, 16, top=20, seed=8, spread=s)
         check(d, run(pb, d))
+        if s < 1:
+            d["q"] = (d["q"].double() / s * 1e-3).clamp(-1e38, 1e38).bfloat16()
+            check(d, run(pb, d))
+            d["q"] = (d["q"].double() * 1e-39).bfloat16()
+            check(d, run(pb, d))
 
 
 def test_infinities_and_nan(pb):

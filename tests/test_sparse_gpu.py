@@ -312,6 +312,42 @@ def test_other_stream(pb):
     check(p, d, run(pb, p, d, stream=torch.cuda.Stream()))
 
 
+def test_two_streams_at_a_time(pb):
+    # two calls in flight, each with its workspace: the results are those of one at a time
+    jobs = []
+    for seed in (21, 22):
+        p, d = make([3000, 2000, 50, 1700], 16, 4, 128, 16, top=48, seed=seed)
+        plan = pb.sparse_plan(num_q_heads=16, num_kv_heads=4, head_dim=128, page_size=16, max_batch=4,
+                              max_pages_per_seq=p.block_table.shape[1], max_total_q=4, top_pages=48)
+        dev = gh.upload(p)
+        bounds = torch.zeros(p.num_pages, 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+        pb.page_bounds(dev["k"], dev["bt"], dev["sl"], bounds)
+        jobs.append(dict(plan=plan, dev=dev, bounds=bounds, q=d["q"].cuda(), scratch=pb.alloc_scratch(plan),
+                         stream=torch.cuda.Stream(), scale=p.scale))
+
+    def step(j, stream):
+        pages = torch.empty(4, 4, 48, dtype=torch.int32, device="cuda")
+        out, lse = torch.empty_like(j["q"]), torch.empty(4, 16, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        d = j["dev"]
+        for _ in range(20):
+            pb.select_pages(j["plan"], j["q"], j["bounds"], d["bt"], d["sl"], pages, scratch=j["scratch"], stream=stream)
+            pb.sparse_attend(j["plan"], j["q"], d["k"], d["v"], d["bt"], d["sl"], pages, scale=j["scale"], out=out,
+                             lse=lse, scratch=j["scratch"], stream=stream)
+        return pages, out, lse
+
+    alone = []
+    for j in jobs:
+        alone.append([x.cpu() for x in step(j, None)])
+    both = [step(j, j["stream"]) for j in jobs]
+    torch.cuda.synchronize()
+    for j, a, b in zip(jobs, alone, both):
+        assert pb.check(j["scratch"]) == 0
+        for x, y in zip(a, b):
+            assert torch.equal(x, y.cpu())
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
 @pytest.mark.parametrize("chunk", [False, True])
 def test_whole_step(pb, kv, chunk):
