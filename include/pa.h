@@ -403,8 +403,8 @@ pa_status pa_sparse_plan(const pa_sparse_shape* shape, pa_sparse_plan_t* plan);
  * K - first - last with the highest score
  *   score(page) = max over the group's q heads of  sum_d max(q_d lo_d, q_d hi_d),
  * lo / hi the page's bounds: no key of the page has a larger q.k.  The order is
- * that of the exact sums (what the tensor cores leave undecided is summed again
- * in 64 bits); equal scores go to the lower page.  A head's score that is not
+ * that of sums of at least 64-bit precision (what the tensor cores leave undecided
+ * is summed again); equal scores go to the lower page.  A head's score that is not
  * finite (an infinity or NaN in q or the bounds) counts as +infinity.
  *   q              device bf16 [total_q, Hq, D], strides q_stride_tok / q_stride_head, rows 16-byte aligned
  *   bounds         as pa_page_bounds writes them (16-byte aligned)

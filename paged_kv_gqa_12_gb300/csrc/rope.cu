@@ -12,16 +12,16 @@
 // pairs 4j .. 4j+3, i.e. two 4-element vectors: the two halves' when pairs lie
 // rot_dim / 2 apart, neighbours when they are interleaved or do not rotate.  A
 // pair's two elements are therefore always in one lane and the rotation needs
-// no exchange; the norm needs log2(D / 8) shuffles.  A CTA takes one token's
-// rows: cosines and sines are read once per lane and used for all its rows.
+// no exchange; the norm needs log2(D / 8) shuffles.
 //
 // Measured (411 MB: 16381 tokens, 32 + 2 x 8 heads of 128, norms, three axes):
-// 85 us, 4.8 TB/s, 71 % of the copy bandwidth; the same rows without rotation and
-// norm 63 us.  What is left is issue slots (547 warp instructions a token's three
-// rows per lane; packed fp32 arithmetic and 32-bit strides took 245 off) and the
-// position -> angle chain.  Slower: one persistent CTA loop with hoisted rows
-// (register spills, 120 us), the rows through a cp.async ring (141 us), 16-byte
-// vectors (spills, 134 us), rows prefetched into L2 (84 us: nothing).
+// 76.5 us, 5.4 TB/s, 79 % of the copy bandwidth.  With eight warps a token 85 us:
+// half of its 547 warp instructions a lane were the token's own (slot, positions,
+// angles, 64-bit addresses); one warp a token leaves 386.  Packed fp32 arithmetic
+// and 32-bit byte strides took a third off before that (119 -> 93 us).  Slower: one
+// persistent CTA loop with hoisted rows (register spills, 120 us), the rows through a
+// cp.async ring (141 us), 16-byte vectors (spills, 101 us), rows prefetched into L2
+// (no change).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -37,9 +37,10 @@ namespace pa {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens ahead whose angles are asked for: a little more than an SM's six CTAs on
-// all SMs hold at a time (16381 tokens at random positions: none 91.9 us, 1024
-// 85.0, 1536 86.0, 3000 89.6).
+constexpr int kWarps = kThreads / 32;
+// Tokens ahead whose angles are asked for: about what the SMs hold at a time (16381
+// tokens at random positions, eight warps each: none 91.9 us, 1024 85.0, 1536 86.0,
+// 3000 89.6).
 constexpr int kAhead = 1024;
 
 // Strides are in bytes and below 2^32: an address is one 32 x 32 + 64 bit product.
@@ -59,7 +60,8 @@ struct RopeParams {
   uint8_t* k_cache;
   uint8_t* v_cache;
   uint32_t page_bytes, tok_bytes, head_bytes;
-  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;   // ps_log2: -1, no power of two
+  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;
+  int token_warps;       // warps per token: 1, 2, 4 or 8   // ps_log2: -1, no power of two
   int half;              // rot_dim / 2
   int interleaved, num_axes, max_position;
   int axis_end[4];       // first pair behind each axis
@@ -112,17 +114,23 @@ __device__ __forceinline__ uint32_t quant4(F2 lo, F2 hi, float scale) {
   return l | (h << 16);
 }
 
-// One CTA = one token.  UQ query rows and UKV key or value rows per lane group are
-// in flight at a time, their loads ahead of the token's slot and positions, and
-// those of the norm weights and the angles; longer tokens loop.
-template <int D, bool FP8, bool INTERLEAVED, int UQ>
-__global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) append_rope_kernel(const RopeParams p) {
+// A token takes `token_warps` warps (1, 2, 4 or 8 of the CTA's eight): what is worked
+// out once a token (slot, positions, angles, addresses: half the instructions when
+// eight warps each do it) is shared by more rows the fewer they are, and the rows
+// run at the same time the more they are.  kQ query rows and kKv key or value rows
+// per lane group are in flight at a time, the first ones' loads ahead of the token's
+// slot and positions.
+template <int D, bool FP8, bool INTERLEAVED>
+__global__ void __launch_bounds__(kThreads, FP8 ? 3 : 4) append_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 8;                  // lanes per row
-  constexpr int ROWS = kThreads / LPR;        // rows a CTA holds at a time
-  constexpr int UKV = D == 256 ? 2 : 1;
-  const int t = blockIdx.x;
+  constexpr int kQ = 4, kKv = 2;
+  const int warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * (kWarps / p.token_warps) + warp / p.token_warps;
+  if (t >= p.num_tokens) return;
   const int lane = threadIdx.x % LPR;
-  const int sub = threadIdx.x / LPR;
+  const int lead = (warp & (p.token_warps - 1)) * (32 / LPR);    // the warp's first row
+  const int row = lead + (threadIdx.x & 31) / LPR;               // this lane's first row
+  const int step = p.token_warps * (32 / LPR);                   // from a warp's rows to its next
   // this lane's two 4-element vectors of a row, as bytes of a bf16 row
   const bool turns = 4 * lane < p.half;
   const bool apart = turns && !INTERLEAVED;
@@ -132,11 +140,11 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
 
   const uint8_t* q_src = p.q + offset(t, p.q_tok);
   const uint64_t new_at = offset(t, p.new_tok);
-  uint2 qa[UQ], qb[UQ], na[UKV], nb[UKV];
+  uint2 qa[kQ], qb[kQ], na[kKv], nb[kKv];
   auto load_q = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < UQ; ++u) {
-      const int h = r0 + u * ROWS + sub;
+    for (int u = 0; u < kQ; ++u) {
+      const int h = r0 + u * step;
       if (h < nq) {
         qa[u] = *reinterpret_cast<const uint2*>(q_src + da + offset(h, p.q_head));
         qb[u] = *reinterpret_cast<const uint2*>(q_src + db + offset(h, p.q_head));
@@ -145,8 +153,8 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   };
   auto load_kv = [&](int r0) {
 #pragma unroll
-    for (int u = 0; u < UKV; ++u) {
-      const int r = r0 + u * ROWS + sub;
+    for (int u = 0; u < kKv; ++u) {
+      const int r = r0 + u * step;
       if (r < 2 * nk) {
         const uint8_t* x = (r < nk ? p.k_new : p.v_new) + new_at + offset(r < nk ? r : r - nk, p.new_head);
         na[u] = *reinterpret_cast<const uint2*>(x + da);
@@ -154,8 +162,8 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
       }
     }
   };
-  load_q(0);
-  load_kv(0);
+  load_q(row);
+  load_kv(row);
 
   const int64_t slot = p.slot_mapping[t];
   int pos[4] = {0, 0, 0, 0};
@@ -171,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   if (slot < 0) return;                       // padding token
   const int64_t page = p.ps_log2 >= 0 ? slot >> p.ps_log2 : slot / p.page_size;
   if (page >= p.num_pages || bad) {           // outside the pool or the table: nothing written
-    if (p.err != nullptr && threadIdx.x == 0) atomicOr(p.err, page >= p.num_pages ? kErrPageId : PA_DEVICE_POSITION);
+    if (p.err != nullptr && (threadIdx.x & 31) == 0)
+      atomicOr(p.err, page >= p.num_pages ? kErrPageId : PA_DEVICE_POSITION);
     return;
   }
 
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   // A token's angles are two dependent loads away (position, then a row of the
   // table, from HBM if no token near has been there): the first row's lanes ask L2
   // for those of the token kAhead further on.
-  if (threadIdx.x < LPR && turns && t + kAhead < p.num_tokens && (lane & 1) == 0) {
+  if (row == 0 && turns && t + kAhead < p.num_tokens && (lane & 1) == 0) {
     const int i = 4 * lane;
     const int a = i < p.axis_end[0] ? 0 : i < p.axis_end[1] ? 1 : i < p.axis_end[2] ? 2 : 3;
     const int ahead = p.positions[a * p.positions_stride + t + kAhead];
@@ -258,15 +267,14 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   };
   uint2 x = make_uint2(0u, 0u), y = x;
   weights(p.q_norm, x, y);
-  const int lead = (threadIdx.x & ~31) / LPR;   // first row of the warp: whole warps shuffle, and skip
 
   uint8_t* q_dst = p.q_out + offset(t, p.qo_tok);
-  for (int r0 = 0; r0 < nq; r0 += UQ * ROWS) {
-    if (r0 > 0) load_q(r0);
+  for (int r0 = 0; r0 + lead < nq; r0 += kQ * step) {
+    if (r0 > 0) load_q(r0 + row);
 #pragma unroll
-    for (int u = 0; u < UQ; ++u) {
-      const int h = r0 + u * ROWS + sub;
-      if (r0 + u * ROWS + lead >= nq) break;
+    for (int u = 0; u < kQ; ++u) {
+      if (r0 + u * step + lead >= nq) break;  // (the same for the warp: whole warps shuffle)
+      const int h = r0 + u * step + row;
       F2 a[2], b[2];
       turn(qa[u], qb[u], p.q_norm != nullptr, x, y, a, b);
       if (h < nq) {
@@ -280,16 +288,16 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   const uint64_t cell = offset(static_cast<uint32_t>(page), p.page_bytes) +
                         offset(static_cast<uint32_t>(slot - page * p.page_size), p.tok_bytes);
   weights(p.k_norm, x, y);
-  for (int r0 = 0; r0 < 2 * nk; r0 += UKV * ROWS) {
-    if (r0 > 0) load_kv(r0);
+  for (int r0 = 0; r0 + lead < 2 * nk; r0 += kKv * step) {
+    if (r0 > 0) load_kv(r0 + row);
 #pragma unroll
-    for (int u = 0; u < UKV; ++u) {
-      const int r = r0 + u * ROWS + sub;
-      if (r0 + u * ROWS + lead >= 2 * nk) break;
+    for (int u = 0; u < kKv; ++u) {
+      if (r0 + u * step + lead >= 2 * nk) break;
+      const int r = r0 + u * step + row;
       const bool k = r < nk;
       F2 a[2], b[2];
       // (a warp of values alone has nothing to turn)
-      if (FP8 || r0 + u * ROWS + lead < nk) turn(na[u], nb[u], p.k_norm != nullptr, x, y, a, b);
+      if (FP8 || r0 + u * step + lead < nk) turn(na[u], nb[u], p.k_norm != nullptr, x, y, a, b);
       if (r >= 2 * nk) continue;
       uint8_t* dst = (k ? p.k_cache : p.v_cache) + cell + offset(k ? r : r - nk, p.head_bytes);
       if constexpr (FP8) {
@@ -312,21 +320,13 @@ __global__ void __launch_bounds__(kThreads, FP8 || UQ > 2 || D == 256 ? 4 : 6) a
   }
 }
 
-template <int D, bool FP8, bool INTERLEAVED>
-cudaError_t launch_rows(const RopeParams& p, int tokens, cudaStream_t st) {
-  constexpr int kRows = kThreads / (D / 8);
-  auto kern = p.num_q_heads <= kRows ? append_rope_kernel<D, FP8, INTERLEAVED, 1>
-              : p.num_q_heads <= 2 * kRows ? append_rope_kernel<D, FP8, INTERLEAVED, 2>
-                                           : append_rope_kernel<D, FP8, INTERLEAVED, 4>;
-  kern<<<tokens, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
-}
-
 template <int D>
-cudaError_t launch(const RopeParams& p, bool fp8, int tokens, cudaStream_t st) {
-  if (p.interleaved)
-    return fp8 ? launch_rows<D, true, true>(p, tokens, st) : launch_rows<D, false, true>(p, tokens, st);
-  return fp8 ? launch_rows<D, true, false>(p, tokens, st) : launch_rows<D, false, false>(p, tokens, st);
+cudaError_t launch(const RopeParams& p, bool fp8, cudaStream_t st) {
+  auto kern = p.interleaved ? (fp8 ? append_rope_kernel<D, true, true> : append_rope_kernel<D, false, true>)
+                            : (fp8 ? append_rope_kernel<D, true, false> : append_rope_kernel<D, false, false>);
+  const int per_cta = kWarps / p.token_warps;
+  kern<<<(p.num_tokens + per_cta - 1) / per_cta, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -444,8 +444,15 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   p.v_scale = v_scale;
   p.err = static_cast<uint32_t*>(scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, num_tokens, st)
-                        : head_dim == 128 ? launch<128>(p, fp8, num_tokens, st)
-                                          : launch<256>(p, fp8, num_tokens, st);
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return PA_ERR_CUDA;
+  // warps per token: eight while the SMs have no more than 64 warps each to run
+  p.token_warps = kWarps;
+  while (p.token_warps > 1 && static_cast<int64_t>(num_tokens) * p.token_warps > static_cast<int64_t>(sms) * 64)
+    p.token_warps /= 2;
+  const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, st)
+                        : head_dim == 128 ? launch<128>(p, fp8, st) : launch<256>(p, fp8, st);
   return r == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

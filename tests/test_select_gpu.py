@@ -88,6 +88,19 @@ def test_packed_rows(pb, Hq, Hkv, D, ps):
     check(d, run(pb, d))
 
 
+@pytest.mark.parametrize("Hq,D", [(128, 64), (96, 256), (65, 128)])
+def test_large_groups(pb, Hq, D):
+    d = make([70 * 16, 33 * 16 + 2], Hq, 1, D, 16, top=9, seed=Hq)
+    check(d, run(pb, d))
+    d = make([70 * 16, 33 * 16 + 2], Hq, 1, D, 16, top=9, rows=[3, 5], seed=Hq)
+    check(d, run(pb, d))
+
+
+def test_many_rows(pb):
+    d = make([1300], 8, 2, 64, 16, top=6, rows=[700], seed=20)
+    check(d, run(pb, d))
+
+
 def test_long_context(pb):
     d = make([131071, 70000], 16, 2, 64, 16, top=128, last=4, seed=1)
     check(d, run(pb, d))

@@ -119,6 +119,13 @@ def test_packed_rows(pb, kv, Hq, Hkv, D, ps):
         check(p, d, run(pb, p, d, num_splits=splits))
 
 
+@pytest.mark.parametrize("Hq,D,kv", [(128, 64, "bf16"), (96, 256, "bf16"), (65, 128, "fp8_e4m3"), (33, 256, "fp8_e4m3")])
+def test_large_groups(pb, Hq, D, kv):
+    p, d = make([300, 45], Hq, 1, D, 16, top=7, kv=kv, seed=Hq, sinks=True)
+    check(p, d, run(pb, p, d))
+    check(p, d, run(pb, p, d, num_splits=3))
+
+
 def test_rows_without_pages(pb):
     for sinks in (False, True):
         p, d = make([100, 200], 8, 2, 64, 16, top=6, seed=1, sinks=sinks)
