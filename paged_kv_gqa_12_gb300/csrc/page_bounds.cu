@@ -297,7 +297,7 @@ extern "C" pa_status pa_page_bounds(const void* k_cache, int64_t kv_stride_page,
   p.bounds_stride_head = bounds_stride_head;
   p.err = static_cast<uint32_t*>(scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int ctas = sms * 4;
+  const int ctas = sms * 4;   // as many as the registers let share an SM (5 would take a second wave: 74.7 us for 62.9)
   const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, ctas, st)
                         : head_dim == 128 ? launch<128>(p, fp8, ctas, st) : launch<256>(p, fp8, ctas, st);
   return r == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -60,8 +60,8 @@ struct RopeParams {
   uint8_t* k_cache;
   uint8_t* v_cache;
   uint32_t page_bytes, tok_bytes, head_bytes;
-  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;
-  int token_warps;       // warps per token: 1, 2, 4 or 8   // ps_log2: -1, no power of two
+  int num_pages, page_size, ps_log2, num_q_heads, num_kv_heads, num_tokens;   // ps_log2: -1, no power of two
+  int token_warps;       // warps per token: 1, 2, 4 or 8
   int half;              // rot_dim / 2
   int interleaved, num_axes, max_position;
   int axis_end[4];       // first pair behind each axis
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, FP8 ? 3 : 4) append_rope_kernel(cons
   // A token's angles are two dependent loads away (position, then a row of the
   // table, from HBM if no token near has been there): the first row's lanes ask L2
   // for those of the token kAhead further on.
-  if (row == 0 && turns && t + kAhead < p.num_tokens && (lane & 1) == 0) {
+  if (row == 0 && turns && t < p.num_tokens - kAhead && (lane & 1) == 0) {
     const int i = 4 * lane;
     const int a = i < p.axis_end[0] ? 0 : i < p.axis_end[1] ? 1 : i < p.axis_end[2] ? 2 : 3;
     const int ahead = p.positions[a * p.positions_stride + t + kAhead];
@@ -325,7 +325,7 @@ cudaError_t launch(const RopeParams& p, bool fp8, cudaStream_t st) {
   auto kern = p.interleaved ? (fp8 ? append_rope_kernel<D, true, true> : append_rope_kernel<D, false, true>)
                             : (fp8 ? append_rope_kernel<D, true, false> : append_rope_kernel<D, false, false>);
   const int per_cta = kWarps / p.token_warps;
-  kern<<<(p.num_tokens + per_cta - 1) / per_cta, kThreads, 0, st>>>(p);
+  kern<<<(p.num_tokens - 1) / per_cta + 1, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -448,9 +448,12 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return PA_ERR_CUDA;
-  // warps per token: eight while the SMs have no more than 64 warps each to run
+  // Warps per token: as many as leave the SMs no more than 32 warps each to run (us
+  // for 8 / 4 / 2 / 1 warps, bf16: 300 tokens 3.8 / 4.2 / 6.1 / 10.0, 1200 tokens 10.6 /
+  // 8.1 / 9.6 / 14.0, 2400 tokens 20.0 / 16.2 / 15.1 / 17.9, 4800 tokens 36.0 / 28.0 /
+  // 26.3 / 25.5).
   p.token_warps = kWarps;
-  while (p.token_warps > 1 && static_cast<int64_t>(num_tokens) * p.token_warps > static_cast<int64_t>(sms) * 64)
+  while (p.token_warps > 1 && static_cast<int64_t>(num_tokens) * p.token_warps > static_cast<int64_t>(sms) * 32)
     p.token_warps /= 2;
   const cudaError_t r = head_dim == 64 ? launch<64>(p, fp8, st)
                         : head_dim == 128 ? launch<128>(p, fp8, st) : launch<256>(p, fp8, st);
