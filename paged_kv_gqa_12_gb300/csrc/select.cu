@@ -34,8 +34,7 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 // histogram, undecided pages ranked in shared memory.
 template <int T>
 struct Sel {
-  static constexpr int kPer = T == 1024 ? 8 : 16;
-  static constexpr int kBins = T <= 64 ? 512 : T == 128 ? 1024 : 2048;
+  static constexpr int kBins = T == 32 ? 256 : T <= 256 ? 1024 : 2048;
   static constexpr int kListCap = 2 * T < 512 ? 2 * T : 512;
 };
 
@@ -480,7 +479,7 @@ __device__ __forceinline__ void find_bin(SelShared<T>& s, int n_bins, uint32_t k
 
 // The k-th largest of the 32-bit keys in `keys` of the pages marked in `open`.
 template <int T>
-__device__ uint32_t kth_largest(SelShared<T>& s, const uint32_t* keys, const uint32_t* open, int n, uint32_t k) {
+__device__ __noinline__ uint32_t kth_largest(SelShared<T>& s, const uint32_t* keys, const uint32_t* open, int n, uint32_t k) {
   uint32_t prefix = 0;
   for (int shift = 24; shift >= 0; shift -= 8) {
     for (int i = threadIdx.x; i < 256; i += T) s.hist[i] = 0;
@@ -572,10 +571,10 @@ __device__ double exact_score(const SelectParams& p, const int32_t* bt, int row,
 // two edges take the place of t: in above the upper edge + 2 eps, out below the
 // lower edge - 2 eps.  What is chosen and what is open is kept as bit maps in
 // shared memory, and the chosen pages are written in ascending order at the end.
-template <int D, int T>
+template <int D, int T, int kPer>
 __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
   constexpr int W = T / 32;
-  constexpr int kPer = Sel<T>::kPer, kBins = Sel<T>::kBins, kListCap = Sel<T>::kListCap;
+  constexpr int kBins = Sel<T>::kBins, kListCap = Sel<T>::kListCap;
   extern __shared__ uint32_t bits[];                 // chosen, then open
   __shared__ SelShared<T> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -803,7 +802,7 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
       out[at_out++] = w * 32 + __ffs(m) - 1;
 }
 
-template <int D, int T>
+template <int D, int T, int kPer>
 cudaError_t launch_select(const SelectParams& p, bool scored, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(p.rows, p.num_kv_heads);
@@ -815,7 +814,7 @@ cudaError_t launch_select(const SelectParams& p, bool scored, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = scored ? 1 : 0;   // overlaps the score kernel's end, and waits for its scores
-  return cudaLaunchKernelEx(&cfg, select_kernel<D, T>, p);
+  return cudaLaunchKernelEx(&cfg, select_kernel<D, T, kPer>, p);
 }
 
 // Shared memory of a score CTA of `rows` rows.
@@ -842,15 +841,18 @@ cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
   // Threads per row: sixteen scores each where rows are many (the fixed work of a
   // row is per warp: 3200 rows of 512 pages 30.3 us against 34.8 with eight, 45.8
   // with four), eight where they are few and the time of one row counts (512 rows of
-  // 2048 pages 64.7 us against 66.3 with sixteen, 73.6 with four); at most 1024
-  // (longer rows read their scores again).
-  const int each = static_cast<int64_t>(p.rows) * p.num_kv_heads >= 8 * p.num_sms ? 16 : 8;
-  if (p.row_pages <= 32 * each) return launch_select<D, 32>(p, chunks > 0, st);
-  if (p.row_pages <= 64 * each) return launch_select<D, 64>(p, chunks > 0, st);
-  if (p.row_pages <= 128 * each) return launch_select<D, 128>(p, chunks > 0, st);
-  if (p.row_pages <= 256 * each) return launch_select<D, 256>(p, chunks > 0, st);
-  if (p.row_pages <= 512 * each) return launch_select<D, 512>(p, chunks > 0, st);
-  return launch_select<D, 1024>(p, chunks > 0, st);
+  // 2048 pages 64.7 us against 66.3 with sixteen, 73.6 with four); at most 512
+  // or 1024 (longer rows read their scores again).
+  if (static_cast<int64_t>(p.rows) * p.num_kv_heads >= 8 * p.num_sms) {
+    if (p.row_pages <= 32 * 16) return launch_select<D, 32, 16>(p, chunks > 0, st);
+    if (p.row_pages <= 64 * 16) return launch_select<D, 64, 16>(p, chunks > 0, st);
+    if (p.row_pages <= 128 * 16) return launch_select<D, 128, 16>(p, chunks > 0, st);
+    if (p.row_pages <= 256 * 16) return launch_select<D, 256, 16>(p, chunks > 0, st);
+    return launch_select<D, 512, 16>(p, chunks > 0, st);
+  }
+  if (p.row_pages <= 64 * 8) return launch_select<D, 64, 8>(p, chunks > 0, st);
+  if (p.row_pages <= 256 * 8) return launch_select<D, 256, 8>(p, chunks > 0, st);
+  return launch_select<D, 1024, 8>(p, chunks > 0, st);
 }
 
 }  // namespace
