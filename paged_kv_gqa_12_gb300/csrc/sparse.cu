@@ -38,10 +38,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSmem = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A tile takes exact weights (P = P_hi + P_lo, two bf16) when some row's largest
-// weight in it exceeds 1 / kHotShare of the row's denominator: one bf16 P is off
-// by up to 2^-8 of a weight, which only many small weights average out.
-constexpr float kHotShare = 8.f;
 
 struct SparseParams {
   const uint16_t* q;
@@ -85,7 +81,8 @@ struct Cfg;
 // hold the compiler to (the figures above are without them): the plan counts on
 // them.  e4m3 D 64 has five where the compiler by itself makes room for four: 400
 // rows of 2048 keys 181 -> 173.5 us, the 64 rows 51.2 -> 51.5.  e4m3 D 128 held to its
-// own four takes 75.3 -> 71.4, with five 80.4; the others do not change.
+// own four takes 75.3 -> 71.4, with five 80.4; the others do not change.  (All of this
+// with one bf16 of small weights; see the P V step.)
 template <int NH8> struct Cfg<64, false, NH8> { static constexpr int TS = 16, NS = 2, CTAS = NH8 == 1 ? 5 : 4; };
 template <int NH8> struct Cfg<128, false, NH8> { static constexpr int TS = 16, NS = NH8 == 1 ? 1 : 2, CTAS = NH8 == 1 ? 5 : 3; };
 template <int NH8> struct Cfg<256, false, NH8> { static constexpr int TS = 16, NS = 1, CTAS = NH8 == 1 ? 3 : 2; };
@@ -327,7 +324,6 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   }
   const uint64_t k_sc = dequant_scale2(p.k_scales != nullptr ? p.k_scales[at.b] : p.k_scale);
   const uint64_t v_sc = dequant_scale2(p.v_scales != nullptr ? p.v_scales[at.b] : p.v_scale);
-  bool l_small = true;   // some row's running denominator is below kHotShare
 
   int it = 0;
   for (int k = warp; k < tiles; k += kWarps, ++it) {
@@ -456,28 +452,14 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
           for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha[j][e & 1];
       }
     }
-    // The denominator only grows, so a key's share of it now bounds its final
-    // weight; weights are at most 1, so once every denominator has reached
-    // kHotShare a tile that raised no maximum cannot be hot.
-    bool hot = false;
-    if (rescale || l_small) {
-      bool small = false;
-#pragma unroll
-      for (int j = 0; j < NH8; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float l = lanes8_sum(l_run[j][h]);
-          const bool real = j * 8 + 2 * c + h < heads;
-          hot |= real && ex2(mx[j][h] - mu[j][h]) * kHotShare > l;
-          small |= real && l < kHotShare;
-        }
-      hot = __any_sync(0xffffffffu, hot);
-      l_small = __any_sync(0xffffffffu, small);
-    }
-
     // ---- O^T += V^T P^T --------------------------------------------------------
-    auto pv = [&](auto exact_tag, auto mask_tag) {
-      constexpr bool EXACT = decltype(exact_tag)::value;
+    // P goes into the MMAs as P_hi + P_lo, two bf16: off by 2^-16 of a weight.  One
+    // bf16 would be off by up to 2^-8, in the same direction for equal weights, which
+    // no number of keys averages out.  Choosing by tile whether the second part is
+    // needed costs as much as always taking it (us, by tile / always: 64 rows of 2048
+    // keys, bf16 D 128 86.4 / 86.2, e4m3 D 128 71.5 / 71.8, D 256 148 / 150; 400 e4m3
+    // rows of D 64 172.9 / 166.1).
+    auto pv = [&](auto mask_tag) {
       constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll
       for (int mt = 0; mt < T::MT; ++mt) {
@@ -489,9 +471,8 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
             const float x = s[mt][j][2 * h], y = s[mt][j][2 * h + 1];
             const uint32_t w = pack_bf16x2(x, y);
             pb[j][h] = movmatrix_t(w);
-            if constexpr (EXACT)
-              pl[j][h] = movmatrix_t(
-                  pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
+            pl[j][h] =
+                movmatrix_t(pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));
           }
         // masked keys have P = 0, but their V may be stale or NaN: zero it
         uint32_t lo_mask = 0xffffffffu, hi_mask = 0xffffffffu;
@@ -510,7 +491,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
 #pragma unroll
           for (int j = 0; j < NH8; ++j) {
             mma_bf16(o[i][j], a, pb[j][0], pb[j][1]);
-            if constexpr (EXACT) mma_bf16(o[i][j], a, pl[j][0], pl[j][1]);
+            mma_bf16(o[i][j], a, pl[j][0], pl[j][1]);
           }
         };
         if constexpr (!FP8) {
@@ -550,11 +531,9 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       }
     };
     if (partial) {
-      pv(std::true_type{}, std::true_type{});
-    } else if (hot) {
-      pv(std::true_type{}, std::false_type{});
+      pv(std::true_type{});
     } else {
-      pv(std::false_type{}, std::false_type{});
+      pv(std::false_type{});
     }
 
     __syncwarp();
