@@ -38,6 +38,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kMaxSmem = 232448;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kBelow = 1.f - 0x1p-12f;
 
 struct SparseParams {
   const uint16_t* q;
@@ -114,6 +115,12 @@ struct Tile {
     return static_cast<uint32_t>(cc * TS * RB + row * RB) + ((((x >> 4) ^ sw) << 4) | (x & 15));
   }
 };
+
+__device__ __forceinline__ uint32_t pack_bf16x2_down(float lo, float hi) {   // rounded towards zero
+  uint32_t r;
+  asm("cvt.rz.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 __device__ __forceinline__ float lanes8_max(float v) {   // over the 8 lanes of equal lane % 4
   v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
@@ -453,12 +460,14 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       }
     }
     // ---- O^T += V^T P^T --------------------------------------------------------
-    // P goes into the MMAs as P_hi + P_lo, two bf16: off by 2^-16 of a weight.  One
+    // P goes into the MMAs as P_hi + P_lo, two bf16: off by 2^-15 of a weight.  One
     // bf16 would be off by up to 2^-8, in the same direction for equal weights, which
     // no number of keys averages out.  Choosing by tile whether the second part is
     // needed costs as much as always taking it (us, by tile / always: 64 rows of 2048
     // keys, bf16 D 128 86.4 / 86.2, e4m3 D 128 71.5 / 71.8, D 256 148 / 150; 400 e4m3
-    // rows of D 64 172.9 / 166.1).
+    // rows of D 64 172.9 / 166.1).  P_hi lies below P, by at least 2^-12 of it, so that
+    // both parts are positive (or zero with P) and an infinite V stays that infinity in
+    // either product (the chunk 168.4 us, the others as they were).
     auto pv = [&](auto mask_tag) {
       constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll
@@ -469,7 +478,7 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float x = s[mt][j][2 * h], y = s[mt][j][2 * h + 1];
-            const uint32_t w = pack_bf16x2(x, y);
+            const uint32_t w = pack_bf16x2_down(x * kBelow, y * kBelow);
             pb[j][h] = movmatrix_t(w);
             pl[j][h] =
                 movmatrix_t(pack_bf16x2(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xffff0000u)));

@@ -69,3 +69,52 @@ def test_equal_weights_between_two_bf16(pb, D, ps, kv, group, splits):
         err = (out.double() - o).abs()
         assert (err <= 2.0 ** -8 * o.abs() + 2.0 ** -13 * spread).all(), (n, (err / spread).max())
         assert (lse.double() - math.log(L / 2 * (1 + w))).abs().max() < 2.0 ** -15
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("D,ps,group", [(64, 16, 4), (128, 16, 8), (256, 32, 4), (128, 64, 16)])
+def test_infinite_values(pb, D, ps, group, splits):
+    """An attended value of +-infinity makes its dim of the output that infinity (both, or a NaN: NaN), on whole pages
+    and on one that the context ends in, and no other dim or head changes a bit."""
+    g = torch.Generator().manual_seed(D)
+    n = 40
+    L = n * ps - 7
+    k, v = (torch.randn(n, ps, 2, D, generator=g).bfloat16() for _ in range(2))
+    q = torch.randn(1, 2 * group, D, generator=g).bfloat16()
+    sinks = torch.randn(2 * group, generator=g)
+    clean, _ = attend(pb, q, k, v, L, scale=D ** -0.5, splits=splits, sinks=sinks)
+    inf = float("inf")
+    put = {3: [(5, 2, inf)], 8: [(n - 1, 1, inf)], 17: [(0, 0, -inf)], 30: [(n - 1, ps - 8, -inf)],
+           41: [(20, 3, inf), (21, 9, inf)], 50: [(7, 1, inf), (30, 4, -inf)], 63: [(11, 6, float("nan"))]}
+    for d, cells in put.items():
+        for page, slot, x in cells:
+            v[page, slot, 1, d] = x
+    v[n - 1, ps - 7:, :, 5] = inf                 # behind the end: not attended
+    out, _ = attend(pb, q, k, v, L, scale=D ** -0.5, splits=splits, sinks=sinks)
+    assert torch.equal(out[:group], clean[:group])
+    rest = [d for d in range(D) if d not in put]
+    assert torch.equal(out[group:, rest], clean[group:, rest])
+    for d, want in ((3, inf), (8, inf), (17, -inf), (30, -inf), (41, inf)):
+        assert (out[group:, d] == want).all(), (d, out[group:, d])
+    assert out[group:, [50, 63]].isnan().all()
+
+
+def test_weights_that_are_powers_of_two_and_zero(pb):
+    """Weights that one bf16 holds (1, and the 2^-20 of far keys) with infinite values, and far keys whose weight is
+    exactly zero beside finite ones."""
+    D, ps = 64, 16
+    k = torch.zeros(4, ps, 1, D)
+    k[2:, :, 0, 0] = -20.0
+    v = torch.ones(4, ps, 1, D)
+    v[1, 4, 0, 7] = float("inf")
+    v[3, 2, 0, 9] = float("-inf")
+    q = torch.zeros(1, 4, D)
+    q[:, :, 0] = 1.0
+    out, _ = attend(pb, q.bfloat16(), k.bfloat16(), v.bfloat16(), 64, scale=math.log(2.0), splits=1)
+    rest = [d for d in range(D) if d not in (7, 9)]
+    assert (out[:, 7] == float("inf")).all() and (out[:, 9] == float("-inf")).all() and (out[:, rest] == 1).all()
+    v[3, 2, 0, 9] = v[1, 4, 0, 7] = 1.0
+    k[2:, :, 0, 0] = -3000.0                      # 2^-3000: zero
+    v[2:] = 500.0
+    out, _ = attend(pb, q.bfloat16(), k.bfloat16(), v.bfloat16(), 64, scale=math.log(2.0), splits=1)
+    assert (out == 1).all()
