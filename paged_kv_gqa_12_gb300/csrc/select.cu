@@ -30,6 +30,9 @@ namespace {
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
 
+// |q|_1 is summed times this: 256 bf16 of any size stay below the largest float.
+constexpr float kQScale = 0x1p-8f;
+
 // Selection by T threads a row: scores kept per thread, steps of the score
 // histogram, undecided pages ranked in shared memory.
 template <int T>
@@ -505,8 +508,8 @@ __device__ __forceinline__ void two_sum(float& a, float b, float& e) {
 }
 
 // Exact score of a page for the group by one warp, scaled by the powers of two
-// sq sa (which bring q and the bounds to about 1, so that products stay in
-// range).  A product of two bf16 is exact in 32 bits and the sums are kept in
+// sq sa (which bring |q|_1 to [256, 512) and the bounds to about 1, so that products
+// stay in range).  A product of two bf16 is exact in 32 bits and the sums are kept in
 // three floats each, s + t + u: what is lost is below 2^-53 of the largest, and
 // the slow 64-bit pipe only joins the three.  Eight lanes take a head.
 template <int D>
@@ -599,8 +602,10 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
   const int lo = p.first, hi = n - p.last;           // pages chosen by score: [lo, hi)
   const uint32_t want = p.top - p.first - p.last;    // (n > top, so hi - lo > want)
 
-  // the largest |q|_1 of the group's heads (before the scores are waited for):
-  // D / 8 lanes a head
+  // the largest |q|_1 of the group's heads (before the scores are waited for), times
+  // kQScale: the scaled elements are exact (a subnormal bf16's too) and up to 256 of
+  // them have a finite sum, so the sum is infinite only where q is not finite.  D / 8
+  // lanes a head.
   float q1 = 0.f;
   for (int j0 = 0; j0 < p.group; j0 += W * (256 / D)) {
     const int j = min(j0 + tid / (D / 8), p.group - 1);
@@ -610,7 +615,8 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      sum += fabsf(__uint_as_float((&x.x)[e] << 16)) + fabsf(__uint_as_float((&x.x)[e] & 0xffff0000u));
+      sum += kQScale * fabsf(__uint_as_float((&x.x)[e] << 16)) +
+             kQScale * fabsf(__uint_as_float((&x.x)[e] & 0xffff0000u));
 #pragma unroll
     for (int k = D / 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
     q1 = sum <= FLT_MAX ? fmaxf(q1, sum) : INFINITY;
@@ -637,9 +643,9 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
 
   float above = INFINITY, below = INFINITY;
   bool all_open = false, ties = true;                // ties: what is open is exactly equal
-  float sq = 1.f, sa = 1.f;                          // 1 / |q|_1 and 1 / A, as powers of two
+  float sq = 1.f, sa = 1.f;                          // 1 / (kQScale |q|_1) and 1 / A, as powers of two
   if (want > 0) {
-    float v[4] = {-INFINITY, -INFINITY, 0.f, q1};    // largest and -smallest finite score, A, |q|_1
+    float v[4] = {-INFINITY, -INFINITY, 0.f, q1};    // largest and -smallest finite score, A, kQScale |q|_1
     uint32_t infs = 0;
     each([&](int, float x) {
       infs += x == INFINITY;
@@ -658,12 +664,14 @@ __global__ void __launch_bounds__(T) select_kernel(const SelectParams p) {
     // sums below the normal range may be flushed: (|q|_1 + D A + 2 D) times the
     // smallest normal covers them.  Where a sum could overflow everything is open.
     // A q that is not finite gives every page +infinity, a zero one zero: exact.
-    const float size = v[3] * am;
+    const float size = v[3] * am;                    // kQScale |q|_1 A
     sq = inverse_power(v[3]);
     sa = inverse_power(am);
     const float eps = !(v[3] <= FLT_MAX) || v[3] == 0.f || am == 0.f ? 0.f
-                      : size <= 0.5f * FLT_MAX
-                          ? 1.01f * (D * 0x1p-22f) * size + (v[3] + D * am + 2 * D) * FLT_MIN : INFINITY;
+                      : size <= 0.5f * kQScale * FLT_MAX
+                          ? 1.01f * (D * 0x1p-22f / kQScale) * size +
+                                (v[3] * (FLT_MIN / kQScale) + (D * am + 2 * D) * FLT_MIN)
+                          : INFINITY;
     all_open = !(eps <= FLT_MAX);
     ties = !all_open;
     if (infs >= want && !all_open) {

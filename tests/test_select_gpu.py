@@ -246,3 +246,36 @@ def test_strided_inputs_graph_and_stream(pb):
         graph.replay()
         torch.cuda.synchronize()
         check(e, pages.cpu())
+
+
+@pytest.mark.parametrize("n", [300, 1500])
+@pytest.mark.parametrize("D", [64, 256])
+def test_finite_queries_whose_magnitudes_sum_past_the_32_bit_range(pb, n, D):
+    # |q|_1 = D 2^124 is not a float, the scores are: near-ties that 32-bit sums cannot tell apart
+    d = make([n * 16], 4, 1, D, 16, top=50, seed=30)
+    g = torch.Generator().manual_seed(31)
+    b = torch.zeros_like(d["bounds"])
+    b[:, :, :, 0] = 2.0 ** -90
+    b[:, :, :, 1] = (1 + torch.rand(b.shape[0], 1, 1, generator=g)).bfloat16() * 2.0 ** -118
+    d["bounds"] = b
+    d["q"][:] = 2.0 ** 124
+    check(d, run(pb, d))
+    d["q"][:, :, 2:] = -(2.0 ** 124)
+    check(d, run(pb, d))
+    # products near the end of the range: sums that overflow in 32 bits but not in 64
+    sign = 1 - 2.0 * (torch.arange(D) % 2)
+    b = (8 * sign * (1 + 2.0 ** -6 * torch.randint(0, 9, (b.shape[0], 1, 1, D), generator=g))).bfloat16()
+    d["bounds"] = b.expand_as(d["bounds"]).contiguous()
+    check(d, run(pb, d))
+    # beside them one that is not finite
+    d["q"][0, 2, 5] = float("inf")
+    check(d, run(pb, d))
+
+
+def test_largest_and_smallest_finite_queries(pb):
+    for q in (3.3895313892515355e38, 2.0 ** -133, 2.0 ** -126):
+        for s in (2.0 ** -100, 1.0, 2.0 ** 100):
+            d = make([300 * 16], 8, 2, 128, 16, top=20, seed=32, spread=s)
+            d["q"] = (torch.sign(d["q"].float()) * q).bfloat16()
+            assert torch.isfinite(d["q"]).all() and (d["q"] != 0).all()
+            check(d, run(pb, d))
