@@ -782,12 +782,16 @@ __global__ void __launch_bounds__(128) decode_merge_kernel(const DecodeParams p)
   }
 }
 
+constexpr int kMaxSmemPerCta = 232448;
+
 template <int D, bool FP8, int NH8, int TS, int NS>
 cudaError_t launch_variant(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeParams& p, dim3 grid,
                            int smem, cudaStream_t stream) {
   auto kern = p.cap_log2 > 0.f ? decode_split_kernel<D, FP8, NH8, TS, NS, true>
                                : decode_split_kernel<D, FP8, NH8, TS, NS, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit is the kernel's, not this call's: of two host threads that set a size of
+  // their own, one could launch under the other's.
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmemPerCta);
   if (e != cudaSuccess) return e;
   if (grid.x > 0 && grid.y > 0 && grid.z > 0) {
     kern<<<grid, kWarps * 32, smem, stream>>>(tmk, tmv, p);

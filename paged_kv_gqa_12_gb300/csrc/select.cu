@@ -837,8 +837,12 @@ cudaError_t launch(const SelectParams& p, int chunks, cudaStream_t st) {
     const bool one = p.block_rows == 1 && p.group <= 8;
     const int smem = one ? One<D>::SMEM : score_smem(p, D, p.block_rows);
     auto kern = one ? score_one_kernel<D> : score_block_kernel<D>;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The limit is the kernel's, not this call's (128 heads of a row; a block of several
+    // rows stays below 48 KB): of two host threads that set a size of their own, one
+    // could launch under the other's.
+    const int most = one ? One<D>::SMEM : 128 * (4 * D + 64);
+    if (most > 48 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
       if (e != cudaSuccess) return e;
     }
     const dim3 grid((p.rows + p.block_rows - 1) / p.block_rows * p.num_kv_heads, chunks);

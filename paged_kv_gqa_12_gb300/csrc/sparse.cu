@@ -665,7 +665,10 @@ cudaError_t launch(const CUtensorMap& tmk, const CUtensorMap& tmv, const SparseP
   const bool wide = std::min(p.group, 16) > 8, cap = p.cap_log2 > 0.f;
   auto kern = wide ? (cap ? sparse_attn_kernel<D, FP8, 2, true> : sparse_attn_kernel<D, FP8, 2, false>)
                    : (cap ? sparse_attn_kernel<D, FP8, 1, true> : sparse_attn_kernel<D, FP8, 1, false>);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit is the kernel's, not this call's (the longest list): of two host threads
+  // that set a size of their own, one could launch under the other's.
+  const int most = (wide ? variant_of<D, FP8, 2>() : variant_of<D, FP8, 1>()).smem0 + kMaxTopPages * 8;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, smem, st>>>(tmk, tmv, p);
   return cudaGetLastError();
