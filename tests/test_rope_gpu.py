@@ -248,3 +248,62 @@ def test_graph_capture_and_other_stream(pb):
     torch.cuda.synchronize()
     e["wq"], e["wk"], e["table"] = d["wq"], d["wk"], d["table"]
     check(e, (qo.cpu(), kc.cpu(), vc.cpu()))
+
+
+# Calls of many tokens: a token takes 8, 4, 2 or 1 warps by how many there are (on 152
+# SMs 8 up to 608 tokens, 1 beyond 2432), a CTA several tokens, and from 1025 tokens on the
+# angles of tokens further on are asked for.
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(9, 3, 64), (9, 3, 128), (5, 3, 256)])
+@pytest.mark.parametrize("T", [700, 1300, 2500, 5003])
+@pytest.mark.parametrize("interleaved,norm", [(False, True), (True, False)])
+def test_many_tokens(pb, kv, Hq, Hkv, D, T, interleaved, norm):
+    half = D // 2
+    d = make(T, Hq, Hkv, D, 16, kv=kv, axes=3, sections=(half // 4, half // 4 + 3, half - half // 2 - 3), norm=norm,
+             interleaved=interleaved, seed=T + D, layout="interleaved" if T == 1300 else "separate")
+    pad = torch.zeros(T, dtype=torch.bool)
+    pad[3::11] = True
+    pad[T - 1] = T == 2500
+    d["slots"][pad] = -1
+    got = run(pb, d)
+    assert (got[0][pad] == 7.0).all()
+    check(d, got, torch.arange(T)[~pad])
+
+
+@pytest.mark.parametrize("T", [700, 1300, 2500])
+def test_many_tokens_norm_of_one_side_keys_alone_and_in_place(pb, T):
+    for drop in ("wq", "wk"):
+        d = make(T, 8, 2, 128, 64, kv="bf16", rot=64, seed=T)
+        d[drop] = None
+        d["offset"] = 1.0
+        check(d, run(pb, d, inplace=True))
+        check(d, run(pb, d, q=False))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [40, 2600])
+@pytest.mark.parametrize("Hq,Hkv,D", [(261, 69, 64), (131, 35, 128), (67, 17, 256)])
+def test_heads_that_take_several_rounds(pb, kv, T, Hq, Hkv, D):
+    # more heads than a token's warps hold rows of at a time
+    if T > 40:
+        Hq, Hkv = Hq // 8, Hkv // 8
+    d = make(T, Hq, Hkv, D, 16, kv=kv, seed=T + Hq, interleaved=kv == "e4m3")
+    check(d, run(pb, d))
+
+
+def test_many_tokens_with_bad_slots_and_positions(pb):
+    T = 2700
+    d = make(T, 4, 2, 64, 16, kv="bf16", seed=40)
+    skip = torch.zeros(T, dtype=torch.bool)
+    for i, (slot, pos) in {5: (-1, 0), 1600: (d["kc"].shape[0] * 16, 0), 2699: (None, 4096), 2000: (None, -1)}.items():
+        skip[i] = True
+        if slot is None:
+            d["pos"][0, i] = pos
+        else:
+            d["slots"][i] = slot
+    scratch = torch.zeros(pb.SCRATCH_HEADER_BYTES, dtype=torch.uint8, device="cuda")
+    got = run(pb, d, scratch=scratch)
+    assert pb.check(scratch) == pb.DEVICE_PAGE_ID | pb.DEVICE_POSITION
+    assert (got[0][skip] == 7.0).all()
+    check(d, got, torch.arange(T)[~skip])
