@@ -141,3 +141,44 @@ def test_strided_bounds_and_far_pages(pb):
     assert torch.equal(got[:2, :, 0], rows[:2].amin(1)) and torch.equal(got[:2, :, 1], rows[:2].amax(1))
     assert torch.equal(got[2, :, 0], rows[2, :ps - 4].amin(0)) and torch.equal(got[2, :, 1], rows[2, :ps - 4].amax(0))
     assert not wide[:, :, 2].any()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("Hkv,D,ps,lo,hi,batch", [(20, 256, 16, 0, 150, 300), (2, 64, 16, 300, 1000, 330),
+                                                  (1, 128, 64, 2000, 4000, 270)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_more_groups_of_pages_than_ctas(pb, kv, Hkv, D, ps, lo, hi, batch, fresh):
+    """Each CTA takes several groups of pages, over more requests than it lists at a time."""
+    rng = np.random.default_rng(D + batch)
+    lens = rng.integers(lo, hi, size=batch)
+    n = -(-lens // ps)
+    pool = int(n.sum()) + 5
+    g = torch.Generator(device="cuda").manual_seed(D)
+    k = torch.randn(pool, ps, Hkv, D, generator=g, device="cuda").bfloat16()
+    if kv == "fp8_e4m3":
+        k = k.to(torch.float8_e4m3fn).view(torch.uint8)
+    table = torch.full((batch, int(n.max())), -1, dtype=torch.int32)
+    perm = torch.from_numpy(rng.permutation(pool)[:int(n.sum())].astype(np.int32))
+    filled = torch.zeros(pool, dtype=torch.int64)          # filled slots of the pages that are to be written
+    new = rng.integers(0, lens + 1) if fresh else lens
+    at = 0
+    for b in range(batch):
+        table[b, :n[b]] = perm[at:at + n[b]]
+        if new[b]:
+            first = (lens[b] - new[b]) // ps
+            ids = table[b, first:n[b]].long()
+            filled[ids] = ps
+            filled[ids[-1]] = int(lens[b] - (n[b] - 1) * ps)
+        at += n[b]
+    bounds = torch.full((pool, Hkv, 2, D), MARK, dtype=torch.bfloat16, device="cuda")
+    qsl = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda() if fresh else None
+    scratch = torch.zeros(pb.SCRATCH_HEADER_BYTES, dtype=torch.uint8, device="cuda")
+    pb.page_bounds(k, table.cuda(), torch.from_numpy(lens.astype(np.int32)).cuda(), bounds, query_start_loc=qsl,
+                   kv_dtype=pb.KV_FP8_E4M3 if kv == "fp8_e4m3" else pb.KV_BF16, k_scale=0.5, scratch=scratch)
+    assert pb.check(scratch) == 0
+    x = k.float() if kv == "bf16" else (k.view(torch.float8_e4m3fn).float() * 0.5).bfloat16().float()
+    f = filled.cuda()
+    out = (torch.arange(ps, device="cuda") >= f[:, None])[..., None, None]
+    want = torch.stack([x.masked_fill(out, float("inf")).amin(1), x.masked_fill(out, -float("inf")).amax(1)], 2)
+    want = torch.where((f > 0)[:, None, None, None], want, torch.full_like(want, MARK))
+    assert torch.equal(bounds.float(), want)
