@@ -293,7 +293,7 @@ typedef struct {
   int32_t rot_dim;       /* leading dims of each head that rotate: a multiple of 8, 0 (none) .. head_dim */
   int32_t interleaved;   /* pair i is dims (i, i + rot_dim / 2) when 0, (2i, 2i + 1) when 1 */
   int32_t num_axes;      /* position axes, 1 .. 4 (1 for text; 3 for time, height, width) */
-  int32_t sections[4];   /* pairs of each axis, in order; they sum to rot_dim / 2 */
+  int32_t sections[4];   /* pairs of each axis, in order; they sum to rot_dim / 2 (one axis: or 0, all pairs) */
   int32_t max_position;  /* rows of cos_sin */
   const float* cos_sin;  /* fp32 [max_position, rot_dim]: a position's cosines of pairs 0 .. rot_dim / 2 - 1,
                             then its sines; 16-byte aligned */

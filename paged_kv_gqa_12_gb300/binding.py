@@ -308,6 +308,11 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
     RMS norm weights or None.  The tensors are kept alive by the returned struct."""
     if (cos_sin is None) != (rot_dim == 0):
         raise ValueError("cos_sin is given exactly when rot_dim > 0")
+    sec = [int(x) for x in sections] if sections is not None else [rot_dim // 2]
+    if not 1 <= len(sec) <= 4:
+        raise ValueError("1 to 4 position axes")
+    if min(sec) < 0 or sum(sec) != rot_dim // 2:
+        raise ValueError("sections must sum to rot_dim / 2")
     dev = _device(*(t for t in (cos_sin, q_norm, k_norm) if t is not None))
     for name, t, dtype, dims in (("q_norm", q_norm, torch.bfloat16, 1), ("k_norm", k_norm, torch.bfloat16, 1),
                                  ("cos_sin", cos_sin, torch.float32, 2)):
@@ -315,9 +320,6 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
             _typed(name, t, dtype, dims, dev)
     if cos_sin is not None and cos_sin.shape[1] != rot_dim:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
-    sec = [int(x) for x in sections] if sections is not None else [rot_dim // 2]
-    if not 1 <= len(sec) <= 4:
-        raise ValueError("1 to 4 position axes")
     r = PaRope(rot_dim=rot_dim, interleaved=1 if interleaved else 0, num_axes=len(sec),
                sections=(ctypes.c_int32 * 4)(*sec), max_position=0 if cos_sin is None else cos_sin.shape[0],
                cos_sin=_ptr(cos_sin), cos_sin_stride=0 if cos_sin is None else cos_sin.stride(0), q_norm=_ptr(q_norm),

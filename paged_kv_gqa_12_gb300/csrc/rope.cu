@@ -361,14 +361,12 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
     return PA_ERR_INVALID_ARG;
   if (rot > 0) {
     if (rope->num_axes < 1 || rope->num_axes > 4 || rope->max_position <= 0) return PA_ERR_INVALID_ARG;
-    if (rope->num_axes > 1) {
-      int64_t sum = 0;
-      for (int a = 0; a < rope->num_axes; ++a) {
-        if (rope->sections[a] < 0) return PA_ERR_INVALID_ARG;
-        sum += rope->sections[a];
-      }
-      if (sum != rot / 2) return PA_ERR_INVALID_ARG;
+    int64_t sum = 0;
+    for (int a = 0; a < rope->num_axes; ++a) {
+      if (rope->sections[a] < 0) return PA_ERR_INVALID_ARG;
+      sum += rope->sections[a];
     }
+    if (sum != rot / 2 && !(rope->num_axes == 1 && sum == 0)) return PA_ERR_INVALID_ARG;
   }
   if (num_tokens == 0) return PA_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !slot_mapping) return PA_ERR_INVALID_ARG;

@@ -72,6 +72,17 @@ def test_append_rope_sections_have_to_sum_up(lib):
         assert rope_args(lib, num_axes=3, sections=(ctypes.c_int32 * 4)(*sec)) == status
 
 
+def test_sections_of_one_axis(lib):
+    sec = lambda *x: (ctypes.c_int32 * 4)(*x)
+    for s in (sec(32), sec(63), sec(65), sec(-64)):
+        assert rope_args(lib, sections=s) == INVALID
+    for s in (sec(64), sec(0), sec(64, 7, 7, 7)):        # all pairs; 0 stands for all
+        assert rope_args(lib, sections=s, tokens=0) == OK
+    for s in ((16,), (), (33,), (-32, 64), (16, 17)):
+        with pytest.raises(ValueError, match="sections|axes"):
+            pb.rope(torch.zeros(4, 64), rot_dim=64, sections=s)
+
+
 def bounds_args(lib, **over):
     a = dict(k=0x10000, kvs=(16384, 1024, 128), pages=8, page=16, hkv=8, d=128, kv=0, bt=0x20000, bts=10, width=10,
              lens=0x30000, qsl=0, batch=4, scale=1.0, scales=0, bounds=0x40000, bs=(2048, 256))
