@@ -328,6 +328,8 @@ def rope(cos_sin=None, *, rot_dim: int, interleaved: bool = False, sections=None
     if len(dims) > 1:
         raise ValueError("q_norm and k_norm must be [head_dim]")
     r.tensors = (cos_sin, q_norm, k_norm)
+    if dev >= 0:
+        r.device = dev
     if dims:
         r.norm_dim = dims.pop()
     return r
@@ -373,6 +375,22 @@ def _pair(k_name, k, v_name, v, dtype, dims, dev):
     return shape, stride
 
 
+def _scratch(scratch, dev):
+    """Pointer of a workspace (alloc_scratch makes one); the call itself checks its size."""
+    if scratch.get_device() != dev or not scratch.is_contiguous():
+        raise ValueError("scratch must be a contiguous tensor on the current CUDA device")
+    return scratch.data_ptr()
+
+
+def _header(scratch, dev):
+    """Pointer of an optional workspace of which the header alone is used."""
+    if scratch is None:
+        return None
+    if scratch.nbytes < SCRATCH_HEADER_BYTES:
+        raise ValueError(f"scratch must hold the header's {SCRATCH_HEADER_BYTES} bytes")
+    return _scratch(scratch, dev)
+
+
 def _cache_type(kv_dtype):
     return torch.uint8 if kv_dtype == KV_FP8_E4M3 else _BF16
 
@@ -402,6 +420,8 @@ def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_ma
         hq, qp, op = shape[1], q.data_ptr(), q_out.data_ptr()
     if getattr(r, "norm_dim", D) != D:
         raise ValueError("q_norm and k_norm must be [head_dim]")
+    if getattr(r, "device", dev) != dev:
+        raise ValueError("cos_sin, q_norm and k_norm must be on the current CUDA device")
     pp, ps = None, 0
     if r.rot_dim > 0:
         if positions is None:
@@ -415,7 +435,7 @@ def append_rope_kv(r: PaRope, k_new, v_new, positions, k_cache, v_cache, slot_ma
     status = load().pa_append_rope_kv(
         ctypes.byref(r), qp, qs[0], qs[1], op, os_[0], os_[1], hq, k_new.data_ptr(), v_new.data_ptr(), ns[0], ns[1], pp,
         ps, k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2], cs[0], cs[1], hkv, D, kv_dtype,
-        slot_mapping.data_ptr(), T, k_scale, v_scale, None if scratch is None else scratch.data_ptr(),
+        slot_mapping.data_ptr(), T, k_scale, v_scale, _header(scratch, dev),
         _raw_stream(stream, dev))
     if status != PA_OK:
         raise PaError(status, "pa_append_rope_kv")
@@ -473,7 +493,7 @@ def page_bounds(k_cache, block_table, seq_lens, bounds, *, query_start_loc=None,
         k_cache.data_ptr(), ks[0], ks[1], ks[2], pages, ps, hkv, D, kv_dtype, block_table.data_ptr(), bts, width,
         seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(), batch, k_scale,
         _floats("k_scales", k_scales, batch, dev), bounds.data_ptr(), bs[0], bs[1],
-        None if scratch is None else scratch.data_ptr(), _raw_stream(stream, dev))
+        _header(scratch, dev), _raw_stream(stream, dev))
     if status != PA_OK:
         raise PaError(status, "pa_page_bounds")
 
@@ -522,7 +542,7 @@ def select_pages(p: PaSparsePlan, q, bounds, block_table, seq_lens, pages, *, qu
     status = load().pa_select_pages(
         ctypes.byref(p), q.data_ptr(), qs[0], qs[1], bounds.data_ptr(), bs[0], bs[1], pool, block_table.data_ptr(), bts,
         seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows,
-        pages.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
+        pages.data_ptr(), _scratch(scratch, dev), scratch.nbytes, _raw_stream(stream, dev))
     if status != PA_OK:
         raise PaError(status, "pa_select_pages")
 
@@ -554,7 +574,7 @@ def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, p
         None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows, pages.data_ptr(), scale,
         _floats("sinks", sinks, s.num_q_heads, dev), k_scale, v_scale, _floats("k_scales", k_scales, batch, dev),
         _floats("v_scales", v_scales, batch, dev), out.data_ptr(), os_[0], os_[1],
-        None if lse is None else lse.data_ptr(), scratch.data_ptr(), scratch.nbytes, _raw_stream(stream, dev))
+        None if lse is None else lse.data_ptr(), _scratch(scratch, dev), scratch.nbytes, _raw_stream(stream, dev))
     if status != PA_OK:
         raise PaError(status, "pa_sparse_attend")
 

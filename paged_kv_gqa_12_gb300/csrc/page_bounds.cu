@@ -270,7 +270,7 @@ extern "C" pa_status pa_page_bounds(const void* k_cache, int64_t kv_stride_page,
   const int e = fp8 ? 1 : 2;
   auto a16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
   if (!a16(k_cache) || (kv_stride_page * e) % 16 || (kv_stride_tok * e) % 16 || (kv_stride_head * e) % 16 ||
-      !a16(bounds) || bounds_stride_page % 8 || bounds_stride_head % 8)
+      !a16(bounds) || bounds_stride_page % 8 || bounds_stride_head % 8 || reinterpret_cast<uintptr_t>(scratch) % 4)
     return PA_ERR_UNSUPPORTED;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -386,7 +386,8 @@ extern "C" pa_status pa_append_rope_kv(const pa_rope* rope, const void* q, int64
   if (q && (!at(q, 8) || !at(q_out, 8) || (q_stride_tok % 4) || (q_stride_head % 4) || (q_out_stride_tok % 4) ||
             (q_out_stride_head % 4)))
     return PA_ERR_UNSUPPORTED;
-  if (!at(rope->q_norm, 8) || !at(rope->k_norm, 8) || !at(slot_mapping, 8)) return PA_ERR_UNSUPPORTED;
+  if (!at(rope->q_norm, 8) || !at(rope->k_norm, 8) || !at(slot_mapping, 8) || !at(scratch, 4))
+    return PA_ERR_UNSUPPORTED;
   if (!at(k_cache, 16) || !at(v_cache, 16) || (kv_stride_page * e) % 16 || (kv_stride_tok * e) % 16 ||
       (kv_stride_head * e) % 16)
     return PA_ERR_UNSUPPORTED;

@@ -250,3 +250,13 @@ def test_structs_have_the_sizes_c_gives_them(tmp_path):
                     str(exe)], check=True)
     got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
     assert got == [ctypes.sizeof(pb.PaRope), ctypes.sizeof(pb.PaSparseShape), ctypes.sizeof(pb.PaSparsePlan)]
+
+
+def test_binding_refuses_workspaces_of_another_kind():
+    with pytest.raises(ValueError, match="scratch"):
+        pb._scratch(torch.zeros(1 << 17, dtype=torch.uint8), 0)
+    with pytest.raises(ValueError, match="scratch"):
+        pb._header(torch.zeros(1 << 17, dtype=torch.uint8), 0)
+    with pytest.raises(ValueError, match="header"):
+        pb._header(torch.zeros(64, dtype=torch.uint8), -1)
+    assert pb._header(None, 0) is None
