@@ -15,13 +15,14 @@
 // no exchange; the norm needs log2(D / 8) shuffles.
 //
 // Measured (411 MB: 16381 tokens, 32 + 2 x 8 heads of 128, norms, three axes):
-// 76.5 us, 5.4 TB/s, 79 % of the copy bandwidth.  With eight warps a token 85 us:
+// 76.4 us, 5.4 TB/s, 79 % of the copy bandwidth.  With eight warps a token 85 us:
 // half of its 547 warp instructions a lane were the token's own (slot, positions,
 // angles, 64-bit addresses); one warp a token leaves 386.  Packed fp32 arithmetic
-// and 32-bit byte strides took a third off before that (119 -> 93 us).  Slower: one
-// persistent CTA loop with hoisted rows (register spills, 120 us), the rows through a
-// cp.async ring (141 us), 16-byte vectors (spills, 101 us), rows prefetched into L2
-// (no change).
+// and 32-bit byte strides took a fifth off before that (119 -> 93 us).  Slower: one
+// persistent CTA loop with hoisted rows (120 us), the rows through a cp.async ring (141
+// us), 16-byte vectors (101 us), rows prefetched into L2 (no change).  Nor does it pay to
+// prefetch the angles of tokens further on: 512 / 1024 / 2432 / 4864 ahead 77.2 / 76.9 /
+// 77.9 / 77.8 us, 8191 tokens of heads of 256 61 us for 54.1 without.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -38,10 +39,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Tokens ahead whose angles are asked for: about what the SMs hold at a time (16381
-// tokens at random positions, eight warps each: none 91.9 us, 1024 85.0, 1536 86.0,
-// 3000 89.6).
-constexpr int kAhead = 1024;
 
 // Strides are in bytes and below 2^32: an address is one 32 x 32 + 64 bit product.
 struct RopeParams {
@@ -120,6 +117,10 @@ __device__ __forceinline__ uint32_t quant4(F2 lo, F2 hi, float scale) {
 // run at the same time the more they are.  kQ query rows and kKv key or value rows
 // per lane group are in flight at a time, the first ones' loads ahead of the token's
 // slot and positions.
+// CTAs an SM: four of bf16, which spill (bytes stored: heads of 64 and 128 40, 92 to 100
+// where pairs are interleaved, of 256 136 and 104), three of e4m3, which hardly do.  us with
+// three / four: 16381 tokens bf16 78.9 / 76.4, interleaved 77.5 / 78.6, e4m3 90.3 / 88.4; 8191
+// tokens of heads of 256 58.1 / 54.2; 250 e4m3 tokens 3.8 / 4.0.
 template <int D, bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, FP8 ? 3 : 4) append_rope_kernel(const RopeParams p) {
   constexpr int LPR = D / 8;                  // lanes per row
@@ -206,20 +207,6 @@ __global__ void __launch_bounds__(kThreads, FP8 ? 3 : 4) append_rope_kernel(cons
         (&cs.x)[e] = __ldg(row);
         (&sn.x)[e] = __ldg(row + p.half);
       }
-    }
-  }
-
-  // A token's angles are two dependent loads away (position, then a row of the
-  // table, from HBM if no token near has been there): the first row's lanes ask L2
-  // for those of the token kAhead further on.
-  if (row == 0 && turns && t < p.num_tokens - kAhead && (lane & 1) == 0) {
-    const int i = 4 * lane;
-    const int a = i < p.axis_end[0] ? 0 : i < p.axis_end[1] ? 1 : i < p.axis_end[2] ? 2 : 3;
-    const int ahead = p.positions[a * p.positions_stride + t + kAhead];
-    if (static_cast<unsigned>(ahead) < static_cast<unsigned>(p.max_position)) {
-      const float* row = p.cos_sin + offset(ahead, p.cos_sin_row) + i;
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(row + p.half));
     }
   }
 
