@@ -701,20 +701,27 @@ pa_status validate_sparse(const pa_sparse_shape& s) {
 
 // Splits of each row: as many as keep the call one wave of the CTAs that the SMs
 // hold, with at least 32 keys each, and 256 beyond sixteen (whose merging costs
-// more than it gains).  Just above one wave three splits fill the second one.
+// more than it gains).  Up to a quarter above one wave three splits fill the second
+// one; stages of 64 keys do not divide so finely, and stay whole.
 // Measured, rows of 2048 keys, 8 kv heads, head_dim 128 bf16 (us by splits): 1 row
 // 1: 35.2, 8: 10.6, 16: 8.8, 32: 10.0, 64: 12.7; 16 rows 1: 50.9, 5: 30.7, 8: 35.3;
-// 64 rows (512 pairs on 760 slots) 1: 86.6, 2: 96.5; 100 rows 1: 162, 3: 146; 128
-// rows 1: 174, 2: 170, 3: 182.  The arrival counters of the scratch header bound the
-// rows that may be split at all (a call beyond them has work enough).
+// 64 rows (512 pairs on 760 slots) 1: 86.6, 2: 96.5.  Pairs a slot, 1 / 2 / 3 splits:
+//   bf16 D 128   1.0 126/133/137, 1.02 159/146/142, 1.15 165/152/150, 1.25 170/159/162, 1.4 175/176/184
+//   e4m3 D 128   1.0 73/83/91, 1.03 102/97/98, 1.15 114/108/106, 1.25 113/110/111, 1.4 117/119/128
+//   bf16 D 256   1.0 150/159/163, 1.02 187/170/167, 1.16 194/181/179, 1.25 198/189/193, 1.4 208/213/218
+//   bf16 D 64    1.0 86/93/99, 1.02 108/102/102, 1.15 114/109/106, 1.25 114/113/115, 1.4 117/127/133
+//   e4m3 D 64 (stages of 64)   1.0 69/79/87, 1.02 81/82/88, 1.15 94/94/96, 1.25 100/101/105
+// The arrival counters of the scratch header bound the rows that may be split at all
+// (a call beyond them has work enough).
 int sparse_splits(const pa_sparse_shape& s, int64_t rows) {
   const int64_t pairs = rows * s.num_kv_heads * sparse_head_groups(s);
   if (pairs <= 0 || pairs > kMergeCounters) return 1;
   const int64_t keys = static_cast<int64_t>(s.top_pages) * s.page_size;
   if (s.num_splits > 0) return std::min(s.num_splits, s.top_pages);
-  const int64_t slots = static_cast<int64_t>(s.num_sms) * variant(s).ctas;
+  const Variant v = variant(s);
+  const int64_t slots = static_cast<int64_t>(s.num_sms) * v.ctas;
   int64_t n = std::min({slots / pairs, keys / 32, std::max<int64_t>(16, keys / 256)});
-  if (pairs > slots && 4 * pairs <= 5 * slots) n = std::min<int64_t>(3, keys / 256);
+  if (pairs > slots && 4 * pairs <= 5 * slots && v.tile_tokens < 64) n = std::min<int64_t>(3, keys / 256);
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, s.top_pages)));
 }
 

@@ -260,3 +260,13 @@ def test_binding_refuses_workspaces_of_another_kind():
     with pytest.raises(ValueError, match="header"):
         pb._header(torch.zeros(64, dtype=torch.uint8), -1)
     assert pb._header(None, 0) is None
+
+
+def test_splits_just_above_one_wave_of_ctas(lib):
+    # 100 rows of 8 kv heads on 760 (608: e4m3, heads of 128, 80 rows) CTAs: three splits fill the second wave; the
+    # 64-key stages of e4m3 heads of 64 are not cut so finely and stay whole
+    def partials(rows, **over):
+        return plan(max_total_q=rows, max_batch=rows, **over).partial_rows
+    assert partials(100) == 300 and partials(80, kv_dtype=1) == 240 and partials(100, head_dim=64) == 300
+    assert partials(100, head_dim=64, kv_dtype=1) < 100
+    assert partials(95) < 100                        # no more than one wave
