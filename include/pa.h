@@ -338,7 +338,7 @@ pa_status pa_append_rope_kv(const pa_rope* rope,
  * bounds[page][kv head][1][d] the largest value of dim d over the page's filled
  * slots (those of keys j < seq_lens[b]), in bf16 -- exact, for an e4m3 cache
  * bounds of bf16(float(code) * scale).  A NaN among the values gives a NaN bound.
- *   k_cache, strides, num_pages, kv_dtype, k_scale, k_scales   as for pa_decode
+ *   k_cache, strides, num_pages, kv_dtype, k_scale, k_scales   as for pa_decode (finite scales)
  *   block_table    device int32 [batch, bt_stride]; max_pages_per_seq (<= bt_stride) bounds a row
  *   seq_lens       device int32 [batch]
  *   query_start_loc  device int32 [batch + 1]: the last (query_start_loc[b+1] - query_start_loc[b])

@@ -105,3 +105,15 @@ def test_sums_of_alternating_sign(pb, D, many):
         ts.check(d, run(pb, d, many))
         d["q"][:, 1] = -1.0
         ts.check(d, run(pb, d, many))
+
+
+def test_capacities_beyond_the_call(pb):
+    # a plan for more rows and wider block tables than the call has; entries behind a context are never read
+    d = ts.make([3000, 2000, 900], 8, 2, 64, 16, top=12, rows=[60, 31, 20], seed=3)
+    want = ts.run(pb, d)
+    wide = torch.full((3, 1000), 2 ** 31 - 1, dtype=torch.int32)
+    wide[:, :d["W"]] = d["bt"]
+    d["bt"] = wide
+    got = ts.run(pb, d, max_total_q=500, max_pages=1000)
+    assert torch.equal(got, want)
+    ts.check(d, got)
