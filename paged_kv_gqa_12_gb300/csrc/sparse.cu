@@ -466,8 +466,9 @@ sparse_attn_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     // needed costs as much as always taking it (us, by tile / always: 64 rows of 2048
     // keys, bf16 D 128 86.4 / 86.2, e4m3 D 128 71.5 / 71.8, D 256 148 / 150; 400 e4m3
     // rows of D 64 172.9 / 166.1).  P_hi lies below P, by at least 2^-12 of it, so that
-    // both parts are positive (or zero with P) and an infinite V stays that infinity in
-    // either product (the chunk 168.4 us, the others as they were).
+    // both parts are positive (or zero with P; P_lo of a weight below 2^-120 is too) and
+    // an infinite V stays that infinity in either product (the chunk 168.4 us, the others
+    // as they were).
     auto pv = [&](auto mask_tag) {
       constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll

@@ -251,8 +251,7 @@ def test_graph_capture_and_other_stream(pb):
 
 
 # Calls of many tokens: a token takes 8, 4, 2 or 1 warps by how many there are (on 152
-# SMs 8 up to 608 tokens, 1 beyond 2432), a CTA several tokens, and from 1025 tokens on the
-# angles of tokens further on are asked for.
+# SMs 8 up to 608 tokens, 1 beyond 2432), and a CTA several tokens.
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("Hq,Hkv,D", [(9, 3, 64), (9, 3, 128), (5, 3, 256)])
