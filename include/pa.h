@@ -78,7 +78,9 @@ typedef enum {
   PA_DEVICE_PAGE_ID = 8,        /* a block-table entry of a page holding attended keys lies outside
                                    [0, num_pages) (or an append slot's page does); that page reads
                                    as zeros (is not written), every other page is unaffected */
-  PA_DEVICE_POSITION = 16       /* a position outside the rotation table; that token is not written */
+  PA_DEVICE_POSITION = 16,      /* a position outside the rotation table; that token is not written */
+  PA_DEVICE_NO_PAGES = 32       /* pa_step_tables: the step needs more pages than are free; nothing of the
+                                   pool or the tables has changed */
 } pa_device_code;
 
 typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 } pa_kv_dtype;
@@ -442,6 +444,173 @@ pa_status pa_sparse_attend(const pa_sparse_plan_t* plan,
                            const float* k_scales, const float* v_scales,
                            void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
                            void* scratch, int64_t scratch_bytes, void* stream);
+
+/* ---- the step of a server with an 8-bit cache and drafted tokens --------------
+ * A step calls, in this order on one stream,
+ *   pa_step_tables     hand out pages, build block tables, slots and positions from lengths
+ *   pa_append_blocks   append K / V as 8-bit codes with a scale for each page and kv head
+ *   pa_block_attend    attend over that cache (one row a request, several, or chunks)
+ *   pa_verify_tokens   accept or replace the drafted tokens by the target's probabilities
+ * pa_step_tables and pa_verify_tokens go with any cache of the library. */
+
+/* Tables of a step from the lengths of its requests, for a pool whose free pages are a stack
+ * (each page belongs to one request at a time).  Request b holds page_counts[b] pages, listed in
+ * block_table[b], and context_lens[b] tokens.  new_lens[b] >= 0 tokens are to come; -1: the
+ * request has ended, its pages go back to the stack (requests ascending, each one's pages in
+ * order), its length and count become 0.  The other requests get the pages they need, requests
+ * ascending and each one's pages in order, from the top of the stack (pages that came back in
+ * this call first):
+ *   page_counts_out[b] = max(page_counts[b], ceil((context_lens[b] + new_lens[b]) / page_size))
+ *   seq_lens[b]        = context_lens[b] + new_lens[b]
+ *   query_start_loc    = running sum of the new tokens (0 for an ended request), [batch + 1]
+ *   positions[t], slots[t] = position and slot (page * page_size + place in it) of new token t;
+ *                        behind the last token positions 0 and slots -1 (padding) up to max_tokens
+ *   context_lens, new_lens, page_counts   device int32 [batch], 0 <= batch <= 8192
+ *   page_counts_out, free_count_out   device int32 [batch] / [1]; seq_lens, page_counts_out and
+ *                  free_count_out may be context_lens, page_counts and free_count themselves
+ *   free_pages     device int32 [free_capacity]: entries [0, *free_count) are the stack, top last
+ *   block_table    device int32 [batch, bt_stride]; max_pages_per_seq (<= bt_stride) bounds a row;
+ *                  only the entries of new pages are written
+ *   slots          device int64 [max_tokens]; positions device int32 [max_tokens]
+ *   scratch        optional (may be NULL), as for pa_append_kv
+ * A step that does not fit is refused whole: block_table, free_pages and the counts stay (the
+ * _out arrays get the counts given), seq_lens is context_lens, query_start_loc is 0, and all of
+ * slots is padding.  Recorded where scratch is given: PA_DEVICE_NO_PAGES; PA_DEVICE_CAPACITY (a
+ * negative length or count, a length beyond max_pages_per_seq, more tokens than max_tokens, a
+ * context that the held pages do not cover, a stack beyond free_capacity).  A page id outside
+ * [0, num_pages) makes its tokens' slots padding and records PA_DEVICE_PAGE_ID.
+ * Asynchronous on `stream`; one kernel launch; the arrays given must not overlap otherwise. */
+pa_status pa_step_tables(const int32_t* context_lens, const int32_t* new_lens, int32_t batch, int32_t page_size,
+                         const int32_t* page_counts, int32_t* page_counts_out,
+                         int32_t* free_pages, int32_t free_capacity, const int32_t* free_count,
+                         int32_t* free_count_out, int32_t num_pages,
+                         int32_t* block_table, int64_t bt_stride, int32_t max_pages_per_seq,
+                         int32_t* seq_lens, int32_t* query_start_loc,
+                         int64_t* slots, int32_t* positions, int32_t max_tokens, void* scratch, void* stream);
+
+/* Codes of an 8-bit cache: e4m3 (bytes, largest 448) or int8 (-127 .. 127).  The element of a
+ * page's slot and kv head is code * scale[page][kv head], K and V with scales of their own. */
+typedef enum { PA_CODE_E4M3 = 0, PA_CODE_INT8 = 1 } pa_code;
+
+/* Append new tokens' K and V to an 8-bit cache with a scale for each page and kv head.  The last
+ * n_b tokens of request b's seq_lens[b] are new (n_b = query_start_loc[b+1] - query_start_loc[b];
+ * 1 with query_start_loc NULL, then num_tokens == batch), packed rows query_start_loc[b] .. of
+ * k_new / v_new.  For each page and kv head that gets some of them
+ *   scale = fp32(max |x| over its new tokens / Q), Q = 448 or 127,
+ *           or the page's old scale if that is larger and the page keeps older tokens
+ *   code  = x / scale, rounded to the nearest code (ties to even), never beyond +-Q
+ * and where the scale of a page with older tokens grew, their codes become code * old / scale,
+ * rounded the same way.  Both are the roundings of the exact quotient.  Infinities do not count
+ * in the maximum and become +-Q; NaN does not count either and becomes e4m3's NaN or int8's 0.
+ * A scale of 0 (all new values 0) has codes 0.
+ *   k_new, v_new   device bf16 [num_tokens, Hkv, head_dim], strides new_stride_tok /
+ *                  new_stride_head, rows 16-byte aligned
+ *   k_cache, v_cache, kv strides, num_pages   as for pa_decode, one byte an element
+ *   k_scales, v_scales   device fp32 [num_pages, Hkv], rows scale_stride apart; scales are >= 0
+ *   block_table, bt_stride, max_pages_per_seq, seq_lens, query_start_loc, scratch  as for pa_page_bounds
+ * A length beyond max_pages_per_seq, or more new tokens than the length or than num_tokens holds,
+ * leaves that request unwritten (PA_DEVICE_CAPACITY); a page id outside the pool leaves that page
+ * unwritten (PA_DEVICE_PAGE_ID).  The pages written belong to one request each.
+ * Asynchronous on `stream`; one kernel launch. */
+pa_status pa_append_blocks(const void* k_new, const void* v_new, int64_t new_stride_tok, int64_t new_stride_head,
+                           void* k_cache, void* v_cache,
+                           int64_t kv_stride_page, int64_t kv_stride_tok, int64_t kv_stride_head,
+                           int32_t num_pages, int32_t page_size, int32_t num_kv_heads, int32_t head_dim, int32_t code,
+                           float* k_scales, float* v_scales, int64_t scale_stride,
+                           const int32_t* block_table, int64_t bt_stride, int32_t max_pages_per_seq,
+                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch,
+                           int32_t num_tokens, void* scratch, void* stream);
+
+/* Static description of pa_block_attend (capacities). */
+typedef struct {
+  int32_t num_q_heads;        /* Hq; Hq % Hkv == 0 and Hq / Hkv <= 128 */
+  int32_t num_kv_heads;       /* Hkv */
+  int32_t head_dim;           /* D in {64, 128, 256} */
+  int32_t page_size;          /* ps in {16, 32, 64} */
+  int32_t code;               /* pa_code */
+  int32_t max_batch;          /* capacity: requests per call, at most 65535 */
+  int32_t max_pages_per_seq;  /* capacity: block-table row width */
+  int32_t max_total_q;        /* capacity of query rows per call */
+  int32_t max_new;            /* capacity: query rows of one request (1: decode) */
+  int32_t window;             /* sliding window W; 0 = off */
+  int32_t has_sinks;          /* 1: calls pass a [Hq] fp32 sink logit array */
+  float soft_cap;             /* 0 = off; else s = cap * tanh(s / cap) */
+  int32_t num_splits;         /* 0 = planner's choice, >0 = max KV splits per request (few rows) */
+  int32_t num_sms;            /* SMs to plan for; 0 = query the current device */
+} pa_block_shape;
+
+/* Plan produced by pa_block_plan; plain data, may be copied. */
+typedef struct {
+  pa_block_shape shape;
+  int32_t chunked;            /* 0: split-KV kernel (few rows a request); 1: chunks of many rows on the
+                                 tcgen05 kernel of pa_extend, over a 16-bit copy of the attended pages' codes */
+  int32_t tile_tokens;        /* keys per pipeline stage */
+  int32_t split_tiles;        /* stages per KV split (0 when num_splits is fixed) */
+  int32_t max_splits;         /* largest split count a request can get */
+  int32_t row_groups;         /* CTAs of 16 rows (8 where one such CTA is enough) a kv head */
+  int32_t bt_cache;           /* block-table entries staged in shared memory per CTA */
+  int32_t smem_bytes;         /* dynamic shared memory per CTA */
+  int32_t group_requests;     /* chunked: requests copied and attended at a time */
+  int64_t scratch_bytes;      /* device scratch the calls need (>= 65536, the header) */
+  int32_t reserved[6];
+} pa_block_plan_t;
+
+/* Plan from capacities; host_seq_lens as for pa_plan (host memory, `batch` entries, or NULL). */
+pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_lens, int32_t batch,
+                        pa_block_plan_t* plan);
+
+/* Attention over an 8-bit cache with a scale for each page and kv head: as pa_decode / pa_extend
+ * with K_j = code * k_scales[page][kv head], V_j likewise.  With query_start_loc NULL one row a
+ * request at seq_lens[b] - 1 (total_q == batch); else rows query_start_loc[b] .. of request b, at
+ * most max_new of them, at the request's last positions.
+ *   k_cache, v_cache   device bytes [num_pages, page_size, Hkv, head_dim], strides as for pa_decode
+ *   k_scales, v_scales device fp32 [num_pages, Hkv], rows scale_stride apart, finite and >= 0
+ *                  (a V scale below 2^-100 counts as 2^-100)
+ * q and out rows are 4-byte aligned for a plan that is not chunked, 16-byte aligned for one that
+ * is.  Few rows: the codes enter the products exactly and the scales in fp32; q is scaled by a
+ * power of two a row and exact in f16 down to 2^-32 of its row's largest value, weights are rounded to
+ * f16 (half a step 2^-12).  Chunks: the same with q as it is.
+ * A length beyond the plan's capacity, a packing with more rows than tokens, than max_new or than
+ * total_q leaves that request's rows untouched (PA_DEVICE_CAPACITY); a block-table entry outside
+ * the pool reads as zeros (PA_DEVICE_PAGE_ID).  Rows behind query_start_loc[batch] are left as they
+ * were.  The other arguments as for pa_extend.  Asynchronous on `stream`; one kernel launch, or
+ * three for each plan->group_requests requests of a chunked plan. */
+pa_status pa_block_attend(const pa_block_plan_t* plan,
+                          const void* q, int64_t q_stride_tok, int64_t q_stride_head,
+                          const void* k_cache, const void* v_cache,
+                          int64_t kv_stride_page, int64_t kv_stride_tok, int64_t kv_stride_head,
+                          int32_t num_pages, const float* k_scales, const float* v_scales, int64_t scale_stride,
+                          const int32_t* block_table, int64_t bt_stride,
+                          const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q,
+                          float scale, const float* sinks,
+                          void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
+                          void* scratch, int64_t scratch_bytes, void* stream);
+
+/* Verification of drafted tokens.  Request b has n_b = query_start_loc[b+1] - query_start_loc[b]
+ * packed rows r (as its new tokens went through the model): tokens[r] is the token fed at row r,
+ * target_probs[r] the target's distribution of the token after it, and so tokens[r + 1] the draft
+ * that row r proposes (n_b - 1 drafts), drawn from draft_probs[r].  In order, row r's draft x is
+ * accepted iff
+ *   accept_u[r] * draft_probs[r][x] < target_probs[r][x]        (draft_probs NULL: 1 in its place)
+ * At the first row whose draft is not accepted -- or the last row -- one token is drawn: the first v with
+ *   sum_{i <= v} y_i  >  sample_u[b] * sum_i y_i
+ * where y = max(target_probs[r] - draft_probs[r], 0) after a rejection (draft_probs NULL: 1 at the
+ * draft, 0 elsewhere; where every y is 0, target_probs[r]), else y = target_probs[r].  The products are exact, the sums keep at least
+ * 44 bits.  out_tokens[b] gets the accepted drafts, the drawn token and then -1 (to its width), num_tokens[b] the accepted drafts + 1.  n_b = 1 is plain
+ * sampling; n_b = 0 gives no token.  If no probability of the row is positive the token is -1.
+ *   tokens, accept_u  device int32 / fp32 [total_rows]; sample_u device fp32 [batch]; u in [0, 1)
+ *   target_probs, draft_probs  device fp32 [total_rows, vocab], rows their stride apart; NaN and
+ *                  negative values count as 0
+ *   out_tokens     device int32 [batch, out_width], rows out_stride apart; num_tokens device int32 [batch]
+ *   scratch        optional (may be NULL), as for pa_append_kv: PA_DEVICE_CAPACITY where a request's rows are more
+ *                  than out_width or lie outside total_rows (its outputs are left untouched)
+ * A draft outside [0, vocab) is not accepted.  Asynchronous on `stream`; one kernel launch. */
+pa_status pa_verify_tokens(const int32_t* tokens, const float* target_probs, int64_t target_stride,
+                           const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                           const int32_t* query_start_loc, int32_t batch, int32_t total_rows,
+                           const float* accept_u, const float* sample_u,
+                           int32_t* out_tokens, int64_t out_stride, int32_t out_width, int32_t* num_tokens,
+                           void* scratch, void* stream);
 
 /* Zero the 64 KiB header at the start of a scratch buffer (enqueued on
  * `stream`): the error word, and the split-arrival counters that decode

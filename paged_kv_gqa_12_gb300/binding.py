@@ -27,6 +27,7 @@ DEVICE_WORK_OVERFLOW = 2
 DEVICE_CAPACITY = 4
 DEVICE_PAGE_ID = 8
 DEVICE_POSITION = 16
+DEVICE_NO_PAGES = 32
 
 # bytes of the scratch header (error word, then split-arrival counters) at
 # the start of every scratch workspace
@@ -39,11 +40,15 @@ MODE_EXTEND = 1
 MODE_VERIFY = 2
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+# codes of an 8-bit cache with block scales (pa_code)
+CODE_E4M3 = 0
+CODE_INT8 = 1
 
 EXPORTED_SYMBOLS = ("pa_plan", "pa_decode", "pa_extend", "pa_scratch_init", "pa_check",
                     "pa_status_string", "pa_version", "pa_decode_static_scratch", "pa_append_kv",
                     "pa_debug_wait_expiry", "pa_append_rope_kv", "pa_page_bounds", "pa_sparse_plan",
-                    "pa_select_pages", "pa_sparse_attend")
+                    "pa_select_pages", "pa_sparse_attend", "pa_step_tables", "pa_append_blocks", "pa_block_plan",
+                    "pa_block_attend", "pa_verify_tokens")
 
 
 class PaShape(ctypes.Structure):
@@ -135,6 +140,41 @@ class PaSparsePlan(ctypes.Structure):
     ]
 
 
+class PaBlockShape(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("code", ctypes.c_int32),
+        ("max_batch", ctypes.c_int32),
+        ("max_pages_per_seq", ctypes.c_int32),
+        ("max_total_q", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("has_sinks", ctypes.c_int32),
+        ("soft_cap", ctypes.c_float),
+        ("num_splits", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+    ]
+
+
+class PaBlockPlan(ctypes.Structure):
+    _fields_ = [
+        ("shape", PaBlockShape),
+        ("chunked", ctypes.c_int32),
+        ("tile_tokens", ctypes.c_int32),
+        ("split_tiles", ctypes.c_int32),
+        ("max_splits", ctypes.c_int32),
+        ("row_groups", ctypes.c_int32),
+        ("bt_cache", ctypes.c_int32),
+        ("smem_bytes", ctypes.c_int32),
+        ("group_requests", ctypes.c_int32),
+        ("scratch_bytes", ctypes.c_int64),
+        ("reserved", ctypes.c_int32 * 6),
+    ]
+
+
 class PaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -183,6 +223,19 @@ def load(path: str | None = None) -> ctypes.CDLL:
     L.pa_sparse_attend.argtypes = [ctypes.POINTER(PaSparsePlan), vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, i64,
                                    vp, vp, i32, i32, vp, f32, vp, f32, f32, vp, vp, vp, i64, i64, vp, vp, i64, vp]
     L.pa_sparse_attend.restype = ctypes.c_int
+    L.pa_step_tables.argtypes = [vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, i64, i32, vp, vp, vp, vp, i32, vp,
+                                 vp]
+    L.pa_step_tables.restype = ctypes.c_int
+    L.pa_append_blocks.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32, vp, vp, i64, vp,
+                                   i64, i32, vp, vp, i32, i32, vp, vp]
+    L.pa_append_blocks.restype = ctypes.c_int
+    L.pa_block_plan.argtypes = [ctypes.POINTER(PaBlockShape), vp, i32, ctypes.POINTER(PaBlockPlan)]
+    L.pa_block_plan.restype = ctypes.c_int
+    L.pa_block_attend.argtypes = [ctypes.POINTER(PaBlockPlan), vp, i64, i64, vp, vp, i64, i64, i64, i32, vp, vp, i64,
+                                  vp, i64, vp, vp, i32, i32, f32, vp, vp, i64, i64, vp, vp, i64, vp]
+    L.pa_block_attend.restype = ctypes.c_int
+    L.pa_verify_tokens.argtypes = [vp, vp, i64, vp, i64, i32, vp, i32, i32, vp, vp, vp, i64, i32, vp, vp, vp]
+    L.pa_verify_tokens.restype = ctypes.c_int
     L.pa_debug_wait_expiry.argtypes = [vp, i32, i64, vp]
     L.pa_debug_wait_expiry.restype = ctypes.c_int
     L.pa_scratch_init.argtypes = [vp, vp]
@@ -577,6 +630,161 @@ def sparse_attend(p: PaSparsePlan, q, k_cache, v_cache, block_table, seq_lens, p
         None if lse is None else lse.data_ptr(), _scratch(scratch, dev), scratch.nbytes, _raw_stream(stream, dev))
     if status != PA_OK:
         raise PaError(status, "pa_sparse_attend")
+
+
+def _vector(name, t, dtype, n, dev):
+    """Pointer of a contiguous [n] tensor."""
+    if t.dtype is not dtype or t.get_device() != dev or t.stride() != (1,):
+        _typed(name, t, dtype, 1, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}]")
+    return t.data_ptr()
+
+
+def step_tables(context_lens, new_lens, page_counts, free_pages, free_count, block_table, *, page_size: int,
+                num_pages: int, seq_lens, query_start_loc, slots, positions, page_counts_out=None, free_count_out=None,
+                scratch=None, stream=None):
+    """pa_step_tables: hand out pages and fill block_table, seq_lens, query_start_loc (int32 [batch + 1]), slots (int64)
+    and positions (int32) of a step from context_lens, new_lens (-1: the request ends) and page_counts (int32 [batch]).
+    free_pages / free_count: the pool's stack (int32 [capacity] / [1]).  Without page_counts_out / free_count_out the
+    counts are updated in place."""
+    dev = _device(context_lens)
+    B, bts, (rows, width) = context_lens.shape[0], block_table.stride(), block_table.shape
+    if block_table.dtype is not _I32 or block_table.get_device() != dev or bts[-1] != 1:
+        _typed("block_table", block_table, _I32, 2, dev)
+    if rows < B:
+        raise ValueError("block_table must have a row per request")
+    held = _vector("page_counts", page_counts, _I32, B, dev)
+    count = _vector("free_count", free_count, _I32, 1, dev)
+    tokens = slots.shape[0]
+    status = load().pa_step_tables(
+        _vector("context_lens", context_lens, _I32, B, dev), _vector("new_lens", new_lens, _I32, B, dev), B, page_size,
+        held, held if page_counts_out is None else _vector("page_counts_out", page_counts_out, _I32, B, dev),
+        _vector("free_pages", free_pages, _I32, free_pages.shape[0], dev), free_pages.shape[0], count,
+        count if free_count_out is None else _vector("free_count_out", free_count_out, _I32, 1, dev), num_pages,
+        block_table.data_ptr(), bts[0], width, _vector("seq_lens", seq_lens, _I32, B, dev),
+        _vector("query_start_loc", query_start_loc, _I32, B + 1, dev), _vector("slots", slots, _I64, tokens, dev),
+        _vector("positions", positions, _I32, tokens, dev), tokens, _header(scratch, dev), _raw_stream(stream, dev))
+    if status != PA_OK:
+        raise PaError(status, "pa_step_tables")
+
+
+def _code_type(code):
+    return torch.int8 if code == CODE_INT8 else torch.uint8
+
+
+def _block_scales(k_scales, v_scales, pages, kv_heads, dev):
+    """Checks of a cache's scales; returns their row stride."""
+    shape, stride = _pair("k_scales", k_scales, "v_scales", v_scales, _F32, 2, dev)
+    if shape != (pages, kv_heads):
+        raise ValueError("k_scales and v_scales must be [pages, kv_heads]")
+    return stride[0]
+
+
+def append_blocks(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, *, query_start_loc=None,
+                  scratch=None, stream=None):
+    """pa_append_blocks: quantise the requests' last tokens (bf16 [T, Hkv, D], packed by query_start_loc; one a request
+    without it) into caches of codes (uint8: e4m3, or int8) with scales per page and kv head (fp32 [pages, Hkv])."""
+    dev = _device(k_new)
+    (T, hkv, D), ns = _pair("k_new", k_new, "v_new", v_new, _BF16, 3, dev)
+    code = CODE_INT8 if k_cache.dtype is torch.int8 else CODE_E4M3
+    cs, kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _code_type(code), 4, dev)
+    if cs[2] != hkv or cs[3] != D:
+        raise ValueError("k_new must be [tokens, kv_heads, head_dim] of the cache")
+    ss = _block_scales(k_scales, v_scales, cs[0], hkv, dev)
+    batch, bts, width = _requests(block_table, seq_lens, query_start_loc, dev)
+    status = load().pa_append_blocks(
+        k_new.data_ptr(), v_new.data_ptr(), ns[0], ns[1], k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1],
+        kvs[2], cs[0], cs[1], hkv, D, code, k_scales.data_ptr(), v_scales.data_ptr(), ss, block_table.data_ptr(), bts,
+        width, seq_lens.data_ptr(), None if query_start_loc is None else query_start_loc.data_ptr(), batch, T,
+        _header(scratch, dev), _raw_stream(stream, dev))
+    if status != PA_OK:
+        raise PaError(status, "pa_append_blocks")
+
+
+def block_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, code: int, max_batch: int,
+               max_pages_per_seq: int, max_total_q: int, max_new: int = 1, window: int = 0, has_sinks: bool = False,
+               soft_cap: float = 0.0, num_splits: int = 0, num_sms: int = 0, host_seq_lens=None) -> PaBlockPlan:
+    """pa_block_plan: the plan of block_attend.  ``max_new``: most query rows of a request; ``host_seq_lens``: optional
+    host sequence of lengths."""
+    s = PaBlockShape(num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, page_size=page_size,
+                     code=code, max_batch=max_batch, max_pages_per_seq=max_pages_per_seq, max_total_q=max_total_q,
+                     max_new=max_new, window=window, has_sinks=1 if has_sinks else 0, soft_cap=soft_cap,
+                     num_splits=num_splits, num_sms=num_sms)
+    p = PaBlockPlan()
+    lens, n = None, 0
+    if host_seq_lens is not None:
+        vals = [int(x) for x in host_seq_lens]
+        n = len(vals)
+        lens = (ctypes.c_int32 * max(n, 1))(*vals)
+    _check(load().pa_block_plan(ctypes.byref(s), lens, n, ctypes.byref(p)), "pa_block_plan")
+    return p
+
+
+def block_attend(p: PaBlockPlan, q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, *,
+                 query_start_loc=None, scale: float, out, lse=None, sinks=None, scratch, stream=None):
+    """pa_block_attend: attention of q (bf16 [rows, Hq, D]; one row a request, or packed by query_start_loc) over caches
+    of codes with scales per page and kv head.  out: bf16 like q, lse: fp32 [rows, Hq]."""
+    dev, s = _device(q), p.shape
+    qs, os_ = q.stride(), out.stride()
+    if q.dtype is not _BF16 or out.dtype is not _BF16 or out.get_device() != dev or len(qs) != 3 or qs[-1] != 1 \
+            or len(os_) != 3 or os_[-1] != 1:
+        _typed("q", q, _BF16, 3, dev)
+        _typed("out", out, _BF16, 3, dev)
+    rows, hq, D = q.shape
+    if hq != s.num_q_heads or D != s.head_dim or out.shape != q.shape:
+        raise ValueError("q and out must be [rows, q_heads, head_dim] of the plan")
+    (pool, ps, hkv, d), kvs = _pair("k_cache", k_cache, "v_cache", v_cache, _code_type(s.code), 4, dev)
+    if ps != s.page_size or hkv != s.num_kv_heads or d != D:
+        raise ValueError("caches must be [pages, page_size, kv_heads, head_dim] of the plan")
+    ss = _block_scales(k_scales, v_scales, pool, hkv, dev)
+    batch, bts, width = _requests(block_table, seq_lens, query_start_loc, dev)
+    if width < s.max_pages_per_seq:
+        raise ValueError("block_table must be max_pages_per_seq of the plan wide")
+    if lse is not None:
+        if lse.dtype is not _F32 or lse.get_device() != dev or len(lse.shape) != 2:
+            _typed("lse", lse, _F32, 2, dev)
+        if lse.shape != (rows, hq) or (lse.stride() != (hq, 1) and not lse.is_contiguous()):
+            raise ValueError("lse must be contiguous [rows, q_heads]")
+    status = load().pa_block_attend(
+        ctypes.byref(p), q.data_ptr(), qs[0], qs[1], k_cache.data_ptr(), v_cache.data_ptr(), kvs[0], kvs[1], kvs[2],
+        pool, k_scales.data_ptr(), v_scales.data_ptr(), ss, block_table.data_ptr(), bts, seq_lens.data_ptr(),
+        None if query_start_loc is None else query_start_loc.data_ptr(), batch, rows, scale,
+        _floats("sinks", sinks, hq, dev), out.data_ptr(), os_[0], os_[1], None if lse is None else lse.data_ptr(),
+        _scratch(scratch, dev), scratch.nbytes, _raw_stream(stream, dev))
+    if status != PA_OK:
+        raise PaError(status, "pa_block_attend")
+
+
+def verify_tokens(tokens, target_probs, query_start_loc, accept_u, sample_u, out_tokens, num_tokens, *,
+                  draft_probs=None, scratch=None, stream=None):
+    """pa_verify_tokens: out_tokens (int32 [batch, width]) and num_tokens (int32 [batch]) from tokens (int32 [T]),
+    target_probs and draft_probs (fp32 [T, vocab]; None: drafts are certain), accept_u (fp32 [T]), sample_u (fp32
+    [batch])."""
+    dev = _device(target_probs)
+    B, (T, V), ts = num_tokens.shape[0], target_probs.shape, target_probs.stride()
+    if target_probs.dtype is not _F32 or ts[-1] != 1:
+        _typed("target_probs", target_probs, _F32, 2, dev)
+    dp, ds = None, (0, 0)
+    if draft_probs is not None:
+        ds = draft_probs.stride()
+        if draft_probs.dtype is not _F32 or draft_probs.get_device() != dev or ds[-1] != 1:
+            _typed("draft_probs", draft_probs, _F32, 2, dev)
+        if draft_probs.shape != (T, V):
+            raise ValueError("draft_probs must be [rows, vocab] like target_probs")
+        dp = draft_probs.data_ptr()
+    os_ = out_tokens.stride()
+    if out_tokens.dtype is not _I32 or out_tokens.get_device() != dev or len(os_) != 2 or os_[-1] != 1:
+        _typed("out_tokens", out_tokens, _I32, 2, dev)
+    if out_tokens.shape[0] != B:
+        raise ValueError("out_tokens must have a row per request")
+    status = load().pa_verify_tokens(
+        _vector("tokens", tokens, _I32, T, dev), target_probs.data_ptr(), ts[0], dp, ds[0], V,
+        _vector("query_start_loc", query_start_loc, _I32, B + 1, dev), B, T, _vector("accept_u", accept_u, _F32, T, dev),
+        _vector("sample_u", sample_u, _F32, B, dev), out_tokens.data_ptr(), os_[0], out_tokens.shape[1],
+        _vector("num_tokens", num_tokens, _I32, B, dev), _header(scratch, dev), _raw_stream(stream, dev))
+    if status != PA_OK:
+        raise PaError(status, "pa_verify_tokens")
 
 
 def debug_wait_expiry(scratch, which: int, limit_ns: int, stream=None):

@@ -257,7 +257,7 @@ using namespace pa;
 
 extern "C" {
 
-int32_t pa_version(void) { return 105; }
+int32_t pa_version(void) { return 106; }
 
 const char* pa_status_string(pa_status status) {
   switch (status) {

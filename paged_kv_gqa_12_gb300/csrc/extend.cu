@@ -49,11 +49,13 @@
 //     copy would not fit dequantise each tile in shared memory instead (the
 //     TMA producer warps convert it in place).  Either way the MMAs see the
 //     same bf16 values.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
 
+#include "blocks.cuh"
 #include "extend.h"
 #include "pa_internal.h"
 #include "tcgen05.cuh"
@@ -87,6 +89,7 @@ struct ExtendParams {
   uint16_t* out;
   int64_t out_stride_tok, out_stride_head;
   float* lse;
+  const float2* page_scales;   // cache of codes: [copy page][Hkv] (K scale, log2 of the V scale)
   int4* work;               // [work_cap][2]: WorkItem
   int* work_count;
   int work_cap;
@@ -341,12 +344,19 @@ __device__ __forceinline__ void dequant_tile(uint8_t* tile, float scale, int lan
   }
 }
 
+// BLK: K and V hold 8-bit codes (exact, K as bf16, V as f16) with a scale for each page and kv
+// head.  The softmax folds both in: x = s (scale ks) log2 e + log2 vs, weights p = 2^(x - m + 7)
+// (f16, at most 2^15 with the lazy maximum; half a step 2^-12) meet the codes of V, and the
+// denominator sums p / vs.  Such weights need no second part.
+constexpr float kBlkBias = 7.f;
+
 // Two CTAs per SM cap a thread at 128 registers (allocation counts 8 warps).
-template <int D, int BN, int NST, int CPS, bool FP8>
+template <int D, int BN, int NST, int CPS, bool FP8, bool BLK>
 __global__ void __launch_bounds__(kThreads, CPS)
 extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                    const __grid_constant__ CUtensorMap tmv, const ExtendParams p) {
   using T = ExtTraits<D, BN, NST, CPS, FP8>;
+  static_assert(!(FP8 && BLK), "codes with block scales come as 16-bit copies");
   const int idx = blockIdx.x / p.num_kv_heads;
   const int kvh = blockIdx.x - idx * p.num_kv_heads;
   if (threadIdx.x == 0) {
@@ -551,7 +561,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   } else if (warp == 7) {
     // ---------------- O += P V issuer (one thread) ----------------
     if (lane == 0) {
-      constexpr uint32_t idesc_pv = idesc_bf16(kRows, D, false, true);
+      constexpr uint32_t idesc_pv = BLK ? idesc_f16(kRows, D, false, true) : idesc_bf16(kRows, D, false, true);
       const uint32_t v_ring = smem_u32(v_s);
       bool ok = true;
       for (int jj = 0; jj < n && ok; ++jj) {
@@ -566,7 +576,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         // P_lo pass runs when a softmax warp flagged the tile (flags written
         // before the warps released the first half of P).  Steps 0 and 1
         // need only the first half.
-        const uint32_t hot = *reinterpret_cast<volatile const uint32_t*>(vflag + 4 * T::sbuf(jj));
+        const uint32_t hot = BLK ? 0u : *reinterpret_cast<volatile const uint32_t*>(vflag + 4 * T::sbuf(jj));
 #pragma unroll
         for (int s = 0; s < BN / 16; ++s) {
           if (s == 2) {
@@ -636,8 +646,17 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         if (lane == 0) mbar_arrive(q_moved);
       }
     }
+    // the request's pages' scales; pages without an attended key are never read
+    const float2* scales = BLK ? p.page_scales + static_cast<int64_t>(b) * p.bt_stride * p.num_kv_heads + kvh : nullptr;
+    const int pg_lo = lo_min >> ps_log2, pg_hi = (L - 1) >> ps_log2;
     for (int j = 0; j < n && ok; ++j) {
       const int k0 = (kt0 + j) * BN;
+      [[maybe_unused]] float2 ksv[BN / 16];      // of each 16 keys (asked for before the wait)
+      if constexpr (BLK) {
+#pragma unroll
+        for (int i = 0; i < BN / 16; ++i)
+          ksv[i] = __ldg(scales + static_cast<int64_t>(min(max((k0 + 16 * i) >> ps_log2, pg_lo), pg_hi)) * p.num_kv_heads);
+      }
       ok = __all_sync(0xffffffffu, wait_or_abort(&s_full[T::sbuf(j)], T::sphase(j), p.err));
       if (!ok) break;
       tc_fence_after();
@@ -650,7 +669,31 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       float mx8[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) mx8[k] = -INFINITY;
-      if (plain) {
+      if constexpr (BLK) {
+        if (!capped) {
+#pragma unroll
+          for (int i = 0; i < BN / 2; ++i) {
+            const float f = ksv[i / 8].x * p.scale_log2, lv = ksv[i / 8].y;
+            const float2 v = __ffma2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])),
+                                        make_float2(f, f), make_float2(lv, lv));
+            sr[2 * i] = __float_as_uint(v.x);
+            sr[2 * i + 1] = __float_as_uint(v.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+            sr[i] = __float_as_uint(fmaf(
+                p.cap_log2, tanh_exp2(__uint_as_float(sr[i]) * (ksv[i / 16].x * p.scale_over_cap)), ksv[i / 16].y));
+        }
+        if (!full) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i)
+            if (k0 + i > pos || k0 + i < lo) sr[i] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i)
+          mx8[i & 7] = fmax3(mx8[i & 7], __uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1]));
+      } else if (plain) {
         // raw scores: masked keys become -inf (it stays -inf through the
         // positive scale); the max is taken raw and the scale folds into the
         // exponent's FFMA
@@ -674,7 +717,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         }
       }
       float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-      if (plain) mx *= p.scale_log2;
+      if (!BLK && plain) mx *= p.scale_log2;
       const float m_new = fmaxf(m_run, mx);
       const bool need = m_new > m_run + kRescaleThreshold;
       const bool any_need = __any_sync(0xffffffffu, need);
@@ -687,7 +730,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       // rescaled, plus the tile's largest weight pm, with mx in the
       // exponent's units; -inf gives 0): a superset of such rows.
       const float pm = ex2(mx - m_base);
-      const bool hot = __any_sync(0xffffffffu, row_ok && pm * (kHotShare - 1.f) > l_run * alpha);
+      const bool hot = !BLK && __any_sync(0xffffffffu, row_ok && pm * (kHotShare - 1.f) > l_run * alpha);
       // O is rescaled and value rows past the sequence end are zeroed before
       // any P is released: PV of this tile may start on its first half
       if (any_need && j > 0) {
@@ -752,7 +795,18 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_half[2 * T::sbuf(j) + half]);
       };
-      if (hot) {
+      if constexpr (BLK) {
+        const float2 nb2 = make_float2(kBlkBias - m_base, kBlkBias - m_base);
+#pragma unroll
+        for (int i = 0; i < BN / 2; ++i) {
+          const float iv = ex2(-ksv[i / 8].y);
+          const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), nb2);
+          const float2 ev = make_float2(ex2(x.x), ex2(x.y));
+          ls2[i & 1] = __ffma2_rn(ev, make_float2(iv, iv), ls2[i & 1]);
+          sr[i] = pack_f16x2(ev.x, ev.y);
+          if (i == 15) release(0);
+        }
+      } else if (hot) {
 #pragma unroll
         for (int blk = 0; blk < BN / 16; ++blk) {
           float2 ev[8];
@@ -796,7 +850,17 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       tc_fence_after();
       const int hq = kvh * G + hh;
       float M2 = m_run, f = 1.f, Z = l_run;
-      if (p.sinks != nullptr) {
+      if constexpr (BLK) {
+        // the row's own LSE is m - 7 + log2 l; against the sink everything is in units of 2^M2
+        M2 = l_run == 0.f ? -INFINITY : m_run - kBlkBias + lg2(l_run);
+        const float sk = p.sinks != nullptr ? p.sinks[hq] * kLog2e : -INFINITY;
+        const float top = fmaxf(M2, sk);
+        const float own = M2 == -INFINITY ? 0.f : ex2(M2 - top);
+        f = own / l_run;            // (no key: 0 / 0, and Z = 0 or the sink's 1 decides below)
+        Z = own + (sk == -INFINITY ? 0.f : ex2(sk - top));
+        if (own == 0.f) f = 0.f;
+        M2 = top;
+      } else if (p.sinks != nullptr) {
         const float sk = p.sinks[hq] * kLog2e;
         M2 = fmaxf(m_run, sk);
         f = (m_run == -INFINITY) ? 0.f : ex2(m_run - M2);
@@ -841,14 +905,14 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   if (warp == 1) tmem_dealloc(tbase, T::TMEM_COLS);
 }
 
-template <int D, int BN, int NST, int CPS, bool FP8>
+template <int D, int BN, int NST, int CPS, bool FP8, bool BLK = false>
 cudaError_t launch_ext(const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                        const ExtendParams& p, cudaStream_t stream) {
   using T = ExtTraits<D, BN, NST, CPS, FP8>;
   extend_schedule_kernel<<<1, kSchedThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  auto kern = extend_attn_kernel<D, BN, NST, CPS, FP8>;
+  auto kern = extend_attn_kernel<D, BN, NST, CPS, FP8, BLK>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t blocks = static_cast<int64_t>(p.work_cap) * p.num_kv_heads;
@@ -1022,7 +1086,143 @@ constexpr float kLog2eHost = 1.4426950408889634f;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// The last part of an extend call: where its keys are read from, and the rest of its arguments.
+struct ExtendCall {
+  const void* kbase;
+  const void* vbase;
+  int64_t st_page, st_tok, st_head;
+  int32_t pages;
+  const int32_t* bt;
+  int64_t bts;
+  const int32_t* seq_lens;
+  const int32_t* qsl;
+  int32_t batch, total_q;
+  float scale;
+  const float* sinks;
+  bool fp8_tiles;           // the attention kernel dequantises e4m3 tiles
+  float k_scale, v_scale;
+  const float* k_scales;
+  const float* v_scales;
+  const float2* page_scales;   // set: K and V are codes, K as bf16, V as f16
+  void* out;
+  int64_t out_stride_tok, out_stride_head;
+  float* lse;
+  void* header;
+  void* work;
+  int work_cap;
+};
+
+// The scheduler and the attention kernel.
+pa_status run_tiles(const pa_shape& s, const CUtensorMap& tmq, const ExtendCall& c, cudaStream_t strm) {
+  const ExtChoice ch = ext_choice(s.head_dim);
+  CUtensorMap tmk, tmv;
+  pa_status st;
+  if ((st = make_kv_map(&tmk, c.kbase, c.fp8_tiles, s.head_dim, s.num_kv_heads, s.page_size, c.pages, c.st_page,
+                        c.st_tok, c.st_head, s.page_size)) != PA_OK)
+    return st;
+  if ((st = make_kv_map(&tmv, c.vbase, c.fp8_tiles, s.head_dim, s.num_kv_heads, s.page_size, c.pages, c.st_page,
+                        c.st_tok, c.st_head, s.page_size)) != PA_OK)
+    return st;
+  const int G = s.num_q_heads / s.num_kv_heads;
+  ExtendParams p{};
+  p.seq_lens = c.seq_lens;
+  p.qsl = c.qsl;
+  p.block_table = c.bt;
+  p.bt_stride = c.bts;
+  p.batch = c.batch;
+  p.total_q = c.total_q;
+  p.num_q_heads = s.num_q_heads;
+  p.num_kv_heads = s.num_kv_heads;
+  p.group = G;
+  p.page_size = s.page_size;
+  p.num_pages = c.pages;
+  p.tm = kRows / G;
+  p.max_kv = s.max_pages_per_seq * s.page_size;
+  p.block_n = ch.block_n;
+  p.scale_log2 = c.scale * kLog2eHost;
+  p.cap_log2 = s.soft_cap > 0.f ? s.soft_cap * kLog2eHost : 0.f;
+  p.scale_over_cap = s.soft_cap > 0.f ? c.scale / s.soft_cap : 0.f;
+  p.window = s.window;
+  p.sinks = c.sinks;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.k_scales = c.k_scales;
+  p.v_scales = c.v_scales;
+  p.page_scales = c.page_scales;
+  p.out = static_cast<uint16_t*>(c.out);
+  p.out_stride_tok = c.out_stride_tok;
+  p.out_stride_head = c.out_stride_head;
+  p.lse = c.lse;
+  p.err = static_cast<uint32_t*>(c.header);
+  p.work_count = reinterpret_cast<int*>(static_cast<uint8_t*>(c.header) + 16);
+  p.work = static_cast<int4*>(c.work);
+  p.work_cap = c.work_cap;
+
+  cudaError_t e;
+  if (c.page_scales != nullptr) {
+    switch (s.head_dim) {
+      case 64: e = launch_ext<64, 64, 4, 2, false, true>(tmq, tmk, tmv, p, strm); break;
+      case 128: e = launch_ext<128, 64, 2, 2, false, true>(tmq, tmk, tmv, p, strm); break;
+      default: e = launch_ext<256, 64, 3, 1, false, true>(tmq, tmk, tmv, p, strm); break;
+    }
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
+  switch (s.head_dim * 2 + (c.fp8_tiles ? 1 : 0)) {
+    case 128: e = launch_ext<64, 64, 4, 2, false>(tmq, tmk, tmv, p, strm); break;
+    case 129: e = launch_ext<64, 64, 4, 2, true>(tmq, tmk, tmv, p, strm); break;
+    case 256: e = launch_ext<128, 64, 2, 2, false>(tmq, tmk, tmv, p, strm); break;
+    case 257: e = launch_ext<128, 64, 2, 2, true>(tmq, tmk, tmv, p, strm); break;
+    case 512: e = launch_ext<256, 64, 3, 1, false>(tmq, tmk, tmv, p, strm); break;
+    default: e = launch_ext<256, 64, 2, 1, true>(tmq, tmk, tmv, p, strm); break;
+  }
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 }  // namespace
+
+namespace pa {
+
+int64_t extend_work_capacity(const pa_shape& s) { return work_capacity(s); }
+
+pa_status extend_q_map(CUtensorMap* map, const pa_shape& s, const void* q, int64_t q_stride_tok,
+                       int64_t q_stride_head, int32_t total_q) {
+  const int G = s.num_q_heads / s.num_kv_heads;
+  return make_q_map(map, q, s.head_dim, s.num_q_heads, total_q, q_stride_tok, q_stride_head, G, kRows / G);
+}
+
+pa_status extend_over_copy(const pa_shape& s, const CUtensorMap& tmq, const void* k_copy, const void* v_copy,
+                           const float2* page_scales, int32_t copy_pages, const int32_t* table,
+                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q, float scale,
+                           const float* sinks, void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
+                           void* header, void* work, void* stream) {
+  ExtendCall c{};
+  c.kbase = k_copy;
+  c.vbase = v_copy;
+  c.st_head = s.head_dim;
+  c.st_tok = static_cast<int64_t>(s.num_kv_heads) * s.head_dim;
+  c.st_page = c.st_tok * s.page_size;
+  c.pages = copy_pages;
+  c.bt = table;
+  c.bts = s.max_pages_per_seq;
+  c.seq_lens = seq_lens;
+  c.qsl = query_start_loc;
+  c.batch = batch;
+  c.total_q = total_q;
+  c.scale = scale;
+  c.sinks = sinks;
+  c.k_scale = c.v_scale = 1.f;
+  c.page_scales = page_scales;
+  c.out = out;
+  c.out_stride_tok = out_stride_tok;
+  c.out_stride_head = out_stride_head;
+  c.lse = lse;
+  c.header = header;
+  c.work = work;
+  c.work_cap = static_cast<int>(work_capacity(s));
+  return run_tiles(s, tmq, c, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace pa
 
 extern "C" pa_status pa_extend(const pa_plan_t* plan, const void* q, int64_t q_stride_tok, int64_t q_stride_head,
                                const void* k_cache, const void* v_cache, int64_t kv_stride_page,
@@ -1072,8 +1272,7 @@ extern "C" pa_status pa_extend(const pa_plan_t* plan, const void* q, int64_t q_s
 
   const int G = s.num_q_heads / s.num_kv_heads;
   const int tm = kRows / G;
-  const ExtChoice ch = ext_choice(s.head_dim);
-  CUtensorMap tmq, tmk, tmv;
+  CUtensorMap tmq;
   if ((st = make_q_map(&tmq, q, s.head_dim, s.num_q_heads, total_q, q_stride_tok, q_stride_head, G, tm)) !=
       PA_OK)
     return st;
@@ -1136,55 +1335,32 @@ extern "C" pa_status pa_extend(const pa_plan_t* plan, const void* q, int64_t q_s
     pages = static_cast<int32_t>(static_cast<int64_t>(batch) * maxp);
   }
   const bool fp8_tiles = fp8 && !copy;   // the attention kernel dequantises in shared memory
-  if ((st = make_kv_map(&tmk, kbase, fp8_tiles, s.head_dim, s.num_kv_heads, s.page_size, pages, st_page, st_tok,
-                        st_head, s.page_size)) != PA_OK)
-    return st;
-  if ((st = make_kv_map(&tmv, vbase, fp8_tiles, s.head_dim, s.num_kv_heads, s.page_size, pages, st_page, st_tok,
-                        st_head, s.page_size)) != PA_OK)
-    return st;
-
-  ExtendParams p{};
-  p.seq_lens = seq_lens;
-  p.qsl = query_start_loc;
-  p.block_table = bt;
-  p.bt_stride = bts;
-  p.batch = batch;
-  p.total_q = total_q;
-  p.num_q_heads = s.num_q_heads;
-  p.num_kv_heads = s.num_kv_heads;
-  p.group = G;
-  p.page_size = s.page_size;
-  p.num_pages = pages;
-  p.tm = tm;
-  p.max_kv = s.max_pages_per_seq * s.page_size;
-  p.block_n = ch.block_n;
-  p.scale_log2 = scale * kLog2eHost;
-  p.cap_log2 = s.soft_cap > 0.f ? s.soft_cap * kLog2eHost : 0.f;
-  p.scale_over_cap = s.soft_cap > 0.f ? scale / s.soft_cap : 0.f;
-  p.window = s.window;
-  p.sinks = sinks;
-  p.k_scale = fp8_tiles ? k_scale : 1.f;
-  p.v_scale = fp8_tiles ? v_scale : 1.f;
-  p.k_scales = fp8_tiles ? k_scales : nullptr;
-  p.v_scales = fp8_tiles ? v_scales : nullptr;
-  p.out = static_cast<uint16_t*>(out);
-  p.out_stride_tok = out_stride_tok;
-  p.out_stride_head = out_stride_head;
-  p.lse = lse;
-  p.err = reinterpret_cast<uint32_t*>(sc);
-  p.work_count = reinterpret_cast<int*>(sc + 16);
-  p.work = reinterpret_cast<int4*>(sc + kScratchHeaderBytes);
-  p.work_cap = static_cast<int>((plan->scratch_bytes - kScratchHeaderBytes) / 32);
-  if (p.work_cap > cap_items) p.work_cap = static_cast<int>(cap_items);
-
-  cudaError_t e;
-  switch (s.head_dim * 2 + (fp8_tiles ? 1 : 0)) {
-    case 128: e = launch_ext<64, 64, 4, 2, false>(tmq, tmk, tmv, p, strm); break;
-    case 129: e = launch_ext<64, 64, 4, 2, true>(tmq, tmk, tmv, p, strm); break;
-    case 256: e = launch_ext<128, 64, 2, 2, false>(tmq, tmk, tmv, p, strm); break;
-    case 257: e = launch_ext<128, 64, 2, 2, true>(tmq, tmk, tmv, p, strm); break;
-    case 512: e = launch_ext<256, 64, 3, 1, false>(tmq, tmk, tmv, p, strm); break;
-    default: e = launch_ext<256, 64, 2, 1, true>(tmq, tmk, tmv, p, strm); break;
-  }
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  ExtendCall call{};
+  call.kbase = kbase;
+  call.vbase = vbase;
+  call.st_page = st_page;
+  call.st_tok = st_tok;
+  call.st_head = st_head;
+  call.pages = pages;
+  call.bt = bt;
+  call.bts = bts;
+  call.seq_lens = seq_lens;
+  call.qsl = query_start_loc;
+  call.batch = batch;
+  call.total_q = total_q;
+  call.scale = scale;
+  call.sinks = sinks;
+  call.fp8_tiles = fp8_tiles;
+  call.k_scale = fp8_tiles ? k_scale : 1.f;
+  call.v_scale = fp8_tiles ? v_scale : 1.f;
+  call.k_scales = fp8_tiles ? k_scales : nullptr;
+  call.v_scales = fp8_tiles ? v_scales : nullptr;
+  call.out = out;
+  call.out_stride_tok = out_stride_tok;
+  call.out_stride_head = out_stride_head;
+  call.lse = lse;
+  call.header = sc;
+  call.work = sc + kScratchHeaderBytes;
+  call.work_cap = static_cast<int>(std::min<int64_t>((plan->scratch_bytes - kScratchHeaderBytes) / 32, cap_items));
+  return run_tiles(s, tmq, call, strm);
 }

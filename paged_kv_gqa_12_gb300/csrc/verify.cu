@@ -1,0 +1,358 @@
+// Verification of drafted tokens against the target's probabilities, and the draw
+// of the token after them, from given random numbers.
+//
+// A request's drafts are tested in order, u q(x) < p(x) (products of two floats,
+// exact in 64 bits); only the row where they end is read whole: the token there is
+// the first v with  C_v > w C,  C_v the running sum of y = max(p - q, 0).  So a call
+// reads one row of p (and of q) a request and is bound by HBM, or for few requests
+// by the latency of its steps.
+//
+// Which v the sum crosses at depends on sums next to a border: in 32 bits a row of
+// 10^5 entries has errors of the order of an entry.  The difference p - q and the
+// sums are therefore pairs of floats (Knuth's two-sum, Dekker's pairs: about 48 bits
+// at the fp32 rate; the card adds 64-bit numbers 64 times slower), joined in 64 bits.
+// A request has a cluster of CTAs: every warp sums a contiguous part of the row,
+// the parts' sums go to all CTAs over distributed shared memory, and the CTA whose
+// warp holds the crossing sums that part again, a few entries a thread.
+#include <cstdint>
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "pa.h"
+#include "pa_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCtas = 8;             // CTAs a request (portable cluster size)
+constexpr int kUnit = 128;              // entries a warp takes at a time
+
+struct VerifyParams {
+  const int32_t* tokens;
+  const float* target;
+  int64_t target_stride;
+  const float* draft;          // null: drafts are certain
+  int64_t draft_stride;
+  int vocab;
+  const int32_t* qsl;
+  int batch, total_rows;
+  const float* accept_u;
+  const float* sample_u;
+  int32_t* out;
+  int64_t out_stride;
+  int out_width;
+  int32_t* num;
+  uint32_t* err;
+};
+
+// A sum held as two floats, hi + lo.
+struct Pair {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float y) {
+    const float s = __fadd_rn(hi, y);
+    const float t = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(y, t)));
+    hi = s;
+  }
+  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+};
+
+// NaN and what is below 0 count as 0; the bound keeps sums of 2^20 entries finite.
+__device__ __forceinline__ float weight(float x) { return fminf(fmaxf(x, 0.f), 0x1p100f); }
+
+// How a row's entries become weights y.
+struct Row {
+  const float* p;
+  const float* q;       // null: nothing is taken off
+  int taken;            // the certain draft whose entry loses 1, or -1
+
+  __device__ __forceinline__ void add(Pair& sum, float pv, float qv, int v) const {
+    pv = weight(pv);
+    qv = q != nullptr ? weight(qv) : (v == taken ? 1.f : 0.f);
+    const float d = __fsub_rn(pv, qv);
+    if (d > 0.f) {
+      const float t = __fsub_rn(d, pv);
+      sum.add(d);
+      sum.lo = __fadd_rn(sum.lo, __fsub_rn(__fsub_rn(pv, __fsub_rn(d, t)), __fadd_rn(qv, t)));
+    }
+  }
+  __device__ __forceinline__ double y(int v) const {
+    const double pv = weight(p[v]);
+    const double d = pv - (q != nullptr ? static_cast<double>(weight(q[v])) : (v == taken ? 1.0 : 0.0));
+    return d > 0.0 ? d : 0.0;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const VerifyParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ double s_part[2][kMaxCtas * kWarps];   // sums of the parts, all of the cluster
+  __shared__ double s_scan[kWarps];
+  __shared__ int s_kept;
+  __shared__ int s_best;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int b = blockIdx.x / C;
+  const int qs = p.qsl[b];
+  const int n = p.qsl[b + 1] - qs;
+  int32_t* out = p.out + static_cast<int64_t>(b) * p.out_stride;
+  // (the same in all threads of the cluster)
+  if (n < 0 || n > p.out_width || qs < 0 || static_cast<int64_t>(qs) + n > p.total_rows) {
+    if (p.err != nullptr && rank == 0 && tid == 0) atomicOr(p.err, kErrCapacity);
+    return;
+  }
+  if (n == 0) {
+    if (rank == 0) {
+      for (int i = tid; i < p.out_width; i += kThreads) out[i] = -1;
+      if (tid == 0) p.num[b] = 0;
+    }
+    return;
+  }
+
+  // (no CTA's shared memory is written before it runs: the wait is before the first write)
+  cluster.barrier_arrive();
+
+  // ---- the drafts, in order ------------------------------------------------
+  if (warp == 0) {
+    int kept = n - 1;
+    for (int i0 = 0; i0 < n - 1; i0 += 32) {
+      const int i = i0 + lane;
+      bool no = false;
+      if (i < n - 1) {
+        const int64_t r = qs + i;
+        const int x = p.tokens[r + 1];
+        const bool in = static_cast<unsigned>(x) < static_cast<unsigned>(p.vocab);
+        const float pv = in ? weight(p.target[r * p.target_stride + x]) : 0.f;
+        const float qv = p.draft == nullptr ? 1.f : in ? weight(p.draft[r * p.draft_stride + x]) : 0.f;
+        no = !(static_cast<double>(p.accept_u[r]) * qv < static_cast<double>(pv));
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, no);
+      if (m != 0) {
+        kept = i0 + __ffs(m) - 1;
+        break;
+      }
+    }
+    if (lane == 0) s_kept = kept;
+  }
+  __syncthreads();
+  const int kept = s_kept;
+  const bool rejected = kept < n - 1;
+  const int64_t r = qs + kept;
+  Row row;
+  row.p = p.target + r * p.target_stride;
+  row.q = rejected && p.draft != nullptr ? p.draft + r * p.draft_stride : nullptr;
+  row.taken = rejected && p.draft == nullptr ? p.tokens[r + 1] : -1;
+  if (rank == 0) {
+    for (int i = tid; i < p.out_width; i += kThreads)
+      if (i != kept) out[i] = i < kept ? p.tokens[qs + i + 1] : -1;
+    if (tid == 0) p.num[b] = kept + 1;
+  }
+
+  // ---- the parts' sums -------------------------------------------------------
+  const int units = (p.vocab + kUnit - 1) / kUnit;
+  const int parts = C * kWarps;
+  auto part_begin = [&](int w) { return static_cast<int>(static_cast<int64_t>(units) * w / parts) * kUnit; };
+  const double w01 = p.sample_u[b];
+  double total = 0.0;
+  int mine = -1;          // the part that holds the crossing
+  double rest = 0.0;      // how far into it the crossing lies
+  for (int pass = 0; pass < 2; ++pass) {
+    Pair sum;
+    const int v1 = min(part_begin(rank * kWarps + warp + 1), p.vocab);
+    int v = part_begin(rank * kWarps + warp);
+    const bool wide = (reinterpret_cast<uintptr_t>(row.p) & 15u) == 0 && (reinterpret_cast<uintptr_t>(row.q) & 15u) == 0;
+    if (wide) {
+      constexpr int U = 4;               // 16 entries of p and q a lane in flight
+      for (; v + U * kUnit <= v1; v += U * kUnit) {
+        float4 a[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int at = v + u * kUnit + lane * 4;
+          a[u] = __ldg(reinterpret_cast<const float4*>(row.p + at));
+          c[u] = row.q != nullptr ? __ldg(reinterpret_cast<const float4*>(row.q + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int at = v + u * kUnit + lane * 4;
+          row.add(sum, a[u].x, c[u].x, at);
+          row.add(sum, a[u].y, c[u].y, at + 1);
+          row.add(sum, a[u].z, c[u].z, at + 2);
+          row.add(sum, a[u].w, c[u].w, at + 3);
+        }
+      }
+    }
+#pragma unroll 8
+    for (v += lane; v < v1; v += 32) row.add(sum, __ldg(row.p + v), row.q != nullptr ? __ldg(row.q + v) : 0.f, v);
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+      const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, m), lo = __shfl_xor_sync(0xffffffffu, sum.lo, m);
+      sum.add(hi);
+      sum.lo = __fadd_rn(sum.lo, lo);
+    }
+    if (pass == 0) cluster.barrier_wait();
+    if (lane < C) *cluster.map_shared_rank(&s_part[pass][rank * kWarps + warp], lane) = sum.value();
+    cluster.sync();
+
+    // every warp for itself: the total, and the part whose running sum first exceeds w * total
+    double part[kMaxCtas * kWarps / 32];
+    double own = 0.0;
+#pragma unroll
+    for (int k = 0; k < kMaxCtas * kWarps / 32; ++k) {
+      const int i = lane * (kMaxCtas * kWarps / 32) + k;
+      part[k] = i < parts ? s_part[pass][i] : 0.0;
+      own += part[k];
+    }
+    double incl = own;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const double t = __shfl_up_sync(0xffffffffu, incl, m);
+      if (lane >= m) incl += t;
+    }
+    total = __shfl_sync(0xffffffffu, incl, 31);
+    if (total > 0.0) {
+      const double target = w01 * total;
+      double before = __shfl_up_sync(0xffffffffu, incl, 1);
+      if (lane == 0) before = 0.0;
+      int found = -1;
+      double left = 0.0;
+      int last = -1;       // the last part that weighs anything: where rounding leaves the sum short of the target
+#pragma unroll
+      for (int k = 0; k < kMaxCtas * kWarps / 32; ++k) {
+        if (part[k] > 0.0) {
+          last = lane * (kMaxCtas * kWarps / 32) + k;
+          if (found < 0 && before + part[k] > target) {
+            found = last;
+            left = target - before;
+          }
+        }
+        before += part[k];
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, found >= 0);
+      if (m != 0) {
+        mine = __shfl_sync(0xffffffffu, found, __ffs(m) - 1);
+        rest = __shfl_sync(0xffffffffu, left, __ffs(m) - 1);
+      } else {
+        mine = __reduce_max_sync(0xffffffffu, last);
+        rest = total;
+      }
+      break;
+    }
+    if (row.q == nullptr && row.taken < 0) break;     // nothing to draw from
+    row.q = nullptr;                                  // p <= q everywhere: from p itself
+    row.taken = -1;
+  }
+  if (mine < 0) {
+    if (rank == 0 && tid == 0) out[kept] = -1;
+    return;
+  }
+  if (mine / kWarps != rank) return;
+
+  // ---- the entry, within the part --------------------------------------------
+  const int v0 = part_begin(mine), v1 = min(part_begin(mine + 1), p.vocab);
+  const int per = (v1 - v0 + kThreads - 1) / kThreads;
+  const int a0 = min(v0 + tid * per, v1), a1 = min(a0 + per, v1);
+  double own = 0.0;
+  int last = -1;
+  for (int v = a0; v < a1; ++v) {
+    const double y = row.y(v);
+    if (y > 0.0) last = v;
+    own += y;
+  }
+  double incl = own;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const double t = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += t;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  if (tid == 0) s_best = 0x7fffffff;
+  __syncthreads();
+  double before = incl - own;
+  for (int w = 0; w < warp; ++w) before += s_scan[w];
+  // the first thread whose running sum exceeds the rest; none (rounding): the last entry that weighs
+  if (own > 0.0 && before + own > rest) atomicMin(&s_best, tid);
+  __syncthreads();
+  if (s_best == 0x7fffffff) {
+    __syncthreads();
+    if (tid == 0) s_best = -1;
+    __syncthreads();
+    atomicMax(&s_best, last);
+    __syncthreads();
+    if (tid == 0) out[kept] = s_best;
+    return;
+  }
+  if (tid == s_best) {
+    int pick = last;
+    for (int v = a0; v < a1; ++v) {
+      const double y = row.y(v);
+      before += y;
+      if (y > 0.0 && before > rest) {
+        pick = v;
+        break;
+      }
+    }
+    out[kept] = pick;
+  }
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_verify_tokens(const int32_t* tokens, const float* target_probs, int64_t target_stride,
+                                      const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                                      const int32_t* query_start_loc, int32_t batch, int32_t total_rows,
+                                      const float* accept_u, const float* sample_u, int32_t* out_tokens,
+                                      int64_t out_stride, int32_t out_width, int32_t* num_tokens, void* scratch,
+                                      void* stream) {
+  using namespace pa;
+  if (batch < 0 || total_rows < 0 || vocab <= 0 || out_width < 0) return PA_ERR_INVALID_ARG;
+  if (vocab > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (batch == 0) return PA_OK;
+  if (!query_start_loc || !sample_u || !num_tokens || (out_width > 0 && !out_tokens)) return PA_ERR_INVALID_ARG;
+  if (total_rows > 0 && (!tokens || !target_probs || !accept_u)) return PA_ERR_INVALID_ARG;
+  if (total_rows > 1 && (target_stride < vocab || (draft_probs && draft_stride < vocab))) return PA_ERR_INVALID_ARG;
+  if (batch > 1 && out_stride < out_width) return PA_ERR_INVALID_ARG;
+  auto off = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) != 0; };
+  if (off(tokens) || off(target_probs) || off(draft_probs) || off(query_start_loc) || off(accept_u) || off(sample_u) ||
+      off(out_tokens) || off(num_tokens) || off(scratch))
+    return PA_ERR_UNSUPPORTED;
+  VerifyParams p{};
+  p.tokens = tokens;
+  p.target = target_probs;
+  p.target_stride = target_stride;
+  p.draft = draft_probs;
+  p.draft_stride = draft_stride;
+  p.vocab = vocab;
+  p.qsl = query_start_loc;
+  p.batch = batch;
+  p.total_rows = total_rows;
+  p.accept_u = accept_u;
+  p.sample_u = sample_u;
+  p.out = out_tokens;
+  p.out_stride = out_stride;
+  p.out_width = out_width;
+  p.num = num_tokens;
+  p.err = static_cast<uint32_t*>(scratch);
+  // CTAs a request: up to eight while the call is about one wave of CTAs (four an SM) and each
+  // still has 2048 entries
+  int ctas = kMaxCtas;
+  while (ctas > 1 && (static_cast<int64_t>(ctas) * batch > 608 || static_cast<int64_t>(ctas) * 2048 > vocab)) ctas /= 2;
+  if (static_cast<int64_t>(ctas) * batch > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas * batch));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_tokens_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
