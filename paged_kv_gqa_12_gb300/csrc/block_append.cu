@@ -7,15 +7,17 @@
 // touch can hold older ones.
 //
 // The call reads 2 bytes and writes 1 an element, an HBM stream; but the scale is
-// known only when all of a (page, head) has been seen, so its new rows are held in
-// registers (GT threads with NV vectors of 8 elements cover page_size rows of one
-// head) from the one read to the quantisation.  The groups that touch a page are
-// found without a prefix sum: request b with first row q_b has at most
-// floor(q_b / ps) + 2 b groups of pages before it, so group j looks for the last b
-// with that number <= j, and a few groups stay idle.
+// known only when all new rows of a (page, head) have been seen.  GT threads take one
+// (page, head, K or V), GT * 8 vectors of 8 elements at a time, which stay in
+// registers until they are quantised; where a page brings more rows than that they
+// are read again (from L2).  The groups that touch a page are found without a prefix
+// sum: request b with first row q_b has at most floor(q_b / ps) + 2 b pages before
+// it, so page number j of the call belongs to the last b with that number <= j, and
+// some groups stay idle.
 //
-// Quotients are rounded exactly (ties to even): the fp32 quotient is made odd where
-// it is inexact, which no tie of 8-bit codes survives, and rounds on to the code.
+// Codes are those of the exact quotient (ties to even).  x * (1 / scale) in fp32 is at
+// most 2^-23 of it off, which decides the code unless a midpoint h of two codes lies
+// that close; then the sign of the remainder x - h scale does, which one fma has exactly.
 #include <cstdint>
 
 #include <cuda_fp8.h>
@@ -35,7 +37,7 @@ struct BlockAppendParams {
   int64_t new_stride_tok, new_stride_head;
   uint8_t* cache[2];
   int64_t stride_page, stride_tok, stride_head;   // bytes
-  int num_pages, num_kv_heads;
+  int num_pages, num_kv_heads, ps_log2;
   float* scales[2];
   int64_t scale_stride;
   const int32_t* block_table;
@@ -46,27 +48,6 @@ struct BlockAppendParams {
   int batch, num_tokens;
   uint32_t* err;
 };
-
-// x / s for s > 0 in fp32, rounded to odd: where it is inexact and the rounded
-// quotient even, its neighbour on the exact quotient's side.  (The remainder of a
-// rounded quotient is exact in an fma, or has the exact one's sign.)
-__device__ __forceinline__ float quotient_odd(float x, float s) {
-  const float q = __fdiv_rn(x, s);
-  const float r = fmaf(-q, s, x);
-  const int bits = __float_as_int(q);
-  if ((bits & 1) == 0 && q != 0.f) {
-    const bool out = q > 0.f ? r > 0.f : r < 0.f;      // the exact quotient is larger in magnitude
-    const bool in = q > 0.f ? r < 0.f : r > 0.f;
-    return __int_as_float(bits + (out ? 1 : 0) - (in ? 1 : 0));
-  }
-  return q;
-}
-
-// (fp32 rounded to odd of a 64-bit number)
-__device__ __forceinline__ float odd_of(double q) {
-  const float f = __double2float_rz(q);
-  return static_cast<double>(f) != q ? __int_as_float(__float_as_int(f) | 1) : f;
-}
 
 template <bool I8>
 __device__ __forceinline__ uint32_t two_codes(float lo, float hi) {
@@ -80,183 +61,297 @@ __device__ __forceinline__ uint32_t two_codes(float lo, float hi) {
   }
 }
 
+// The number of code next to (hi + lo) / s, exactly, given t = hi * (1 / s) within 2^-23 of it;
+// infinities and NaN stay.
 template <bool I8>
-__device__ __forceinline__ uint2 quantise8(const uint4& w, float scale) {
+__device__ __forceinline__ float nearest_code(float t, float hi, float lo, float s) {
+  float below, above;                    // the codes around t
+  bool odd;                              // `below` is the odd one
+  if constexpr (I8) {
+    below = floorf(t);
+    above = below + 1.f;
+    odd = (static_cast<int>(below) & 1) != 0;
+  } else {
+    // magnitudes: subnormals are multiples of 2^-9, normals have three bits behind the first
+    const float a = fabsf(t);
+    float lower, step;
+    bool lower_odd;
+    if (a < 0x1p-6f) {
+      step = 0x1p-9f;
+      lower = floorf(a * 0x1p9f);
+      lower_odd = (static_cast<int>(lower) & 1) != 0;
+      lower *= step;
+    } else {
+      const uint32_t u = __float_as_uint(a);
+      lower = __uint_as_float(u & 0xfff00000u);
+      step = __uint_as_float((u & 0x7f800000u) - (3u << 23));
+      lower_odd = ((u >> 20) & 1u) != 0;
+    }
+    below = t < 0.f ? -(lower + step) : lower;
+    above = t < 0.f ? -lower : lower + step;
+    odd = t < 0.f ? !lower_odd : lower_odd;
+  }
+  const float h = 0.5f * (below + above);
+  const float r = fmaf(-h, s, hi) + lo;  // (both terms exact: hi is next to h s)
+  const float x = r > 0.f || (r == 0.f && odd) ? above : below;
+  return fabsf(hi) < INFINITY ? x : hi;
+}
+
+// Eight numbers x * was to codes, exactly (PRODUCT false: the numbers themselves).
+template <bool I8, bool PRODUCT>
+__device__ __forceinline__ uint2 careful8(const float (&x)[8], float m, float was, float s) {
+  float f[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float hi = PRODUCT ? __fmul_rn(x[k], was) : x[k];
+    const float lo = PRODUCT ? __fmaf_rn(x[k], was, -hi) : 0.f;
+    f[k] = nearest_code<I8>(x[k] * m, hi, lo, s);
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = two_codes<I8>(f[2 * k], f[2 * k + 1]);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Eight finite numbers to the codes next to x * m; `close` where one may lie on the other
+// side of a midpoint than the exact quotient that m stands for.
+template <bool I8>
+__device__ __forceinline__ uint2 to_codes8(const float (&x)[8], float m, bool& close) {
+  float t[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t[k] = x[k] * m;
+  uint2 out;
+  if constexpr (I8) {
+    // 1.5 * 2^23 added and taken off rounds to a whole number, whose two's complement is the sum's low byte
+    constexpr float kRound = 12582912.f;
+    uint32_t s[8];
+    float away = 0.f;                    // farthest from a whole number: errors are at most 127 * 2^-23 < 2^-16
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float r = __fadd_rn(t[k], kRound);
+      s[k] = __float_as_uint(r);
+      away = fmaxf(away, fabsf(__fsub_rn(t[k], __fsub_rn(r, kRound))));
+    }
+    close = away > 0.5f - 0x1p-15f;
+    out.x = __byte_perm(__byte_perm(s[0], s[1], 0x0040), __byte_perm(s[2], s[3], 0x0040), 0x5410);
+    out.y = __byte_perm(__byte_perm(s[4], s[5], 0x0040), __byte_perm(s[6], s[7], 0x0040), 0x5410);
+  } else {
+    // a midpoint of e4m3's normals has 1 and nineteen 0 behind the third bit of the significand; within two steps of
+    // it, or among the subnormals (below 2^-6, 0 apart), the quotient is taken again
+    uint32_t near = 0xffffffffu, least = 0xffffffffu;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t u = __float_as_uint(t[k]);
+      near = min(near, (u - 0x7fffeu) & 0xfffffu);
+      least = min(least, (u << 1) - 1u);            // (0 becomes the largest)
+    }
+    close = near <= 4u || least < (0x3c800000u << 1) - 1u;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = __nv_cvt_float2_to_fp8x2(make_float2(t[2 * k], t[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+    out = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  }
+  return out;
+}
+
+__device__ __forceinline__ void widen8(const uint4& w, float (&x)[8]) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-  uint32_t out[2] = {0u, 0u};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    float lo = __uint_as_float(in[k] << 16), hi = __uint_as_float(in[k] & 0xffff0000u);
-    if (scale > 0.f) {                    // (0: every finite element is 0)
-      lo = quotient_odd(lo, scale);
-      hi = quotient_odd(hi, scale);
-    }
-    out[k >> 1] |= two_codes<I8>(lo, hi) << (16 * (k & 1));
-  }
-  return make_uint2(out[0], out[1]);
-}
-
-template <bool I8>
-__device__ __forceinline__ double code_value(uint32_t byte) {
-  if constexpr (I8) {
-    return static_cast<double>(static_cast<int>(static_cast<int8_t>(byte)));
-  } else {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
-    return static_cast<double>(__half2float(__half(h)));
+    x[2 * k] = __uint_as_float(in[k] << 16);
+    x[2 * k + 1] = __uint_as_float(in[k] & 0xffff0000u);
   }
 }
 
-// Eight codes under a larger scale.
 template <bool I8>
-__device__ __forceinline__ uint2 requantise8(uint2 w, float was, float scale) {
+__device__ __forceinline__ void code_values8(const uint2& w, float (&x)[8]) {
   const uint32_t in[2] = {w.x, w.y};
-  uint32_t out[2] = {0u, 0u};
-#pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t pair = in[k >> 1] >> (16 * (k & 1));
-    // (the product of an 8-bit and a 24-bit number is exact)
-    const double a = code_value<I8>(pair & 0xffu) * static_cast<double>(was);
-    const double b = code_value<I8>((pair >> 8) & 0xffu) * static_cast<double>(was);
-    out[k >> 1] |= two_codes<I8>(odd_of(a / static_cast<double>(scale)), odd_of(b / static_cast<double>(scale)))
-                   << (16 * (k & 1));
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t byte = (in[k >> 2] >> (8 * (k & 3))) & 0xffu;
+    if constexpr (I8) {
+      x[k] = static_cast<float>(static_cast<int>(static_cast<int8_t>(byte)));
+    } else {
+      x[k] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
+    }
   }
-  return make_uint2(out[0], out[1]);
 }
 
-// GT threads a (page, kv head, K or V), NV vectors of 8 elements each.
-template <int D, bool I8, int GT, int NV>
-__global__ void __launch_bounds__(kCta) block_append_kernel(const BlockAppendParams p) {
+// The largest finite magnitude (bf16 bits) and the largest of all, of eight elements.
+__device__ __forceinline__ void most_of(const uint4& w, uint32_t& finite, uint32_t& any) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = in[k] & 0x7fffu, hi = (in[k] >> 16) & 0x7fffu;
+    any = max(any, max(lo, hi));
+    finite = max(finite, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+  }
+}
+
+// GT threads a (page, kv head, K or V).
+template <int D, bool I8, int GT>
+__global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppendParams p) {
+  constexpr int NV = 8;                    // vectors a thread holds
   constexpr int DV = D / 8;                // vectors a row
-  constexpr int PS = GT * NV / DV;         // page size
-  constexpr int RPS = GT / DV;             // rows a step of the group (GT >= DV)
-  static_assert(GT % 32 == 0 && GT % DV == 0 && PS * DV == GT * NV, "a group covers whole rows");
-  __shared__ uint32_t s_most[kCta / 32];
+  constexpr int RPS = GT / DV;             // rows a step of the group
+  constexpr int ROWS = RPS * NV;           // rows the group holds
+  static_assert(GT % 32 == 0 && GT % DV == 0, "a step covers whole rows");
+  __shared__ uint32_t s_most[2][kCta / 32];
+  const int lane = threadIdx.x & 31;
   const int lt = threadIdx.x % GT;
-  const int64_t group = static_cast<int64_t>(blockIdx.x) * (kCta / GT) + threadIdx.x / GT;
-  const int h = static_cast<int>(group % p.num_kv_heads);
-  const int64_t rest = group / p.num_kv_heads;
-  const int kv = static_cast<int>(rest & 1);
-  const int64_t item = rest >> 1;
+  const int ps_log2 = p.ps_log2;
+  const int ps = 1 << ps_log2;
+  const uint32_t group = blockIdx.x * (kCta / GT) + threadIdx.x / GT;
+  const uint32_t nh = static_cast<uint32_t>(p.num_kv_heads);
+  const uint32_t half = group / nh;
+  const int h = static_cast<int>(group - half * nh);
+  const int kv = static_cast<int>(half & 1);
+  const int item = static_cast<int>(half >> 1);
 
   // ---- the request and its page ------------------------------------------
-  int b = 0, page = -1, first = 0, end = 0;    // new tokens lie in slots [first, end) of the page
-  int64_t row0 = 0;                            // packed row of slot 0
-  int at = 0;
-  if (p.qsl == nullptr) {
-    b = static_cast<int>(item);
-  } else {
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.qsl[mid] / PS + 2 * static_cast<int64_t>(mid) <= item) lo = mid;
-      else hi = mid;
+  int b = item;
+  if (p.qsl != nullptr) {
+    // 32 requests compared at a time
+    int lo = 0, n = p.batch;                          // the last one is in [lo, lo + n)
+    while (n > 1) {
+      const int step = (n + 31) >> 5;
+      const int at = lane * step;
+      const bool fits = at < n && (p.qsl[lo + at] >> ps_log2) + 2 * static_cast<int64_t>(lo + at) <= item;
+      const unsigned m = __ballot_sync(0xffffffffu, fits);
+      const int k = m != 0 ? 31 - __clz(m) : 0;
+      lo += k * step;
+      n = min(step, n - k * step);
     }
     b = lo;
   }
+  int page = -1, first = 0, end = 0;       // new tokens lie in slots [first, end) of the page
+  int64_t row0 = 0;                        // packed row of slot 0
   if (b < p.batch) {
     const int qs = p.qsl != nullptr ? p.qsl[b] : b;
     const int n = p.qsl != nullptr ? p.qsl[b + 1] - qs : 1;
     const int L = p.seq_lens[b];
-    const int64_t k = p.qsl != nullptr ? item - (qs / PS + 2 * static_cast<int64_t>(b)) : 0;
+    const int64_t k = p.qsl != nullptr ? item - ((qs >> ps_log2) + 2 * static_cast<int64_t>(b)) : 0;
     if (n != 0) {
-      if (n < 0 || L < n || L > static_cast<int64_t>(p.max_pages) * PS || qs < 0 ||
+      if (n < 0 || L < n || L > (static_cast<int64_t>(p.max_pages) << ps_log2) || qs < 0 ||
           static_cast<int64_t>(qs) + n > p.num_tokens) {
         if (p.err != nullptr && k == 0 && lt == 0) atomicOr(p.err, kErrCapacity);
-      } else if (k >= 0 && k <= n / PS + 1) {
+      } else if (k >= 0 && k <= (n >> ps_log2) + 1) {
         const int ctx = L - n;
-        at = ctx / PS + static_cast<int>(k);
-        if (static_cast<int64_t>(at) * PS < L) {
-          first = max(0, ctx - at * PS);
-          end = min(PS, L - at * PS);
-          row0 = static_cast<int64_t>(qs) + (static_cast<int64_t>(at) * PS - ctx);
+        const int at = (ctx >> ps_log2) + static_cast<int>(k);
+        const int64_t slot0 = static_cast<int64_t>(at) << ps_log2;
+        if (slot0 < L) {
+          first = static_cast<int>(max(int64_t{0}, ctx - slot0));
+          end = static_cast<int>(min(static_cast<int64_t>(ps), L - slot0));
+          row0 = static_cast<int64_t>(qs) + (slot0 - ctx);
           page = p.block_table[static_cast<int64_t>(b) * p.bt_stride + at];
-          if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-            if (p.err != nullptr && lt == 0) atomicOr(p.err, kErrPageId);
-            page = -1;
-          }
         }
       }
     }
   }
 
-  // ---- new rows and their largest value ------------------------------------
-  const int r0 = lt / DV;
+  // ---- new rows and their largest value (asked for before the page's id is looked at) ----
+  const int r0 = first + lt / DV;
   const int col = (lt % DV) * 8;
+  const uint16_t* src = p.x[kv] + row0 * p.new_stride_tok + static_cast<int64_t>(h) * p.new_stride_head + col;
+  const bool held = end - first <= ROWS;   // all rows at once
   uint4 x[NV];
-  uint32_t most = 0;
-  float was = 0.f;
-  if (page >= 0) {
-    const uint16_t* src = p.x[kv] + static_cast<int64_t>(h) * p.new_stride_head + col;
-    if (first > 0) was = p.scales[kv][static_cast<int64_t>(page) * p.scale_stride + h];
+  uint32_t finite = 0, any = 0;
+  for (int base = r0; base < end; base += ROWS) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int r = r0 + v * RPS;
-      x[v] = make_uint4(0, 0, 0, 0);
-      if (r >= first && r < end)
-        x[v] = *reinterpret_cast<const uint4*>(src + (row0 + r) * p.new_stride_tok);
+      const int r = base + v * RPS;
+      x[v] = r < end ? *reinterpret_cast<const uint4*>(src + r * p.new_stride_tok) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
-        if (lo < 0x7f80u) most = max(most, lo);      // infinities and NaN do not count
-        if (hi < 0x7f80u) most = max(most, hi);
-      }
-    }
+    for (int v = 0; v < NV; ++v) most_of(x[v], finite, any);
   }
-  most = __reduce_max_sync(0xffffffffu, most);
+  if (page >= 0 ? page >= p.num_pages : end > 0) {
+    if (p.err != nullptr && lt == 0) atomicOr(p.err, kErrPageId);
+    page = -1;
+  }
+  float was = 0.f;
+  if (page >= 0 && first > 0) was = p.scales[kv][static_cast<int64_t>(page) * p.scale_stride + h];
+  finite = __reduce_max_sync(0xffffffffu, finite);
+  any = __reduce_max_sync(0xffffffffu, any);
   if constexpr (GT > 32) {
-    if ((threadIdx.x & 31) == 0) s_most[threadIdx.x >> 5] = most;
+    if (lane == 0) {
+      s_most[0][threadIdx.x >> 5] = finite;
+      s_most[1][threadIdx.x >> 5] = any;
+    }
     __syncthreads();
     const int w0 = (threadIdx.x / GT) * (GT / 32);
 #pragma unroll
-    for (int w = 0; w < GT / 32; ++w) most = max(most, s_most[w0 + w]);
+    for (int w = 0; w < GT / 32; ++w) {
+      finite = max(finite, s_most[0][w0 + w]);
+      any = max(any, s_most[1][w0 + w]);
+    }
   }
   if (page < 0) return;
 
   // ---- scale, codes ----------------------------------------------------------
-  const float fresh = __fdiv_rn(__uint_as_float(most << 16), I8 ? 127.f : 448.f);
+  const float fresh = __fdiv_rn(__uint_as_float(finite << 16), I8 ? 127.f : 448.f);
   const float scale = fmaxf(fresh, was);
   uint8_t* dst = p.cache[kv] + static_cast<int64_t>(page) * p.stride_page + static_cast<int64_t>(h) * p.stride_head + col;
+  // a scale next to the smallest numbers, and what it divides, times 2^80 (exact); scale 0: all finite elements are 0
+  const float lift = scale < 0x1p-60f ? 0x1p80f : 1.f;
+  const float s = scale > 0.f ? scale * lift : 1.f;
   if (first > 0 && scale > was) {
-#pragma unroll 1
-    for (int r = r0; r < first; r += RPS) {
+    const float wl = was * lift;
+    const float m = __fdiv_rn(wl, s);
+    for (int r = lt / DV; r < first; r += RPS) {
       uint2* w = reinterpret_cast<uint2*>(dst + r * p.stride_tok);
-      *w = requantise8<I8>(*w, was, scale);
+      float c[8];
+      code_values8<I8>(*w, c);
+      bool close;
+      uint2 out = to_codes8<I8>(c, m, close);
+      if (close) out = careful8<I8, true>(c, m, wl, s);
+      *w = out;
     }
   }
+  const float m = __frcp_rn(s);
+  const bool odd = any >= 0x7f80u;         // infinities or NaN
+  for (int base = r0; base < end; base += ROWS) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int r = r0 + v * RPS;
-    if (r >= first && r < end) *reinterpret_cast<uint2*>(dst + r * p.stride_tok) = quantise8<I8>(x[v], scale);
+    for (int v = 0; v < NV; ++v) {
+      const int r = base + v * RPS;
+      if (r < end) {
+        const uint4 w = held ? x[v] : *reinterpret_cast<const uint4*>(src + r * p.new_stride_tok);
+        float f[8];
+        widen8(w, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= lift;
+        bool close;
+        uint2 out = to_codes8<I8>(f, m, close);
+        if (close || odd) out = careful8<I8, false>(f, m, 1.f, s);
+        *reinterpret_cast<uint2*>(dst + r * p.stride_tok) = out;
+      }
+    }
   }
   if (lt == 0) p.scales[kv][static_cast<int64_t>(page) * p.scale_stride + h] = scale;
 }
 
+// Threads a group: as many as hold the rows a page gets on average (at most all of a
+// page's, at least a warp).
 template <int D, bool I8>
-cudaError_t launch(int page_size, const BlockAppendParams& p, int64_t items, cudaStream_t st) {
-  // threads a group: 8 vectors each, at least a warp
+cudaError_t launch(const BlockAppendParams& p, int64_t items, cudaStream_t st) {
   const int64_t groups = items * 2 * p.num_kv_heads;
-#define PA_APPEND(GT, NV)                                                                  \
-  block_append_kernel<D, I8, GT, NV>                                                       \
-      <<<static_cast<unsigned>((groups + kCta / GT - 1) / (kCta / GT)), kCta, 0, st>>>(p); \
-  return cudaGetLastError()
-  if constexpr (D == 64) {
-    if (page_size == 16) { PA_APPEND(32, 4); }
-    if (page_size == 32) { PA_APPEND(32, 8); }
-    PA_APPEND(64, 8);
-  } else if constexpr (D == 128) {
-    if (page_size == 16) { PA_APPEND(32, 8); }
-    if (page_size == 32) { PA_APPEND(64, 8); }
-    PA_APPEND(128, 8);
+  const int64_t mean = (static_cast<int64_t>(p.num_tokens) + p.batch - 1) / p.batch;
+  const int rows = static_cast<int>(mean < (1 << p.ps_log2) ? mean : 1 << p.ps_log2);
+  const int threads = rows * (D / 8) / 8;
+#define PA_APPEND(GT) \
+  block_append_kernel<D, I8, GT><<<static_cast<unsigned>((groups + kCta / GT - 1) / (kCta / GT)), kCta, 0, st>>>(p)
+  if (threads <= 32) {
+    PA_APPEND(32);
+  } else if (threads <= 64) {
+    PA_APPEND(64);
+  } else if (D == 64 || threads <= 128) {
+    PA_APPEND(128);
   } else {
-    if (page_size == 16) { PA_APPEND(64, 8); }
-    if (page_size == 32) { PA_APPEND(128, 8); }
-    PA_APPEND(256, 8);
+    PA_APPEND(256);
   }
 #undef PA_APPEND
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -307,6 +402,7 @@ extern "C" pa_status pa_append_blocks(const void* k_new, const void* v_new, int6
   p.stride_head = kv_stride_head;
   p.num_pages = num_pages;
   p.num_kv_heads = num_kv_heads;
+  p.ps_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : 6;
   p.scales[0] = k_scales;
   p.scales[1] = v_scales;
   p.scale_stride = scale_stride;
@@ -322,9 +418,9 @@ extern "C" pa_status pa_append_blocks(const void* k_new, const void* v_new, int6
   const bool i8 = code == PA_CODE_INT8;
   cudaError_t e;
   switch (head_dim) {
-    case 64: e = i8 ? launch<64, true>(page_size, p, items, st) : launch<64, false>(page_size, p, items, st); break;
-    case 128: e = i8 ? launch<128, true>(page_size, p, items, st) : launch<128, false>(page_size, p, items, st); break;
-    default: e = i8 ? launch<256, true>(page_size, p, items, st) : launch<256, false>(page_size, p, items, st); break;
+    case 64: e = i8 ? launch<64, true>(p, items, st) : launch<64, false>(p, items, st); break;
+    case 128: e = i8 ? launch<128, true>(p, items, st) : launch<128, false>(p, items, st); break;
+    default: e = i8 ? launch<256, true>(p, items, st) : launch<256, false>(p, items, st); break;
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -8,12 +8,14 @@
 // by the latency of its steps.
 //
 // Which v the sum crosses at depends on sums next to a border: in 32 bits a row of
-// 10^5 entries has errors of the order of an entry.  The difference p - q and the
-// sums are therefore pairs of floats (Knuth's two-sum, Dekker's pairs: about 48 bits
-// at the fp32 rate; the card adds 64-bit numbers 64 times slower), joined in 64 bits.
-// A request has a cluster of CTAs: every warp sums a contiguous part of the row,
-// the parts' sums go to all CTAs over distributed shared memory, and the CTA whose
-// warp holds the crossing sums that part again, a few entries a thread.
+// 10^5 entries has errors of the order of an entry.  The differences p - q and all
+// sums are therefore pairs of floats (Knuth's two-sum, Dekker's pairs: about 47 bits).
+// The card adds 64-bit numbers 64 times slower than floats: with the sums over lanes
+// and parts in 64 bits the call of 64 rows of 131072 entries took 44 us.
+//
+// A request has a cluster of CTAs: every warp sums a contiguous part of the row, the
+// parts' sums go to all CTAs over distributed shared memory, and the CTA whose warp
+// holds the crossing sums that part again, a few entries a thread.
 #include <cstdint>
 
 #include <cooperative_groups.h>
@@ -27,10 +29,11 @@ namespace cg = cooperative_groups;
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;             // CTAs a request (portable cluster size)
 constexpr int kUnit = 128;              // entries a warp takes at a time
+constexpr unsigned kAll = 0xffffffffu;
 
 struct VerifyParams {
   const int32_t* tokens;
@@ -50,7 +53,7 @@ struct VerifyParams {
   uint32_t* err;
 };
 
-// A sum held as two floats, hi + lo.
+// A number held as two floats, hi + lo.
 struct Pair {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float y) {
@@ -59,8 +62,50 @@ struct Pair {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(y, t)));
     hi = s;
   }
-  __device__ __forceinline__ double value() const { return static_cast<double>(hi) + static_cast<double>(lo); }
+  __device__ __forceinline__ void add(const Pair& y) {
+    add(y.hi);
+    lo = __fadd_rn(lo, y.lo);
+  }
+  // lo at most half a step of hi: pairs then compare by hi first
+  __device__ __forceinline__ Pair normal() const {
+    Pair r;
+    r.hi = __fadd_rn(hi, lo);
+    r.lo = __fsub_rn(lo, __fsub_rn(r.hi, hi));
+    return r;
+  }
+  __device__ __forceinline__ bool above(const Pair& y) const {
+    const Pair a = normal(), b = y.normal();
+    return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
+  }
+  __device__ __forceinline__ Pair from(unsigned m, int lane) const {
+    Pair r;
+    r.hi = __shfl_sync(m, hi, lane);
+    r.lo = __shfl_sync(m, lo, lane);
+    return r;
+  }
+  __device__ __forceinline__ Pair up(int n) const {
+    Pair r;
+    r.hi = __shfl_up_sync(kAll, hi, n);
+    r.lo = __shfl_up_sync(kAll, lo, n);
+    return r;
+  }
+  __device__ __forceinline__ Pair minus() const {
+    Pair r;
+    r.hi = -hi;
+    r.lo = -lo;
+    return r;
+  }
 };
+
+// The running sum over the lanes, this one's included.
+__device__ __forceinline__ Pair lane_sums(Pair x, int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const Pair y = x.up(m);
+    if (lane >= m) x.add(y);
+  }
+  return x;
+}
 
 // NaN and what is below 0 count as 0; the bound keeps sums of 2^20 entries finite.
 __device__ __forceinline__ float weight(float x) { return fminf(fmaxf(x, 0.f), 0x1p100f); }
@@ -71,7 +116,8 @@ struct Row {
   const float* q;       // null: nothing is taken off
   int taken;            // the certain draft whose entry loses 1, or -1
 
-  __device__ __forceinline__ void add(Pair& sum, float pv, float qv, int v) const {
+  // adds y of entry v; whether it weighs anything
+  __device__ __forceinline__ bool add(Pair& sum, float pv, float qv, int v) const {
     pv = weight(pv);
     qv = q != nullptr ? weight(qv) : (v == taken ? 1.f : 0.f);
     const float d = __fsub_rn(pv, qv);
@@ -80,20 +126,16 @@ struct Row {
       sum.add(d);
       sum.lo = __fadd_rn(sum.lo, __fsub_rn(__fsub_rn(pv, __fsub_rn(d, t)), __fadd_rn(qv, t)));
     }
-  }
-  __device__ __forceinline__ double y(int v) const {
-    const double pv = weight(p[v]);
-    const double d = pv - (q != nullptr ? static_cast<double>(weight(q[v])) : (v == taken ? 1.0 : 0.0));
-    return d > 0.0 ? d : 0.0;
+    return d > 0.f;
   }
 };
 
-__global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ double s_part[2][kMaxCtas * kWarps];   // sums of the parts, all of the cluster
-  __shared__ double s_scan[kWarps];
-  __shared__ int s_kept;
-  __shared__ int s_best;
+  __shared__ float2 s_part[2][kMaxCtas * kWarps];   // sums of the parts, all of the cluster
+  __shared__ float2 s_scan[kWarps];
+  __shared__ float2 s_rest;
+  __shared__ int s_kept, s_mine, s_best, s_last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
@@ -157,10 +199,6 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const VerifyPar
   const int units = (p.vocab + kUnit - 1) / kUnit;
   const int parts = C * kWarps;
   auto part_begin = [&](int w) { return static_cast<int>(static_cast<int64_t>(units) * w / parts) * kUnit; };
-  const double w01 = p.sample_u[b];
-  double total = 0.0;
-  int mine = -1;          // the part that holds the crossing
-  double rest = 0.0;      // how far into it the crossing lies
   for (int pass = 0; pass < 2; ++pass) {
     Pair sum;
     const int v1 = min(part_begin(rank * kWarps + warp + 1), p.vocab);
@@ -186,112 +224,130 @@ __global__ void __launch_bounds__(kThreads) verify_tokens_kernel(const VerifyPar
         }
       }
     }
-#pragma unroll 8
+#pragma unroll 4
     for (v += lane; v < v1; v += 32) row.add(sum, __ldg(row.p + v), row.q != nullptr ? __ldg(row.q + v) : 0.f, v);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
-      const float hi = __shfl_xor_sync(0xffffffffu, sum.hi, m), lo = __shfl_xor_sync(0xffffffffu, sum.lo, m);
-      sum.add(hi);
-      sum.lo = __fadd_rn(sum.lo, lo);
+      Pair y;
+      y.hi = __shfl_xor_sync(kAll, sum.hi, m);
+      y.lo = __shfl_xor_sync(kAll, sum.lo, m);
+      sum.add(y);
     }
+    sum = sum.from(kAll, 0);
     if (pass == 0) cluster.barrier_wait();
-    if (lane < C) *cluster.map_shared_rank(&s_part[pass][rank * kWarps + warp], lane) = sum.value();
+    if (lane < C) *cluster.map_shared_rank(&s_part[pass][rank * kWarps + warp], lane) = make_float2(sum.hi, sum.lo);
     cluster.sync();
 
-    // every warp for itself: the total, and the part whose running sum first exceeds w * total
-    double part[kMaxCtas * kWarps / 32];
-    double own = 0.0;
+    // the total, and the part whose running sum first exceeds w * total
+    if (warp == 0) {
+      constexpr int K = kMaxCtas * kWarps / 32;
+      Pair part[K], own;
 #pragma unroll
-    for (int k = 0; k < kMaxCtas * kWarps / 32; ++k) {
-      const int i = lane * (kMaxCtas * kWarps / 32) + k;
-      part[k] = i < parts ? s_part[pass][i] : 0.0;
-      own += part[k];
-    }
-    double incl = own;
+      for (int k = 0; k < K; ++k) {
+        if (lane * K + k < parts) {
+          const float2 x = s_part[pass][lane * K + k];
+          part[k].hi = x.x;
+          part[k].lo = x.y;
+        }
+        own.add(part[k]);
+      }
+      const Pair incl = lane_sums(own, lane);
+      const Pair total = incl.from(kAll, 31).normal();
+      int mine = -1;
+      Pair rest;
+      if (total.hi > 0.f) {
+        const float w = p.sample_u[b];
+        Pair target;                     // w * total: the product of the upper parts exactly
+        target.hi = __fmul_rn(w, total.hi);
+        target.lo = __fmaf_rn(w, total.lo, __fmaf_rn(w, total.hi, -target.hi));
+        Pair before = incl.up(1);
+        if (lane == 0) before = Pair();
+        int found = -1, last = -1;       // last: where rounding leaves the sum short of the target
+        Pair left;
 #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const double t = __shfl_up_sync(0xffffffffu, incl, m);
-      if (lane >= m) incl += t;
-    }
-    total = __shfl_sync(0xffffffffu, incl, 31);
-    if (total > 0.0) {
-      const double target = w01 * total;
-      double before = __shfl_up_sync(0xffffffffu, incl, 1);
-      if (lane == 0) before = 0.0;
-      int found = -1;
-      double left = 0.0;
-      int last = -1;       // the last part that weighs anything: where rounding leaves the sum short of the target
-#pragma unroll
-      for (int k = 0; k < kMaxCtas * kWarps / 32; ++k) {
-        if (part[k] > 0.0) {
-          last = lane * (kMaxCtas * kWarps / 32) + k;
-          if (found < 0 && before + part[k] > target) {
-            found = last;
-            left = target - before;
+        for (int k = 0; k < K; ++k) {
+          if (part[k].hi > 0.f) {
+            last = lane * K + k;
+            Pair to = before;
+            to.add(part[k]);
+            if (found < 0 && to.above(target)) {
+              found = last;
+              left = target;
+              left.add(before.minus());
+            }
+            before = to;
           }
         }
-        before += part[k];
+        const unsigned m = __ballot_sync(kAll, found >= 0);
+        if (m != 0) {
+          mine = __shfl_sync(kAll, found, __ffs(m) - 1);
+          rest = left.from(kAll, __ffs(m) - 1);
+        } else {
+          mine = __reduce_max_sync(kAll, last);
+          rest = total;
+        }
       }
-      const unsigned m = __ballot_sync(0xffffffffu, found >= 0);
-      if (m != 0) {
-        mine = __shfl_sync(0xffffffffu, found, __ffs(m) - 1);
-        rest = __shfl_sync(0xffffffffu, left, __ffs(m) - 1);
-      } else {
-        mine = __reduce_max_sync(0xffffffffu, last);
-        rest = total;
+      if (lane == 0) {
+        s_mine = mine;
+        s_rest = make_float2(rest.hi, rest.lo);
+        s_best = 0x7fffffff;
+        s_last = -1;
       }
-      break;
     }
-    if (row.q == nullptr && row.taken < 0) break;     // nothing to draw from
-    row.q = nullptr;                                  // p <= q everywhere: from p itself
+    __syncthreads();
+    if (s_mine >= 0 || (row.q == nullptr && row.taken < 0)) break;      // found, or nothing to draw from
+    row.q = nullptr;                                                    // p <= q everywhere: from p itself
     row.taken = -1;
   }
+  const int mine = s_mine;
   if (mine < 0) {
     if (rank == 0 && tid == 0) out[kept] = -1;
     return;
   }
   if (mine / kWarps != rank) return;
 
-  // ---- the entry, within the part --------------------------------------------
+  // ---- the entry, within the part: some consecutive ones a thread ---------------
+  Pair rest;
+  rest.hi = s_rest.x;
+  rest.lo = s_rest.y;
   const int v0 = part_begin(mine), v1 = min(part_begin(mine + 1), p.vocab);
   const int per = (v1 - v0 + kThreads - 1) / kThreads;
   const int a0 = min(v0 + tid * per, v1), a1 = min(a0 + per, v1);
-  double own = 0.0;
+  Pair own;
   int last = -1;
+#pragma unroll 4
   for (int v = a0; v < a1; ++v) {
-    const double y = row.y(v);
-    if (y > 0.0) last = v;
-    own += y;
+    if (row.add(own, row.p[v], row.q != nullptr ? row.q[v] : 0.f, v)) last = v;
   }
-  double incl = own;
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const double t = __shfl_up_sync(0xffffffffu, incl, m);
-    if (lane >= m) incl += t;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  if (tid == 0) s_best = 0x7fffffff;
+  const Pair incl = lane_sums(own, lane);
+  if (lane == 31) s_scan[warp] = make_float2(incl.hi, incl.lo);
   __syncthreads();
-  double before = incl - own;
-  for (int w = 0; w < warp; ++w) before += s_scan[w];
+  Pair before = incl.up(1);
+  if (lane == 0) before = Pair();
+  for (int w = 0; w < warp; ++w) {
+    Pair y;
+    y.hi = s_scan[w].x;
+    y.lo = s_scan[w].y;
+    before.add(y);
+  }
+  Pair to = before;
+  to.add(own);
+  if (last >= 0) {
+    atomicMax(&s_last, last);
+    if (to.above(rest)) atomicMin(&s_best, tid);
+  }
+  __syncthreads();
   // the first thread whose running sum exceeds the rest; none (rounding): the last entry that weighs
-  if (own > 0.0 && before + own > rest) atomicMin(&s_best, tid);
-  __syncthreads();
-  if (s_best == 0x7fffffff) {
-    __syncthreads();
-    if (tid == 0) s_best = -1;
-    __syncthreads();
-    atomicMax(&s_best, last);
-    __syncthreads();
-    if (tid == 0) out[kept] = s_best;
-    return;
-  }
-  if (tid == s_best) {
+  const int best = s_best;
+  if (best == 0x7fffffff) {
+    if (tid == 0) out[kept] = s_last;
+  } else if (tid == best) {
     int pick = last;
     for (int v = a0; v < a1; ++v) {
-      const double y = row.y(v);
-      before += y;
-      if (y > 0.0 && before > rest) {
+      Pair y;
+      const bool any = row.add(y, row.p[v], row.q != nullptr ? row.q[v] : 0.f, v);
+      before.add(y);
+      if (any && before.above(rest)) {
         pick = v;
         break;
       }
