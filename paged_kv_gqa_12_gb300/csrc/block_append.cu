@@ -15,14 +15,16 @@
 // it, so page number j of the call belongs to the last b with that number <= j, and
 // some groups stay idle.
 //
-// Codes are those of the exact quotient (ties to even).  x * (1 / scale) in fp32 is at
-// most 2^-23 of it off, which decides the code unless a midpoint h of two codes lies
-// that close; then the sign of the remainder x - h scale does, which one fma has exactly.
+// Codes are those of the exact quotient (ties to even).  It lies between x m (1 - 2^-22)
+// and x m (1 + 2^-22), m = 1 / scale in fp32; where both have one code, that is it.  Else
+// a midpoint h of two codes lies between, and the sign of the remainder x - h scale
+// decides, which one fma has exactly.
 #include <cstdint>
 
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "blocks.cuh"
 #include "pa.h"
 #include "pa_internal.h"
 #include "ptx.cuh"
@@ -113,44 +115,37 @@ __device__ __forceinline__ uint2 careful8(const float (&x)[8], float m, float wa
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// Eight finite numbers to the codes next to x * m; `close` where one may lie on the other
-// side of a midpoint than the exact quotient that m stands for.
+// Eight finite numbers (any, for e4m3) to the codes of x * m[0]; whether those of x * m[1] differ.
 template <bool I8>
-__device__ __forceinline__ uint2 to_codes8(const float (&x)[8], float m, bool& close) {
-  float t[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) t[k] = x[k] * m;
+__device__ __forceinline__ uint2 to_codes8(const float (&x)[8], const float (&m)[2], bool& differ) {
   uint2 out;
   if constexpr (I8) {
-    // 1.5 * 2^23 added and taken off rounds to a whole number, whose two's complement is the sum's low byte
-    constexpr float kRound = 12582912.f;
-    uint32_t s[8];
-    float away = 0.f;                    // farthest from a whole number: errors are at most 127 * 2^-23 < 2^-16
+    // x m + 1.5 * 2^23 rounds to a whole number, whose two's complement is the sum's low byte
+    const float2 round = make_float2(12582912.f, 12582912.f);
+    uint32_t s[8], off = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float r = __fadd_rn(t[k], kRound);
-      s[k] = __float_as_uint(r);
-      away = fmaxf(away, fabsf(__fsub_rn(t[k], __fsub_rn(r, kRound))));
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = make_float2(x[2 * k], x[2 * k + 1]);
+      const float2 a = __ffma2_rn(v, make_float2(m[0], m[0]), round);
+      const float2 c = __ffma2_rn(v, make_float2(m[1], m[1]), round);
+      s[2 * k] = __float_as_uint(a.x);
+      s[2 * k + 1] = __float_as_uint(a.y);
+      off |= (s[2 * k] ^ __float_as_uint(c.x)) | (s[2 * k + 1] ^ __float_as_uint(c.y));
     }
-    close = away > 0.5f - 0x1p-15f;
+    differ = off != 0;
     out.x = __byte_perm(__byte_perm(s[0], s[1], 0x0040), __byte_perm(s[2], s[3], 0x0040), 0x5410);
     out.y = __byte_perm(__byte_perm(s[4], s[5], 0x0040), __byte_perm(s[6], s[7], 0x0040), 0x5410);
   } else {
-    // a midpoint of e4m3's normals has 1 and nineteen 0 behind the third bit of the significand; within two steps of
-    // it, or among the subnormals (below 2^-6, 0 apart), the quotient is taken again
-    uint32_t near = 0xffffffffu, least = 0xffffffffu;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t u = __float_as_uint(t[k]);
-      near = min(near, (u - 0x7fffeu) & 0xfffffu);
-      least = min(least, (u << 1) - 1u);            // (0 becomes the largest)
-    }
-    close = near <= 4u || least < (0x3c800000u << 1) - 1u;
-    uint32_t w[4];
+    uint32_t w[2][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      w[k] = __nv_cvt_float2_to_fp8x2(make_float2(t[2 * k], t[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-    out = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 v = __fmul2_rn(make_float2(x[2 * k], x[2 * k + 1]), make_float2(m[i], m[i]));
+        w[i][k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+      }
+    out = make_uint2(w[0][0] | (w[0][1] << 16), w[0][2] | (w[0][3] << 16));
+    differ = out.x != (w[1][0] | (w[1][1] << 16)) || out.y != (w[1][2] | (w[1][3] << 16));
   }
   return out;
 }
@@ -168,25 +163,56 @@ template <bool I8>
 __device__ __forceinline__ void code_values8(const uint2& w, float (&x)[8]) {
   const uint32_t in[2] = {w.x, w.y};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t byte = (in[k >> 2] >> (8 * (k & 3))) & 0xffu;
+  for (int k = 0; k < 2; ++k) {
+    uint32_t h[2];
     if constexpr (I8) {
-      x[k] = static_cast<float>(static_cast<int>(static_cast<int8_t>(byte)));
+      h[0] = int8x2_to_f16x2<0x4140>(in[k] ^ 0x80808080u);
+      h[1] = int8x2_to_f16x2<0x4342>(in[k] ^ 0x80808080u);
     } else {
-      x[k] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3)));
+      h[0] = e4m3x2_to_f16x2<0>(in[k]);
+      h[1] = e4m3x2_to_f16x2<1>(in[k]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      x[4 * k + 2 * i] = f.x;
+      x[4 * k + 2 * i + 1] = f.y;
     }
   }
 }
 
-// The largest finite magnitude (bf16 bits) and the largest of all, of eight elements.
-__device__ __forceinline__ void most_of(const uint4& w, uint32_t& finite, uint32_t& any) {
+// The largest magnitudes (bf16 bits) of the even and the odd elements.
+__device__ __forceinline__ uint32_t most_of(const uint4& w, uint32_t most) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) most = __vmaxu2(most, in[k] & 0x7fff7fffu);
+  return most;
+}
+
+// The same of the finite elements.
+__device__ __forceinline__ uint32_t most_finite(const uint4& w, uint32_t most) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t lo = in[k] & 0x7fffu, hi = (in[k] >> 16) & 0x7fffu;
-    any = max(any, max(lo, hi));
-    finite = max(finite, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    const uint32_t lo = in[k] & 0x7fffu, hi = in[k] & 0x7fff0000u;
+    most = __vmaxu2(most, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
   }
+  return most;
+}
+
+// The larger half, over the group's threads (all threads of the CTA call it).
+template <int GT>
+__device__ __forceinline__ uint32_t group_most(uint32_t most, uint32_t* s_most) {
+  most = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+  if constexpr (GT > 32) {
+    __syncthreads();                       // (an earlier call's reads)
+    if ((threadIdx.x & 31) == 0) s_most[threadIdx.x >> 5] = most;
+    __syncthreads();
+    const int w0 = (threadIdx.x / GT) * (GT / 32);
+#pragma unroll
+    for (int w = 0; w < GT / 32; ++w) most = max(most, s_most[w0 + w]);
+  }
+  return most;
 }
 
 // GT threads a (page, kv head, K or V).
@@ -197,7 +223,7 @@ __global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppend
   constexpr int RPS = GT / DV;             // rows a step of the group
   constexpr int ROWS = RPS * NV;           // rows the group holds
   static_assert(GT % 32 == 0 && GT % DV == 0, "a step covers whole rows");
-  __shared__ uint32_t s_most[2][kCta / 32];
+  __shared__ uint32_t s_most[kCta / 32];
   const int lane = threadIdx.x & 31;
   const int lt = threadIdx.x % GT;
   const int ps_log2 = p.ps_log2;
@@ -253,18 +279,21 @@ __global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppend
   // ---- new rows and their largest value (asked for before the page's id is looked at) ----
   const int r0 = first + lt / DV;
   const int col = (lt % DV) * 8;
-  const uint16_t* src = p.x[kv] + row0 * p.new_stride_tok + static_cast<int64_t>(h) * p.new_stride_head + col;
+  const int64_t step = RPS * p.new_stride_tok;
+  const uint16_t* src = p.x[kv] + (row0 + r0) * p.new_stride_tok + static_cast<int64_t>(h) * p.new_stride_head + col;
   const bool held = end - first <= ROWS;   // all rows at once
   uint4 x[NV];
-  uint32_t finite = 0, any = 0;
+  auto load = [&](int base) {
+    const uint16_t* at = src + (base - r0) * p.new_stride_tok;
+#pragma unroll
+    for (int v = 0; v < NV; ++v, at += step)
+      x[v] = base + v * RPS < end ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+  };
+  uint32_t most = 0;
   for (int base = r0; base < end; base += ROWS) {
+    load(base);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int r = base + v * RPS;
-      x[v] = r < end ? *reinterpret_cast<const uint4*>(src + r * p.new_stride_tok) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int v = 0; v < NV; ++v) most_of(x[v], finite, any);
+    for (int v = 0; v < NV; ++v) most = most_of(x[v], most);
   }
   if (page >= 0 ? page >= p.num_pages : end > 0) {
     if (p.err != nullptr && lt == 0) atomicOr(p.err, kErrPageId);
@@ -272,25 +301,21 @@ __global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppend
   }
   float was = 0.f;
   if (page >= 0 && first > 0) was = p.scales[kv][static_cast<int64_t>(page) * p.scale_stride + h];
-  finite = __reduce_max_sync(0xffffffffu, finite);
-  any = __reduce_max_sync(0xffffffffu, any);
-  if constexpr (GT > 32) {
-    if (lane == 0) {
-      s_most[0][threadIdx.x >> 5] = finite;
-      s_most[1][threadIdx.x >> 5] = any;
-    }
-    __syncthreads();
-    const int w0 = (threadIdx.x / GT) * (GT / 32);
+  most = group_most<GT>(most, s_most);
+  const bool odd = most >= 0x7f80u;        // infinities or NaN, which do not count
+  if (GT > 32 ? __syncthreads_or(odd) : odd) {
+    most = 0;
+    for (int base = r0; base < end; base += ROWS) {
+      load(base);
 #pragma unroll
-    for (int w = 0; w < GT / 32; ++w) {
-      finite = max(finite, s_most[0][w0 + w]);
-      any = max(any, s_most[1][w0 + w]);
+      for (int v = 0; v < NV; ++v) most = most_finite(x[v], most);
     }
+    most = group_most<GT>(most, s_most);
   }
   if (page < 0) return;
 
   // ---- scale, codes ----------------------------------------------------------
-  const float fresh = __fdiv_rn(__uint_as_float(finite << 16), I8 ? 127.f : 448.f);
+  const float fresh = __fdiv_rn(__uint_as_float(most << 16), I8 ? 127.f : 448.f);
   const float scale = fmaxf(fresh, was);
   uint8_t* dst = p.cache[kv] + static_cast<int64_t>(page) * p.stride_page + static_cast<int64_t>(h) * p.stride_head + col;
   // a scale next to the smallest numbers, and what it divides, times 2^80 (exact); scale 0: all finite elements are 0
@@ -299,32 +324,36 @@ __global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppend
   if (first > 0 && scale > was) {
     const float wl = was * lift;
     const float m = __fdiv_rn(wl, s);
+    const float m2[2] = {m * (1.f + 0x1p-22f), m * (1.f - 0x1p-22f)};
     for (int r = lt / DV; r < first; r += RPS) {
       uint2* w = reinterpret_cast<uint2*>(dst + r * p.stride_tok);
       float c[8];
       code_values8<I8>(*w, c);
-      bool close;
-      uint2 out = to_codes8<I8>(c, m, close);
-      if (close) out = careful8<I8, true>(c, m, wl, s);
+      bool differ;
+      uint2 out = to_codes8<I8>(c, m2, differ);
+      if (differ) out = careful8<I8, true>(c, m, wl, s);
       *w = out;
     }
   }
   const float m = __frcp_rn(s);
-  const bool odd = any >= 0x7f80u;         // infinities or NaN
+  const float m2[2] = {m * (1.f + 0x1p-22f), m * (1.f - 0x1p-22f)};
+  const bool careful = (I8 && odd) || lift != 1.f;
   for (int base = r0; base < end; base += ROWS) {
+    if (!held) load(base);
+    uint8_t* to = dst + base * p.stride_tok;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int r = base + v * RPS;
-      if (r < end) {
-        const uint4 w = held ? x[v] : *reinterpret_cast<const uint4*>(src + r * p.new_stride_tok);
+    for (int v = 0; v < NV; ++v, to += RPS * p.stride_tok) {
+      if (base + v * RPS < end) {
         float f[8];
-        widen8(w, f);
+        widen8(x[v], f);
+        bool differ;
+        uint2 out = to_codes8<I8>(f, m2, differ);
+        if (differ || careful) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= lift;
-        bool close;
-        uint2 out = to_codes8<I8>(f, m, close);
-        if (close || odd) out = careful8<I8, false>(f, m, 1.f, s);
-        *reinterpret_cast<uint2*>(dst + r * p.stride_tok) = out;
+          for (int k = 0; k < 8; ++k) f[k] *= lift;
+          out = careful8<I8, false>(f, m, 1.f, s);
+        }
+        *reinterpret_cast<uint2*>(to) = out;
       }
     }
   }
