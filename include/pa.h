@@ -535,7 +535,7 @@ typedef struct {
   int32_t window;             /* sliding window W; 0 = off */
   int32_t has_sinks;          /* 1: calls pass a [Hq] fp32 sink logit array */
   float soft_cap;             /* 0 = off; else s = cap * tanh(s / cap) */
-  int32_t num_splits;         /* 0 = planner's choice, >0 = max KV splits per request (few rows) */
+  int32_t num_ctas;           /* few rows: CTAs that share the work; 0 = one wave of them */
   int32_t num_sms;            /* SMs to plan for; 0 = query the current device */
 } pa_block_shape;
 
@@ -545,17 +545,18 @@ typedef struct {
   int32_t chunked;            /* 0: split-KV kernel (few rows a request); 1: chunks of many rows on the
                                  tcgen05 kernel of pa_extend, over a 16-bit copy of the attended pages' codes */
   int32_t tile_tokens;        /* keys per pipeline stage */
-  int32_t split_tiles;        /* stages per KV split (0 when num_splits is fixed) */
-  int32_t max_splits;         /* largest split count a request can get */
-  int32_t row_groups;         /* CTAs of 16 rows (8 where one such CTA is enough) a kv head */
-  int32_t bt_cache;           /* block-table entries staged in shared memory per CTA */
+  int32_t min_tiles;          /* fewest stages that a CTA is given */
+  int32_t ctas;               /* CTAs that share the work, each an equal run of all requests' stages */
+  int32_t row_groups;         /* CTAs of 16 rows (8 where one such CTA is enough) a group of kv heads */
+  int32_t head_group;         /* kv heads a CTA takes */
   int32_t smem_bytes;         /* dynamic shared memory per CTA */
   int32_t group_requests;     /* chunked: requests copied and attended at a time */
   int64_t scratch_bytes;      /* device scratch the calls need (>= 65536, the header) */
   int32_t reserved[6];
 } pa_block_plan_t;
 
-/* Plan from capacities; host_seq_lens as for pa_plan (host memory, `batch` entries, or NULL). */
+/* Plan from capacities; host_seq_lens (host memory, `batch` entries, may be NULL) lets the planner take
+ * fewer CTAs where these lengths need fewer.  Any lengths within the capacities may be attended. */
 pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_lens, int32_t batch,
                         pa_block_plan_t* plan);
 

@@ -154,7 +154,7 @@ class PaBlockShape(ctypes.Structure):
         ("window", ctypes.c_int32),
         ("has_sinks", ctypes.c_int32),
         ("soft_cap", ctypes.c_float),
-        ("num_splits", ctypes.c_int32),
+        ("num_ctas", ctypes.c_int32),
         ("num_sms", ctypes.c_int32),
     ]
 
@@ -164,10 +164,10 @@ class PaBlockPlan(ctypes.Structure):
         ("shape", PaBlockShape),
         ("chunked", ctypes.c_int32),
         ("tile_tokens", ctypes.c_int32),
-        ("split_tiles", ctypes.c_int32),
-        ("max_splits", ctypes.c_int32),
+        ("min_tiles", ctypes.c_int32),
+        ("ctas", ctypes.c_int32),
         ("row_groups", ctypes.c_int32),
-        ("bt_cache", ctypes.c_int32),
+        ("head_group", ctypes.c_int32),
         ("smem_bytes", ctypes.c_int32),
         ("group_requests", ctypes.c_int32),
         ("scratch_bytes", ctypes.c_int64),
@@ -704,13 +704,13 @@ def append_blocks(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tabl
 
 def block_plan(*, num_q_heads: int, num_kv_heads: int, head_dim: int, page_size: int, code: int, max_batch: int,
                max_pages_per_seq: int, max_total_q: int, max_new: int = 1, window: int = 0, has_sinks: bool = False,
-               soft_cap: float = 0.0, num_splits: int = 0, num_sms: int = 0, host_seq_lens=None) -> PaBlockPlan:
+               soft_cap: float = 0.0, num_ctas: int = 0, num_sms: int = 0, host_seq_lens=None) -> PaBlockPlan:
     """pa_block_plan: the plan of block_attend.  ``max_new``: most query rows of a request; ``host_seq_lens``: optional
     host sequence of lengths."""
     s = PaBlockShape(num_q_heads=num_q_heads, num_kv_heads=num_kv_heads, head_dim=head_dim, page_size=page_size,
                      code=code, max_batch=max_batch, max_pages_per_seq=max_pages_per_seq, max_total_q=max_total_q,
                      max_new=max_new, window=window, has_sinks=1 if has_sinks else 0, soft_cap=soft_cap,
-                     num_splits=num_splits, num_sms=num_sms)
+                     num_ctas=num_ctas, num_sms=num_sms)
     p = PaBlockPlan()
     lens, n = None, 0
     if host_seq_lens is not None:

@@ -205,6 +205,27 @@ pa_status make_kv_map(CUtensorMap* map, const void* base, bool fp8, int D, int H
   });
 }
 
+// The same cache as bytes with the slots inside the kv heads: dims head_dim, slot, kv head, page, and a
+// box of `box_rows` slots of `heads` heads, which lands as [head][slot] rows.
+pa_status make_codes_map(CUtensorMap* map, const void* base, int D, int Hkv, int ps, int num_pages, int64_t st_page,
+                         int64_t st_tok, int64_t st_head, int box_rows, int heads) {
+  auto fn = encode_fn();
+  if (!fn) return PA_ERR_CUDA;
+  const int box_bytes = D < 128 ? D : 128;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(ps), static_cast<cuuint64_t>(Hkv),
+                        static_cast<cuuint64_t>(num_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st_tok), static_cast<cuuint64_t>(st_head),
+                           static_cast<cuuint64_t>(st_page)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows),
+                       static_cast<cuuint32_t>(heads), 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  const CUtensorMapSwizzle sw = box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  return encode_map([&] {
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
+}
+
 // 3-D tensor map over packed queries [rows, Hq, D] (bf16): dims head_dim,
 // q head, row; box 64 dims x `group` heads x `rows_per_box` rows, 128-byte
 // swizzle, so one box per 64-dim chunk lands as a [rows*group, 64] K-major tile.

@@ -15,14 +15,22 @@
 // power of two a row (largest value in [2^14, 2^15): exact to 2^-32 of it).
 //
 // The codes are read once from HBM, which bounds the kernel; per code it spends
-// about a quarter of the instructions that dequantising to bf16 takes.  A CTA is a
-// (split, kv head and group of up to 16 rows, request); its four warps take tiles
-// of TS keys in turn, each with a private ring of stages filled by TMA from the
-// pages.  S^T = K Q^T and O^T += V^T P^T keep the rows in the products' 8-wide
-// dimension.  ldmatrix brings four codes of a key (K), or two codes of two
-// neighbouring keys (V, transposed), into a register; which dims those are is a
-// fixed permutation that the q fragments and the output follow.  Splits are merged
-// by the CTA that finishes last, as in decode.
+// about a quarter of the instructions that dequantising to bf16 takes.  One wave of
+// CTAs shares all tiles (of a request, a group of HG kv heads and of up to 8 or 16
+// rows) evenly: a prefix sum over the requests gives each CTA its run of tiles, which
+// may end one request and begin the next.  W compute warps are HG heads x KW groups
+// of 16 keys of a tile; one more warp fetches a tile's codes, one TMA box for a page's
+// slots of all HG heads, a ring of stages ahead and across requests.  Parts of a
+// request that lie in several shares are merged by the CTA that is done last; what a
+// share costs once (prefix sum, q, merge) is why there is one wave.  (Every warp with a
+// ring and tiles of its own, equal splits of each request: 119 us for 64 requests of
+// up to 8192 tokens, 59 for one of 131071.)
+//
+// S^T = K Q^T and O^T += V^T P^T keep the rows in the products' 8-wide dimension.
+// ldmatrix brings four codes of a key (K), or two codes of two neighbouring keys (V,
+// transposed), into a register; which dims those are is a fixed permutation that the
+// q fragments and the output follow.  A page's scales wait in the lanes of the warp
+// that needs them, 32 pages at a time.
 //
 // Many rows a request (chunks): see "chunks" below.
 #include <algorithm>
@@ -35,14 +43,13 @@
 #include "extend.h"
 #include "pa.h"
 #include "pa_internal.h"
+#include "tcgen05.cuh"
 
 namespace pa {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMaxSmem = 232448;
 constexpr float kWeightBias = 14.f;           // weights are at most 2^14 (f16 holds 65504)
 constexpr float kLeastScale = 0x1p-100f;      // V scales below count as this one: its log2 and inverse are finite
 
@@ -64,84 +71,123 @@ struct BlockParams {
   uint16_t* out;
   int64_t out_stride_tok, out_stride_head;
   float* lse;
-  float* o_part;              // [total_q, Hq, max_splits, D] normalised split outputs
-  float* lse_part;            // [total_q, Hq, max_splits]
-  int max_splits, split_tiles, fixed_splits, bt_cache, row_groups;
-  uint32_t* merge_cnt;        // [batch, Hkv * row_groups] arrival counters
+  float* o_part;              // [2 grid][HG][HW][D] normalised parts of rows
+  float* lse_part;            // [2 grid][HG][HW] their LSEs, log2
+  int min_tiles;              // fewest tiles a CTA is given
+  int hg_log2;                // kv heads a CTA takes: 2^hg_log2
+  uint32_t* merge_cnt;        // [grid] arrivals at the (request, heads, rows) that begins in a CTA's share and ends beyond
   uint32_t* err;
 };
 
-// log2 of a V scale and its inverse, of the K scale: what a page's keys need.
-struct PageScale {
-  float k, v_log2, v_inv, pad;
-};
+// Compute warps a CTA, stages of its ring, CTAs an SM.
+template <int D, int NH8> struct Choice;
+template <> struct Choice<64, 1> { static constexpr int W = 8, NS = 4, CPS = 2; };
+template <> struct Choice<64, 2> { static constexpr int W = 4, NS = 4, CPS = 3; };
+template <> struct Choice<128, 1> { static constexpr int W = 4, NS = 3, CPS = 3; };
+template <> struct Choice<128, 2> { static constexpr int W = 4, NS = 2, CPS = 3; };
+template <> struct Choice<256, 1> { static constexpr int W = 4, NS = 2, CPS = 2; };
+template <> struct Choice<256, 2> { static constexpr int W = 4, NS = 4, CPS = 1; };
 
-template <int D, int NH8, int TS, int NS>
+template <int D, int NH8, int W, int NS>
 struct Traits {
   static constexpr int RB = D < 128 ? D : 128;      // bytes per TMA box row
   static constexpr int NCC = D / RB;                // column chunks per key row
-  static constexpr int TILE = TS * D;               // K (or V) bytes per stage
+  static constexpr int TILE = W * 16 * D;           // K (or V) bytes per stage
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int WARP_BYTES = NS * STAGE;
-  static constexpr int MT = TS / 16;
   static constexpr int KS = D / 16;                 // 16-code units per row
   static constexpr int HW = NH8 * 8;
+  static constexpr int THREADS = (W + 1) * 32;
+  static constexpr int STATES = W * HW * (D + 2) * 4;
+  static constexpr int SMEM = 1024 + NS * STAGE + STATES + 2 * NS * 8;
   static_assert(RB == 128 || RB == 64, "row bytes must use the 128B or 64B swizzle");
-  static_assert(WARP_BYTES >= HW * (D + 2) * 4, "a warp's final state fits in its ring");
 
-  // Byte offset of 16-byte unit `u` of key row `row` as TMA writes it.
+  // Byte offset of 16-byte unit `u` of a warp's key row `row` (0 .. 15) as TMA writes it; column
+  // chunks lie TILE / NCC apart.
   __device__ static __forceinline__ uint32_t unit(int row, int u) {
     constexpr int UPB = RB / 16;
-    const int cc = u / UPB;
     const uint32_t sw = (RB == 128) ? (row & 7) : ((row >> 1) & 3);
-    return static_cast<uint32_t>(cc * (TS * RB) + row * RB) + (((u % UPB) ^ sw) << 4);
+    return static_cast<uint32_t>((u / UPB) * (TILE / NCC) + row * RB) + (((u % UPB) ^ sw) << 4);
   }
 };
 
-struct Split {
-  int lo, hi;            // attended keys of the request [lo, hi)
-  int tile0, n_tiles, per, n;
+// What a request brings: its rows, the tiles of TS keys they attend to, and units = tiles x groups of
+// heads x groups of rows.
+struct Request {
+  int L, qs, n_new;
+  int lo, tile0, n_tiles;
+  int ys;                // groups of heads x groups of rows
 };
 
-__device__ __forceinline__ Split split_of(const BlockParams& p, int L, int n_new, int ts) {
-  Split r;
-  r.hi = L;
-  r.lo = p.window > 0 ? max(0, L - n_new - p.window + 1) : 0;
+// (false: a length or packing beyond the plan)
+__device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts, int hw, int hgroups, Request& r) {
+  r.L = p.seq_lens[b];
+  r.qs = p.qsl != nullptr ? p.qsl[b] : b;
+  r.n_new = p.qsl != nullptr ? p.qsl[b + 1] - r.qs : 1;
+  r.lo = r.tile0 = r.n_tiles = r.ys = 0;
+  if (r.n_new == 0) return true;
+  if (r.n_new < 0 || r.n_new > p.max_new || r.qs < 0 || static_cast<int64_t>(r.qs) + r.n_new > p.total_q || r.L < 0 ||
+      r.L > p.max_kv || (p.qsl != nullptr && r.L < r.n_new)) {
+    r.n_new = 0;
+    return false;
+  }
+  if (r.L == 0) return true;
+  r.lo = p.window > 0 ? max(0, r.L - r.n_new - p.window + 1) : 0;
   r.tile0 = r.lo / ts;
-  r.n_tiles = (r.hi + ts - 1) / ts - r.tile0;
-  r.per = p.fixed_splits > 0 ? (r.n_tiles + p.fixed_splits - 1) / p.fixed_splits : p.split_tiles;
-  r.n = (r.n_tiles + r.per - 1) / r.per;
-  r.per = (r.n_tiles + r.n - 1) / r.n;      // equal splits
-  r.n = (r.n_tiles + r.per - 1) / r.per;
-  return r;
+  r.n_tiles = (r.L + ts - 1) / ts - r.tile0;
+  r.ys = hgroups * ((r.n_new * p.group + hw - 1) / hw);
+  return true;
 }
 
-// Splits of the R rows of one group, merged by their LSEs: thread t takes 4
-// consecutive dims of one row, eight splits' loads in flight together.
-template <int D>
-__device__ __forceinline__ void merge_rows(const BlockParams& p, int n_splits, int R, int row0, int kvh, int64_t qs) {
+// All W compute warps of the CTA (the fetching warp does not take part).
+template <int W>
+__device__ __forceinline__ void compute_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
+}
+
+// Final value of four dims of a row: the sink, if any, joins the denominator.
+__device__ __forceinline__ void write_row(const BlockParams& p, int qs, int kvh, int row, int d, float4 v, float lse2) {
+  const int tq = row / p.group;
+  const int hq = kvh * p.group + (row - tq * p.group);
+  const int64_t orow = qs + tq;
+  if (p.sinks != nullptr) {
+    const float sk = p.sinks[hq] * kLog2e;
+    const float top = fmaxf(lse2, sk);
+    const float own = ex2(lse2 - top), z = own + ex2(sk - top);
+    const float f = own / z;
+    v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+    lse2 = top + lg2(z);
+  }
+  uint16_t* outp = p.out + orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head + d;
+  reinterpret_cast<uint32_t*>(outp)[0] = pack_bf16x2(v.x, v.y);     // (rows are 4-byte aligned)
+  reinterpret_cast<uint32_t*>(outp)[1] = pack_bf16x2(v.z, v.w);
+  if (d == 0 && p.lse != nullptr) p.lse[orow * p.num_q_heads + hq] = lse2 * kLn2;
+}
+
+// The n parts of the R rows of each of the heads of a group, merged by their LSEs: thread t
+// takes 4 consecutive dims of one row, eight parts' loads in flight together.  Part 0 lies at
+// place0, part i at place 2 (first + i).
+template <int D, int HW, int THREADS>
+__device__ __forceinline__ void merge_parts(const BlockParams& p, int place0, int first, int n, int R, int row0,
+                                            int kvh0, int heads, int qs) {
   constexpr int C = D / 4;
   constexpr int U = 8;
-  for (int e = threadIdx.x; e < R * C; e += kWarps * 32) {
-    const int rr = e / C;
-    const int d = (e - rr * C) * 4;
-    const int tq = (row0 + rr) / p.group;
-    const int hq = kvh * p.group + (row0 + rr - tq * p.group);
-    const int64_t orow = qs + tq;
-    const int64_t at = (orow * p.num_q_heads + hq) * p.max_splits;
-    const bool has_sink = p.sinks != nullptr;
-    float M = has_sink ? p.sinks[hq] * kLog2e : -INFINITY;
-    float Z = has_sink ? 1.f : 0.f;
+  for (int e = threadIdx.x; e < heads * R * C; e += THREADS) {
+    const int hr = e / C;
+    const int d = (e - hr * C) * 4;
+    const int head = hr / R;
+    const int rr = hr - head * R;
+    float M = -INFINITY, Z = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < n_splits; s0 += U) {
+    for (int s0 = 0; s0 < n; s0 += U) {
       float l[U];
       float4 o[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool ok = s0 + u < n_splits;
-        l[u] = ok ? __ldcg(p.lse_part + at + s0 + u) * kLog2e : -INFINITY;
-        o[u] = ok ? __ldcg(reinterpret_cast<const float4*>(p.o_part + (at + s0 + u) * D + d))
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool ok = s0 + u < n;
+        const int place = s0 + u == 0 ? place0 : 2 * (first + s0 + u);
+        const int64_t pa = (static_cast<int64_t>(place) * heads + head) * HW + rr;
+        l[u] = ok ? __ldcg(p.lse_part + pa) : -INFINITY;
+        o[u] = ok ? __ldcg(reinterpret_cast<const float4*>(p.o_part + pa * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float mx = l[0];
 #pragma unroll
@@ -154,236 +200,294 @@ __device__ __forceinline__ void merge_rows(const BlockParams& p, int n_splits, i
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (l[u] == -INFINITY) continue;      // padding, or a split with no key for this row
+        if (l[u] == -INFINITY) continue;      // padding, or a part with no key for this row
         const float w = ex2(l[u] - M);
         Z += w;
         acc.x += w * o[u].x; acc.y += w * o[u].y; acc.z += w * o[u].z; acc.w += w * o[u].w;
       }
     }
-    const float inv = Z > 0.f ? 1.f / Z : 0.f;
-    uint16_t* outp = p.out + orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head + d;
-    reinterpret_cast<uint32_t*>(outp)[0] = pack_bf16x2(acc.x * inv, acc.y * inv);
-    reinterpret_cast<uint32_t*>(outp)[1] = pack_bf16x2(acc.z * inv, acc.w * inv);
-    if (d == 0 && p.lse != nullptr)
-      p.lse[orow * p.num_q_heads + hq] = M == -INFINITY ? -INFINITY : (M + lg2(Z)) * kLn2;
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
+    write_row(p, qs, kvh0 + head, row0 + rr, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
+              Z == 0.f ? -INFINITY : M + lg2(Z));
   }
 }
 
-template <int D, bool I8, int NH8, int TS, int NS, bool CAP>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D, bool I8, int NH8, int W, int NS, bool CAP>
+__global__ void __launch_bounds__((W + 1) * 32, (Choice<D, NH8>::CPS))
 block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const BlockParams p) {
-  using T = Traits<D, NH8, TS, NS>;
-  const int split = blockIdx.x;
-  const int kvh = blockIdx.y / p.row_groups;
-  const int rg = blockIdx.y - kvh * p.row_groups;
-  const int b = blockIdx.z;
-  const int L = p.seq_lens[b];
-  const int qs = p.qsl != nullptr ? p.qsl[b] : b;
-  const int n_new = p.qsl != nullptr ? p.qsl[b + 1] - qs : 1;
+  using T = Traits<D, NH8, W, NS>;
+  const int HG = 1 << p.hg_log2;
+  const int KW = W >> p.hg_log2;                         // groups of 16 keys a stage
+  const int TS = 16 * KW;
+  const int hgroups = p.num_kv_heads >> p.hg_log2;
   const int G = p.group;
   const int tid = threadIdx.x;
-  const bool leads = tid == 0 && split == 0 && blockIdx.y == 0;
-  if (n_new == 0) return;
-  if (n_new < 0 || n_new > p.max_new || qs < 0 || static_cast<int64_t>(qs) + n_new > p.total_q || L < 0 ||
-      L > p.max_kv || (p.qsl != nullptr && L < n_new)) {
-    if (leads) atomicOr(p.err, kErrCapacity);
-    return;
-  }
-  const int row0 = rg * (NH8 * 8);                       // first (token, head) row of this CTA
-  const int R = min(n_new * G - row0, NH8 * 8);
-  if (R <= 0) return;
-  if (L == 0) {        // (decode of an empty request) no key: O = 0, LSE the sink's or -inf
-    if (split == 0)
-      for (int i = tid; i < R * D; i += kWarps * 32) {
-        const int rr = i / D, d = i - rr * D;
-        const int hq = kvh * G + row0 + rr;
-        p.out[static_cast<int64_t>(qs) * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head + d] = 0;
-        if (d == 0 && p.lse != nullptr)
-          p.lse[static_cast<int64_t>(qs) * p.num_q_heads + hq] = p.sinks != nullptr ? p.sinks[hq] : -INFINITY;
-      }
-    return;
-  }
-  const Split r = split_of(p, L, n_new, TS);
-  if (split >= r.n) return;
-  if (r.n > p.max_splits) {                              // a length beyond the planned capacity
-    if (leads) atomicOr(p.err, kErrCapacity);
-    return;
-  }
-  const int tile_begin = r.tile0 + split * r.per;
-  const int tile_end = min(tile_begin + r.per, r.tile0 + r.n_tiles);
-  const int tok_lo = max(r.lo, tile_begin * TS);
-  const int tok_hi = min(r.hi, tile_end * TS);
-  const int ps = p.page_size;
-  const int ps_log2 = __ffs(ps) - 1;
-  const int pg0 = (tile_begin * TS) >> ps_log2;
-  const int pg1 = (tok_hi + ps - 1) >> ps_log2;          // <= ceil(L / ps)
-  // tiles where every row sees every key need no mask per element
-  const int pos_first = L - n_new;
-  const int lo_last = p.window > 0 ? L - p.window : 0;
-  const int full_lo = max(tok_lo, lo_last);
-  const int full_hi = min(tok_hi, pos_first + 1);
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  const int cta = blockIdx.x;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * T::WARP_BYTES);
-  PageScale* sc_s = reinterpret_cast<PageScale*>(bars + ((kWarps * NS + 1) & ~1));
-  int32_t* bt_s = reinterpret_cast<int32_t*>(sc_s + p.bt_cache);
+  float* states = reinterpret_cast<float*>(smem + NS * T::STAGE);   // [W][HW][D], then [W][HW] maxima and sums
+  float* wm = states + W * T::HW * D;
+  float* wl = wm + W * T::HW;
+  uint64_t* full = reinterpret_cast<uint64_t*>(wl + W * T::HW);
+  uint64_t* empty = full + NS;
+  __shared__ long long s_sum[W + 1];
+  __shared__ long long s_at;
+  __shared__ int s_first, s_last;
 
-  const int warp = tid >> 5;
-  const int lane = tid & 31;
-  const int g = lane >> 2;
-  const int c = lane & 3;
-
-  // (a split longer than its slice of the table would be a planner's mistake; it
-  // still reports to the merge)
-  const bool bt_fits = pg1 - pg0 <= p.bt_cache;
-  if (!bt_fits && tid == 0) atomicOr(p.err, kErrSchedOverflow);
-  const int n_tiles = bt_fits ? tile_end - tile_begin : 0;
-  const int n_pages = bt_fits ? pg1 - pg0 : 0;
-  const int32_t* bt_row = p.block_table + static_cast<int64_t>(b) * p.bt_stride + pg0;
-  // a page id outside the pool becomes the coordinate num_pages, whose box reads as zeros
-  for (int i = tid; i < n_pages; i += kWarps * 32) {
-    int id = bt_row[i];
-    if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) {
-      if (((pg0 + i + 1) << ps_log2) > tok_lo) atomicOr(p.err, kErrPageId);
-      id = p.num_pages;
+  if (tid == W * 32) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], W);
     }
-    bt_s[i] = id;
-  }
-  if (tid == 0) {
-    prefetch_tensormap(&tmk);
-    prefetch_tensormap(&tmv);
-    for (int i = 0; i < kWarps * NS; ++i) mbar_init(&bars[i], 1);
     fence_mbar_init();
   }
+
+  // ---- this CTA's share of all requests' units --------------------------------
+  const int per = (p.batch + T::THREADS - 1) / T::THREADS;
+  const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    Request r;
+    if (!load_request(p, b, TS, T::HW, hgroups, r) && cta == 0) atomicOr(p.err, kErrCapacity);
+    mine += static_cast<long long>(r.n_tiles) * r.ys;
+  }
+  // (decode of an empty request: no key, O = 0 and the LSE the sink's or -inf)
+  if (p.qsl == nullptr)
+    for (int b = cta; b < p.batch; b += gridDim.x) {
+      if (p.seq_lens[b] != 0) continue;
+      for (int i = tid; i < p.num_q_heads * (D / 2); i += T::THREADS) {
+        const int hq = i / (D / 2), d = 2 * (i - hq * (D / 2));
+        *reinterpret_cast<uint32_t*>(p.out + static_cast<int64_t>(b) * p.out_stride_tok +
+                                     static_cast<int64_t>(hq) * p.out_stride_head + d) = 0u;
+        if (d == 0 && p.lse != nullptr)
+          p.lse[static_cast<int64_t>(b) * p.num_q_heads + hq] = p.sinks != nullptr ? p.sinks[hq] : -INFINITY;
+      }
+    }
+  long long incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-
-  uint8_t* wbase = smem + warp * T::WARP_BYTES;
-  uint64_t* wbar = bars + warp * NS;
-
-  // Lane 0: fetch local tile k into `stage`.  Boxes wholly past the end of the
-  // sequence are not fetched; their rows are masked.
-  auto issue = [&](int k, int stage) {
-    const int t0 = (tile_begin + k) * TS;
-    const int br = ps < TS ? ps : TS;
-    int nb = 0;
-    for (int j = 0; j < TS / br; ++j) nb += (t0 + j * br < L) ? 1 : 0;
-    uint8_t* kst = wbase + stage * T::STAGE;
-    uint8_t* vst = kst + T::TILE;
-    mbar_arrive_expect_tx(&wbar[stage], static_cast<uint32_t>(nb * br * D * 2));
-    for (int j = 0; j < nb; ++j) {
-      const int t = t0 + j * br;
-      const int page = bt_s[(t >> ps_log2) - pg0];
-      const int slot = t & (ps - 1);
+  long long total = 0, before = incl - mine;
 #pragma unroll
-      for (int cc = 0; cc < T::NCC; ++cc) {
-        const int dst = cc * TS * T::RB + j * br * T::RB;
-        tma_load_4d(kst + dst, &tmk, cc * T::RB, kvh, slot, page, &wbar[stage]);
-        tma_load_4d(vst + dst, &tmv, cc * T::RB, kvh, slot, page, &wbar[stage]);
-      }
+  for (int w = 0; w <= W; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  // shares of at least min_tiles units each; share c is [total c / C, total (c + 1) / C)
+  const long long C = min(static_cast<long long>(gridDim.x), (total + p.min_tiles - 1) / p.min_tiles);
+  if (cta >= C) return;
+  long long at = total * cta / C;
+  long long left = total * (cta + 1) / C - at;
+  if (before <= at && at < before + mine) {
+    long long u = before;
+    int b = b0;
+    for (;; ++b) {
+      Request r;
+      load_request(p, b, TS, T::HW, hgroups, r);
+      const long long n = static_cast<long long>(r.n_tiles) * r.ys;
+      if (at < u + n) break;
+      u += n;
     }
+    s_first = b;
+    s_at = at - u;
+  }
+  __syncthreads();
+  // place of the walk over the share: request, group of heads and rows, tile; both the fetching warp and the
+  // compute warps walk it, the former a ring ahead
+  int b = s_first;
+  Request r;
+  load_request(p, b, TS, T::HW, hgroups, r);
+  int y = static_cast<int>(s_at / r.n_tiles);
+  int tile = static_cast<int>(s_at - static_cast<long long>(y) * r.n_tiles);
+  auto advance = [&](int n) {            // n tiles of a (request, y) done
+    at += n;
+    left -= n;
+    tile += n;
+    if (left <= 0 || tile < r.n_tiles) return;
+    tile = 0;
+    if (++y < r.ys) return;
+    y = 0;
+    do {
+      ++b;
+      load_request(p, b, TS, T::HW, hgroups, r);
+    } while (r.n_tiles == 0);            // (units are left, so a request with some follows)
   };
-  if (lane == 0) {
-    for (int s = 0; s < NS; ++s) {
-      const int k = warp + s * kWarps;
-      if (k < n_tiles) issue(k, s);
-    }
-  }
-  __syncwarp();
+  const int ps = p.page_size;
+  const int ps_log2 = __ffs(ps) - 1;
+  // the TMA coordinate of a page (-> `i`): an id outside the pool, or no attended page, becomes num_pages, whose
+  // box reads as zeros
+  auto page_coord = [&](int i, int tok_lo, int tok_hi, bool flag) {
+    if ((i << ps_log2) >= tok_hi) return p.num_pages;
+    const int id = p.block_table[static_cast<int64_t>(b) * p.bt_stride + i];
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages)) return id;
+    if (flag && ((i + 1) << ps_log2) > tok_lo) atomicOr(p.err, kErrPageId);
+    return p.num_pages;
+  };
+  const int br = ps < TS ? ps : TS;      // slots a box
 
-  // scales of this head's pages (under the first tiles' loads); a page wholly before the
-  // window adds nothing, whatever its scales hold by now
-  for (int i = tid; i < n_pages; i += kWarps * 32) {
-    const int id = bt_s[i];
-    const bool in = id < p.num_pages && ((pg0 + i + 1) << ps_log2) > tok_lo;
-    const int64_t at = static_cast<int64_t>(in ? id : 0) * p.scale_stride + kvh;
-    const float ks = in ? p.k_scales[at] : 0.f;
-    const float vs = in ? fmaxf(p.v_scales[at], kLeastScale) : kLeastScale;
-    sc_s[i] = PageScale{ks, lg2(vs), 1.f / vs, 0.f};
-  }
-
-  // Q^T fragments (B operand): unit ks of a row holds dims 16 ks ..; thread c has
-  // codes 4c .. 4c + 3 of it.  Each row times 2^e with its largest value in [2^14, 2^15).
-  uint32_t qf[T::KS][NH8][2];
-  float rsl[NH8][2];         // the score factor of this thread's two accumulator rows
+  if (warp == W) {
+    // ---- the fetching warp: a stage's boxes lie one after the other, [head][slot] rows each ----
+    const int box = br * T::RB << p.hg_log2;
+    int it = 0;
+    while (left > 0) {
+      const int n = static_cast<int>(min(left, static_cast<long long>(r.n_tiles - tile)));
+      const int kvh0 = (y % hgroups) << p.hg_log2;
+      const int tile_begin = r.tile0 + tile;
+      const int tok_lo = max(r.lo, tile_begin * TS), tok_hi = min(r.L, (tile_begin + n) * TS);
+      const int pg0 = (tile_begin * TS) >> ps_log2;
+      int base = pg0;                    // lane i holds page base + i
+      int coord = page_coord(base + lane, tok_lo, tok_hi, true);
+      for (int k = 0; k < n; ++k, ++it) {
+        const int stage = it % NS;
+        if (it >= NS && !__all_sync(0xffffffffu, mbar_wait(&empty[stage], ((it / NS) - 1) & 1, p.err))) return;
+        const int t0 = (tile_begin + k) * TS;
+        int nb = 0;                      // boxes with a key of the sequence
+        for (int j = 0; j < TS / br; ++j) nb += (t0 + j * br < r.L) ? 1 : 0;
+        uint8_t* kst = smem + stage * T::STAGE;
+        if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(nb * (br << p.hg_log2) * D * 2));
+        __syncwarp();
+        for (int j = 0; j < nb; ++j) {
+          const int t = t0 + j * br;
+          const int i = t >> ps_log2;
+          if (i - base >= 32) {
+            base += 32;
+            coord = page_coord(base + lane, tok_lo, tok_hi, true);
+          }
+          const int page = __shfl_sync(0xffffffffu, coord, i - base);
+          if (lane == 0) {
 #pragma unroll
-  for (int j = 0; j < NH8; ++j) {
-    const int rr = j * 8 + g;
-    const bool ok = rr < R;
-    const int tq = ok ? (row0 + rr) / G : 0;
-    const int hq = ok ? row0 + rr - tq * G : 0;
-    const uint16_t* qh = p.q + static_cast<int64_t>(qs + tq) * p.q_stride_tok +
-                         static_cast<int64_t>(kvh * G + hq) * p.q_stride_head + 4 * c;
-    uint32_t most = 0;
-#pragma unroll
-    for (int ks = 0; ks < T::KS; ++ks) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = ok ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 2 * h) : 0u;
-        qf[ks][j][h] = w;
-        most = max(most, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+            for (int cc = 0; cc < T::NCC; ++cc) {
+              uint8_t* dst = kst + cc * (T::TILE / T::NCC) + j * box;
+              tma_load_4d(dst, &tmk, cc * T::RB, t & (ps - 1), kvh0, page, &full[stage]);
+              tma_load_4d(dst + T::TILE, &tmv, cc * T::RB, t & (ps - 1), kvh0, page, &full[stage]);
+            }
+          }
+        }
       }
+      advance(n);
     }
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-    const uint32_t e = max(most >> 7, 15u);              // biased exponent of the row's largest value
-    const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
-#pragma unroll
-    for (int ks = 0; ks < T::KS; ++ks)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t w = qf[ks][j][h];
-        qf[ks][j][h] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t er = __shfl_sync(0xffffffffu, e, (2 * c + h) * 4);
-      rsl[j][h] = (CAP ? p.scale_over_cap : p.scale_log2) * __uint_as_float((er - 14u) << 23);
-    }
+    return;
   }
 
-  float o[T::KS][NH8][4];
-#pragma unroll
-  for (int i = 0; i < T::KS; ++i)
-#pragma unroll
-    for (int j = 0; j < NH8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
-  float m_run[NH8][2], l_run[NH8][2];
-  int rpos[NH8][2], rlo[NH8][2];      // this thread's two rows: last and first attended key
-#pragma unroll
-  for (int j = 0; j < NH8; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      m_run[j][h] = -INFINITY;
-      l_run[j][h] = 0.f;
-      rpos[j][h] = pos_first + (row0 + min(j * 8 + 2 * c + h, R - 1)) / G;
-      rlo[j][h] = p.window > 0 ? rpos[j][h] - p.window + 1 : 0;
-    }
-  __syncthreads();                    // sc_s
-
+  // ---- the compute warps -----------------------------------------------------------
+  const int g = lane >> 2;
+  const int c = lane & 3;
+  const int hw = warp & (HG - 1);                        // head of the group
+  const int kw = warp >> p.hg_log2;                      // 16-key group of a stage
   const int mi = lane >> 3, mr = lane & 7;
+  const int row = mr + ((mi & 1) << 3);
+  // where this warp's 16 rows lie in a stage
+  const int key0 = kw * 16;
+  const uint32_t smem_u = smem_u32(smem) +
+      (static_cast<uint32_t>(key0 / br) * (br << p.hg_log2) + hw * br + key0 % br) * T::RB;
+  bool dead = false;                                     // a wait ran out: no more results
   int it = 0;
-  for (int k = warp; k < n_tiles; k += kWarps, ++it) {
-    const int stage = it % NS;
-    const uint32_t parity = static_cast<uint32_t>((it / NS) & 1);
-    const bool ok = __all_sync(0xffffffffu, mbar_wait(&wbar[stage], parity, p.err));
-    if (!ok) break;
-    const uint32_t kst_u = smem_u32(wbase + stage * T::STAGE);
-    const uint32_t vst_u = kst_u + T::TILE;
-    const int t0 = (tile_begin + k) * TS;
-    const bool partial = (t0 < full_lo) || (t0 + TS > full_hi);
+  while (left > 0) {
+    const int n = static_cast<int>(min(left, static_cast<long long>(r.n_tiles - tile)));
+    const int kvh0 = (y % hgroups) << p.hg_log2;
+    const int kvh = kvh0 + hw;
+    const int row0 = (y / hgroups) * T::HW;              // first (token, head) row
+    const int R = min(r.n_new * G - row0, T::HW);
+    const int tile_begin = r.tile0 + tile;
+    const int tok_lo = max(r.lo, tile_begin * TS), tok_hi = min(r.L, (tile_begin + n) * TS);
+    // scales of this head's pages: lane i holds those of page base + i; a page wholly before the window
+    // adds nothing, whatever its scales hold by now
+    float page_k, page_v;
+    auto scales_of = [&](int i) {
+      const int id = page_coord(i, tok_lo, tok_hi, false);
+      const bool in = id < p.num_pages && ((i + 1) << ps_log2) > tok_lo;
+      const int64_t sa = static_cast<int64_t>(in ? id : 0) * p.scale_stride + kvh;
+      page_k = in ? p.k_scales[sa] : 0.f;
+      page_v = lg2(in ? fmaxf(p.v_scales[sa], kLeastScale) : kLeastScale);
+    };
+    int base = (tile_begin * TS) >> ps_log2;
+    scales_of(base + lane);
 
-    // ---- S^T = K Q^T over the codes ----------------------------------------
-    float s[T::MT][NH8][4];
+    // Q^T fragments (B operand): unit ks of a row holds dims 16 ks ..; thread c has
+    // codes 4c .. 4c + 3 of it.  Each row times 2^e with its largest value in [2^14, 2^15).
+    uint32_t qf[T::KS][NH8][2];
+    float rsl[NH8][2];         // the score factor of this thread's two accumulator rows
+    int rpos[NH8][2];          // and their positions
 #pragma unroll
-    for (int mt = 0; mt < T::MT; ++mt) {
+    for (int j = 0; j < NH8; ++j) {
+      const int rr = j * 8 + g;
+      const bool ok = rr < R;
+      const int tq = ok ? (row0 + rr) / G : 0;
+      const int hq = ok ? row0 + rr - tq * G : 0;
+      const uint16_t* qh = p.q + static_cast<int64_t>(r.qs + tq) * p.q_stride_tok +
+                           static_cast<int64_t>(kvh * G + hq) * p.q_stride_head + 4 * c;
+      uint32_t most = 0;
+#pragma unroll
+      for (int ks = 0; ks < T::KS; ++ks) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = ok ? *reinterpret_cast<const uint32_t*>(qh + ks * 16 + 2 * h) : 0u;
+          qf[ks][j][h] = w;
+          most = max(most, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+        }
+      }
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const uint32_t e = max(most >> 7, 15u);              // biased exponent of the row's largest value
+      const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - (e - 127))
+#pragma unroll
+      for (int ks = 0; ks < T::KS; ++ks)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t w = qf[ks][j][h];
+          qf[ks][j][h] = pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+        }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t er = __shfl_sync(0xffffffffu, e, (2 * c + h) * 4);
+        rsl[j][h] = (CAP ? p.scale_over_cap : p.scale_log2) * __uint_as_float((er - 14u) << 23);
+        rpos[j][h] = r.L - r.n_new + (row0 + min(j * 8 + 2 * c + h, R - 1)) / G;
+      }
+    }
+    float m_run[NH8][2], l_run[NH8][2];
+    float o[T::KS][NH8][4];
+#pragma unroll
+    for (int j = 0; j < NH8; ++j) m_run[j][0] = m_run[j][1] = -INFINITY, l_run[j][0] = l_run[j][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < T::KS; ++i)
 #pragma unroll
       for (int j = 0; j < NH8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
-      const int row = mt * 16 + mr + ((mi & 1) << 3);
+        for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
+
+    // keys [full_lo, full_hi) are seen by every row: other 16-key groups mask each element
+    const int full_lo = max(tok_lo, p.window > 0 ? r.L - p.window : 0);
+    const int full_hi = min(tok_hi, r.L - r.n_new + 1);
+    for (int k = 0; k < n; ++k, ++it) {
+      const int stage = it % NS;
+      const int t0 = (tile_begin + k) * TS + key0;         // this warp's first key
+      // (a page beyond the sequence's last holds only masked keys, any scale will do)
+      const int pg = t0 >> ps_log2;
+      if (pg - base >= 32) {
+        base += 32;
+        scales_of(base + lane);
+      }
+      const float ks = __shfl_sync(0xffffffffu, page_k, pg - base);
+      const float lv = __shfl_sync(0xffffffffu, page_v, pg - base);
+      dead = dead || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (it / NS) & 1, p.err));
+      if (dead) continue;
+      const uint32_t kst_u = smem_u + stage * T::STAGE;
+      const uint32_t vst_u = kst_u + T::TILE;
+      const bool partial = (t0 < full_lo) || (t0 + 16 > full_hi);
+      // ---- S^T = K Q^T over the codes ----------------------------------------
+      float s[NH8][4];
+#pragma unroll
+      for (int j = 0; j < NH8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
 #pragma unroll
       for (int u = 0; u < T::KS; u += 2) {
         uint32_t w[4];               // keys 0-7 and 8-15 of unit u, then of unit u + 1
@@ -404,114 +508,94 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
             a[3] = e4m3x2_to_f16x2<1>(w[2 * v + 1]);
           }
 #pragma unroll
-          for (int j = 0; j < NH8; ++j) mma_f16(s[mt][j], a, qf[u + v][j][0], qf[u + v][j][1]);
+          for (int j = 0; j < NH8; ++j) mma_f16(s[j], a, qf[u + v][j][0], qf[u + v][j][1]);
         }
       }
-    }
 
-    // ---- scales, soft-cap, mask; online softmax (log2 domain) --------------
-    // (the 16 keys of an m-tile lie in one page)
-    float mx[NH8][2];
-    float v_inv[T::MT];
+      // ---- scales, soft-cap, mask; online softmax (log2 domain) --------------
+      float mx[NH8][2];
 #pragma unroll
-    for (int j = 0; j < NH8; ++j) mx[j][0] = mx[j][1] = -INFINITY;
-    auto scores = [&](auto masked_tag) {
-      constexpr bool MASKED = decltype(masked_tag)::value;
+      for (int j = 0; j < NH8; ++j) {
+        const float f[2] = {ks * rsl[j][0], ks * rsl[j][1]};
 #pragma unroll
-      for (int mt = 0; mt < T::MT; ++mt) {
-        // (a tile's last m-tiles may lie behind the request's last page)
-        const int pg = min(((t0 + mt * 16) >> ps_log2), pg1 - 1) - pg0;
-        const float4 ps4 = *reinterpret_cast<const float4*>(&sc_s[pg]);
-        v_inv[mt] = ps4.z;
-#pragma unroll
-        for (int j = 0; j < NH8; ++j) {
-          const float f[2] = {ps4.x * rsl[j][0], ps4.x * rsl[j][1]};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v;
-            if constexpr (CAP) {
-              v = fmaf(p.cap_log2, tanhf(s[mt][j][e] * f[e & 1]), ps4.y);
-            } else {
-              v = fmaf(s[mt][j][e], f[e & 1], ps4.y);
-            }
-            if constexpr (MASKED) {
-              const int tok = t0 + mt * 16 + g + ((e >> 1) << 3);
-              if (tok < tok_lo || tok >= tok_hi || tok > rpos[j][e & 1] || tok < rlo[j][e & 1]) v = -INFINITY;
-            }
-            s[mt][j][e] = v;
-            mx[j][e & 1] = fmaxf(mx[j][e & 1], v);
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (CAP) {
+            s[j][e] = fmaf(p.cap_log2, tanhf(s[j][e] * f[e & 1]), lv);
+          } else {
+            s[j][e] = fmaf(s[j][e], f[e & 1], lv);
           }
         }
       }
-    };
-    if (partial) {
-      scores(std::true_type{});
-    } else {
-      scores(std::false_type{});
-    }
-    float alpha[NH8][2], mu[NH8][2];
-    bool grew = false;
+      if (partial) {
 #pragma unroll
-    for (int j = 0; j < NH8; ++j)
+        for (int j = 0; j < NH8; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float m = mx[j][h];
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        const float m_new = fmaxf(m_run[j][h], m);
-        const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
-        grew |= m_new > m_run[j][h];
-        alpha[j][h] = ex2(m_run[j][h] - m_use);
-        m_run[j][h] = m_new;
-        mu[j][h] = m_use - kWeightBias;
+          for (int e = 0; e < 4; ++e) {
+            const int tok = t0 + g + ((e >> 1) << 3);
+            const int pos = rpos[j][e & 1];
+            if (tok < tok_lo || tok >= tok_hi || tok > pos || (p.window > 0 && tok <= pos - p.window))
+              s[j][e] = -INFINITY;
+          }
       }
-    const bool rescale = __any_sync(0xffffffffu, grew);
+      bool grew = false;
 #pragma unroll
-    for (int j = 0; j < NH8; ++j) {
-      float ls0 = 0.f, ls1 = 0.f;
+      for (int j = 0; j < NH8; ++j)
 #pragma unroll
-      for (int mt = 0; mt < T::MT; ++mt) {
-        s[mt][j][0] = ex2(s[mt][j][0] - mu[j][0]);
-        s[mt][j][1] = ex2(s[mt][j][1] - mu[j][1]);
-        s[mt][j][2] = ex2(s[mt][j][2] - mu[j][0]);
-        s[mt][j][3] = ex2(s[mt][j][3] - mu[j][1]);
-        ls0 = fmaf(s[mt][j][0] + s[mt][j][2], v_inv[mt], ls0);
-        ls1 = fmaf(s[mt][j][1] + s[mt][j][3], v_inv[mt], ls1);
-      }
-      l_run[j][0] = fmaf(l_run[j][0], alpha[j][0], ls0);
-      l_run[j][1] = fmaf(l_run[j][1], alpha[j][1], ls1);
-      if (rescale) {
-#pragma unroll
-        for (int i = 0; i < T::KS; ++i) {
-          o[i][j][0] *= alpha[j][0];
-          o[i][j][1] *= alpha[j][1];
-          o[i][j][2] *= alpha[j][0];
-          o[i][j][3] *= alpha[j][1];
+        for (int h = 0; h < 2; ++h) {
+          float m = fmaxf(s[j][h], s[j][h + 2]);
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          mx[j][h] = m;
+          grew |= m > m_run[j][h];
         }
-      }
-    }
-
-    // ---- O^T += V^T P^T over the codes ---------------------------------------
-    auto pv = [&](auto mask_tag) {
-      constexpr bool MASK = decltype(mask_tag)::value;
-#pragma unroll
-      for (int mt = 0; mt < T::MT; ++mt) {
-        uint32_t pb[NH8][2];
+      // the accumulators need rescaling only after a maximum rose somewhere in the warp
+      if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
         for (int j = 0; j < NH8; ++j) {
-          pb[j][0] = movmatrix_t(pack_f16x2(s[mt][j][0], s[mt][j][1]));
-          pb[j][1] = movmatrix_t(pack_f16x2(s[mt][j][2], s[mt][j][3]));
+          float alpha[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float m_new = fmaxf(m_run[j][h], mx[j][h]);
+            alpha[h] = m_new == -INFINITY ? 1.f : ex2(m_run[j][h] - m_new);
+            m_run[j][h] = m_new;
+            l_run[j][h] *= alpha[h];
+          }
+#pragma unroll
+          for (int i = 0; i < T::KS; ++i) {
+            o[i][j][0] *= alpha[0];
+            o[i][j][1] *= alpha[1];
+            o[i][j][2] *= alpha[0];
+            o[i][j][3] *= alpha[1];
+          }
         }
+      }
+      const float iv = ex2(-lv);
+      uint32_t pb[NH8][2];
+#pragma unroll
+      for (int j = 0; j < NH8; ++j) {
+        float mu[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mu[h] = m_run[j][h] == -INFINITY ? 0.f : m_run[j][h] - kWeightBias;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = ex2(s[j][e] - mu[e & 1]);
+        l_run[j][0] = fmaf(s[j][0] + s[j][2], iv, l_run[j][0]);
+        l_run[j][1] = fmaf(s[j][1] + s[j][3], iv, l_run[j][1]);
+        pb[j][0] = movmatrix_t(pack_f16x2(s[j][0], s[j][1]));
+        pb[j][1] = movmatrix_t(pack_f16x2(s[j][2], s[j][3]));
+      }
+
+      // ---- O^T += V^T P^T over the codes ---------------------------------------
+      auto pv = [&](auto mask_tag) {
+        constexpr bool MASK = decltype(mask_tag)::value;
         // masked keys have P = 0, but their codes may be stale (NaN in e4m3): zeroed
         uint32_t vm_lo = 0xffffffffu, vm_hi = 0xffffffffu;
         if constexpr (MASK) {
-          const int tk = t0 + mt * 16 + 2 * c;
+          const int tk = t0 + 2 * c;
           auto valid = [&](int t) { return t >= tok_lo && t < tok_hi; };
           vm_lo = (valid(tk) ? 0x0000ffffu : 0u) | (valid(tk + 1) ? 0xffff0000u : 0u);
           vm_hi = (valid(tk + 8) ? 0x0000ffffu : 0u) | (valid(tk + 9) ? 0xffff0000u : 0u);
         }
-        const int row = mt * 16 + mr + ((mi & 1) << 3);
 #pragma unroll
         for (int u = 0; u < T::KS; u += 2) {
           uint32_t w[4];             // of unit u: keys 0-7, 8-15; then of unit u + 1
@@ -544,142 +628,123 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
             for (int j = 0; j < NH8; ++j) mma_f16(o[u + v][j], a, pb[j][0], pb[j][1]);
           }
         }
+      };
+      if (partial) {
+        pv(std::true_type{});
+      } else {
+        pv(std::false_type{});
       }
-    };
-    if (partial) {
-      pv(std::true_type{});
-    } else {
-      pv(std::false_type{});
+
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[stage]);
     }
 
-    __syncwarp();
-    const int kn = k + NS * kWarps;
-    if (lane == 0 && kn < n_tiles) {
-      fence_proxy_async_smem();
-      issue(kn, stage);
-    }
-  }
-
-  // ---- merge the four warps' states in shared memory -----------------------
-  // (every copy a warp issued was waited for in its loop, or an expired wait ended
-  // the loop: then its copies may still land in this region, and the call's
-  // results are void)
-  float* wo = reinterpret_cast<float*>(wbase);   // [HW][D]
-  float* wm = wo + T::HW * D;
-  float* wl = wm + T::HW;
-#pragma unroll
-  for (int j = 0; j < NH8; ++j)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = l_run[j][h];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      if (g == 0) {
-        wm[j * 8 + 2 * c + h] = m_run[j][h];
-        wl[j * 8 + 2 * c + h] = l;
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < T::KS; ++i)
+    // ---- the warps' states, merged over a head's KW warps ----------------------------
 #pragma unroll
     for (int j = 0; j < NH8; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<float2*>(wo + (j * 8 + 2 * c + e) * D + 16 * i + 2 * g) =
-            make_float2(o[i][j][e], o[i][j][e + 2]);
-  __syncthreads();
-
-  const bool direct = (r.n == 1);
-  for (int e = tid; e < R * D; e += kWarps * 32) {
-    const int h = e / D;
-    const int d = e - h * D;
-    float M = -INFINITY;
+      for (int h = 0; h < 2; ++h) {
+        float l = l_run[j][h];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int rr = j * 8 + 2 * c + h;
+        if (g == 0) {
+          wm[warp * T::HW + rr] = m_run[j][h];
+          wl[warp * T::HW + rr] = l;
+        }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-      M = fmaxf(M, (reinterpret_cast<const float*>(smem + w * T::WARP_BYTES) + T::HW * D)[h]);
-    if (M == -INFINITY) M = 0.f;
-    float num = 0.f, den = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float* wob = reinterpret_cast<const float*>(smem + w * T::WARP_BYTES);
-      const float f = ex2(wob[T::HW * D + h] - M);
-      num += wob[h * D + d] * f;
-      den += wob[T::HW * D + T::HW + h] * f;
-    }
-    const int tq = (row0 + h) / G;
-    const int hq = kvh * G + (row0 + h - tq * G);
-    const int64_t orow = qs + tq;
-    // den = sum 2^(x - M + 14) / vs: the row's LSE is M - 14 + log2 den
-    const float lse2 = den == 0.f ? -INFINITY : M - kWeightBias + lg2(den);
-    const float ov = den == 0.f ? 0.f : num / den;
-    if (direct) {
-      float f = 1.f, total = lse2;
-      if (p.sinks != nullptr) {
-        const float sk = p.sinks[hq] * kLog2e;
-        const float top = fmaxf(lse2, sk);
-        const float z = ex2(lse2 - top) + ex2(sk - top);
-        f = ex2(lse2 - top) / z;
-        total = top + lg2(z);
+        for (int i = 0; i < T::KS; ++i)
+          *reinterpret_cast<float2*>(states + (warp * T::HW + rr) * D + 16 * i + 2 * g) =
+              make_float2(o[i][j][h], o[i][j][h + 2]);
       }
-      p.out[orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head + d] =
-          __bfloat16_as_ushort(__float2bfloat16_rn(ov * f));
-      if (d == 0 && p.lse != nullptr) p.lse[orow * p.num_q_heads + hq] = total * kLn2;
-    } else {
-      const int64_t row = (orow * p.num_q_heads + hq) * p.max_splits + split;
-      p.o_part[row * D + d] = ov;
-      if (d == 0) p.lse_part[row] = lse2 * kLn2;
+    compute_sync<W>();
+    // the shares that hold parts of this (request, y): first .. last; a share's first part goes to place 2 share,
+    // its last to 2 share + 1
+    const long long pair0 = at - tile, pair1 = pair0 + r.n_tiles;
+    const int first = static_cast<int>(((pair0 + 1) * C - 1) / total);
+    const int last = static_cast<int>((pair1 * C - 1) / total);
+    const bool direct = first == last;
+    const int place = 2 * cta + (at != total * cta / C ? 1 : 0);
+    for (int e = tid; e < HG * R * (D / 4); e += W * 32) {
+      const int hr = e / (D / 4);
+      const int d = (e - hr * (D / 4)) * 4;
+      const int head = hr / R;
+      const int rr = hr - head * R;
+      float M = -INFINITY;
+      for (int w = 0; w < KW; ++w) M = fmaxf(M, wm[((w << p.hg_log2) + head) * T::HW + rr]);
+      if (M == -INFINITY) M = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f;
+      for (int w = 0; w < KW; ++w) {
+        const int sa = ((w << p.hg_log2) + head) * T::HW + rr;
+        const float f = ex2(wm[sa] - M);
+        const float4 x = *reinterpret_cast<const float4*>(states + sa * D + d);
+        num.x += x.x * f; num.y += x.y * f; num.z += x.z * f; num.w += x.w * f;
+        den += wl[sa] * f;
+      }
+      // den = sum 2^(x - M + 14) / vs: the row's LSE is M - 14 + log2 den
+      const float lse2 = den == 0.f ? -INFINITY : M - kWeightBias + lg2(den);
+      const float inv = den == 0.f ? 0.f : 1.f / den;
+      const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+      if (direct) {
+        write_row(p, r.qs, kvh0 + head, row0 + rr, d, v, lse2);
+      } else {
+        const int64_t pa = (static_cast<int64_t>(place) * HG + head) * T::HW + rr;
+        *reinterpret_cast<float4*>(p.o_part + pa * D + d) = v;
+        if (d == 0) p.lse_part[pa] = lse2;
+      }
     }
-  }
-  if (direct) return;
-
-  // ---- the last split of these rows to finish merges --------------------------
-  __syncthreads();
-  int* s_last = reinterpret_cast<int*>(smem);
-  if (tid == 0) {
-    uint32_t* cnt = p.merge_cnt + static_cast<int64_t>(b) * gridDim.y + blockIdx.y;
-    __threadfence();
-    const uint32_t prev = atomicAdd(cnt, 1u);
-    const int last = prev + 1 == static_cast<uint32_t>(r.n);
-    if (last) {
-      atomicExch(cnt, 0u);
-      __threadfence();
+    if (!direct) {
+      // the part of this (request, y) that is done last merges them all; no CTA waits for another, and the last
+      // one resets the counter
+      compute_sync<W>();
+      if (tid == 0) {
+        __threadfence();
+        const uint32_t prev = atomicAdd(p.merge_cnt + first, 1u);
+        s_last = prev == static_cast<uint32_t>(last - first);
+        if (s_last) {
+          atomicExch(p.merge_cnt + first, 0u);
+          __threadfence();
+        }
+      }
+      compute_sync<W>();
+      if (s_last) {
+        const int place0 = 2 * first + (pair0 != total * first / C ? 1 : 0);
+        merge_parts<D, T::HW, W * 32>(p, place0, first, last - first + 1, R, row0, kvh0, HG, r.qs);
+      }
     }
-    *s_last = last;
+    compute_sync<W>();                                   // (the states, s_last are read)
+    advance(n);
   }
-  __syncthreads();
-  if (*s_last == 0) return;
-  merge_rows<D>(p, r.n, R, row0, kvh, qs);
 }
 
-// Keys per stage and stages per warp.
-template <int D> struct Choice;
-template <> struct Choice<64> { static constexpr int TS = 32, NS = 3; };
-template <> struct Choice<128> { static constexpr int TS = 32, NS = 2; };
-template <> struct Choice<256> { static constexpr int TS = 16, NS = 3; };
+struct Variant {
+  int warps, smem, ctas;
+};
 
-int tile_of(int D) { return D == 64 ? Choice<64>::TS : D == 128 ? Choice<128>::TS : Choice<256>::TS; }
-
-template <int D>
-int smem_of(int bt_cache) {
-  using C = Choice<D>;
-  return 1024 + kWarps * C::NS * 2 * C::TS * D + ((kWarps * C::NS + 1) & ~1) * 8 +
-         bt_cache * static_cast<int>(sizeof(PageScale) + 4);
+template <int D, int NH8>
+Variant variant() {
+  using C = Choice<D, NH8>;
+  return {C::W, Traits<D, NH8, C::W, C::NS>::SMEM, C::CPS};
 }
 
-int smem_bytes(int D, int bt_cache) {
-  return D == 64 ? smem_of<64>(bt_cache) : D == 128 ? smem_of<128>(bt_cache) : smem_of<256>(bt_cache);
+Variant variant_of(int D, int nh8) {
+  if (D == 64) return nh8 == 1 ? variant<64, 1>() : variant<64, 2>();
+  if (D == 128) return nh8 == 1 ? variant<128, 1>() : variant<128, 2>();
+  return nh8 == 1 ? variant<256, 1>() : variant<256, 2>();
 }
 
 template <int D, bool I8, int NH8>
-cudaError_t launch_split(const CUtensorMap& tmk, const CUtensorMap& tmv, const BlockParams& p, dim3 grid, int smem,
+cudaError_t launch_split(const CUtensorMap& tmk, const CUtensorMap& tmv, const BlockParams& p, dim3 grid,
                          cudaStream_t stream) {
-  using C = Choice<D>;
-  auto kern = p.cap_log2 > 0.f ? block_split_kernel<D, I8, NH8, C::TS, C::NS, true>
-                               : block_split_kernel<D, I8, NH8, C::TS, C::NS, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  using C = Choice<D, NH8>;
+  using T = Traits<D, NH8, C::W, C::NS>;
+  auto kern = p.cap_log2 > 0.f ? block_split_kernel<D, I8, NH8, C::W, C::NS, true>
+                               : block_split_kernel<D, I8, NH8, C::W, C::NS, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kWarps * 32, smem, stream>>>(tmk, tmv, p);
+  kern<<<grid, T::THREADS, T::SMEM, stream>>>(tmk, tmv, p);
   return cudaGetLastError();
 }
 
@@ -802,7 +867,6 @@ pa_shape as_shape(const pa_block_shape& s, int mode) {
   e.window = s.window;
   e.has_sinks = s.has_sinks;
   e.soft_cap = s.soft_cap;
-  e.num_splits = s.num_splits;
   e.num_sms = s.num_sms;
   return e;
 }
@@ -829,21 +893,32 @@ ChunkScratch chunk_scratch(const pa_block_shape& s, int64_t group) {
 int rows_of(const pa_block_shape& s) { return std::max(s.max_new, 1) * (s.num_q_heads / s.num_kv_heads); }
 int nh8_of(const pa_block_shape& s) { return rows_of(s) <= 8 ? 1 : 2; }
 
-int64_t partial_rows(const pa_block_shape& s, int64_t max_splits) {
-  return static_cast<int64_t>(s.max_total_q) * s.num_q_heads * max_splits;
-}
+// kv heads a CTA takes, as a log2: a power of two that divides Hkv, at most its warps, and no more than
+// leave kGroups groups of heads over all requests: the splits of a group are merged by one CTA.
+constexpr int kGroups = 64;
 
-int64_t split_scratch(const pa_block_shape& s, int64_t max_splits) {
-  const int64_t rows = max_splits > 1 ? partial_rows(s, max_splits) : 0;
-  return kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256) + align_up(rows * 4, 256);
+int heads_log2(const pa_block_shape& s, int warps) {
+  int l = 0;
+  while ((2 << l) <= warps && s.num_kv_heads % (2 << l) == 0 &&
+         static_cast<int64_t>(s.max_batch) * (s.num_kv_heads >> (l + 1)) >= kGroups)
+    ++l;
+  return l;
 }
 
 // Above this many rows a kv head (of one request) the chunked form is taken.
 constexpr int kSplitRows = 64;
 
+// Fewest keys of one head that a CTA of the split kernel is given, so that what a share costs once stays small.
+constexpr int kLeastKeys = 512;
+
+int64_t split_scratch(const pa_block_shape& s, int64_t ctas, int hg) {
+  const int64_t rows = 2 * ctas * nh8_of(s) * 8 << hg;
+  return kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256) + align_up(rows * 4, 256);
+}
+
 pa_status validate(const pa_block_shape& s) {
   if (s.code != PA_CODE_E4M3 && s.code != PA_CODE_INT8) return PA_ERR_INVALID_ARG;
-  if (s.max_new < 1) return PA_ERR_INVALID_ARG;
+  if (s.max_new < 1 || s.num_ctas < 0) return PA_ERR_INVALID_ARG;
   const pa_status st = validate_shape(as_shape(s, PA_MODE_EXTEND));
   if (st != PA_OK) return st;
   if (s.max_batch > 65535) return PA_ERR_UNSUPPORTED;
@@ -851,51 +926,35 @@ pa_status validate(const pa_block_shape& s) {
 }
 
 pa_status plan_split(const pa_block_shape& s, const int32_t* lens, int32_t batch, int num_sms, pa_block_plan_t* out) {
-  const int TS = tile_of(s.head_dim);
-  const int NH = nh8_of(s) * 8;
-  const int groups = static_cast<int>(cdiv(rows_of(s), NH));
-  const int64_t ctas_y = static_cast<int64_t>(s.num_kv_heads) * groups;
-  if (ctas_y > 65535) return PA_ERR_UNSUPPORTED;
-  auto keys = [&](int64_t L) {
-    return s.window > 0 ? std::min<int64_t>(L, static_cast<int64_t>(s.window) + s.max_new - 1) : L;
+  const Variant v = variant_of(s.head_dim, nh8_of(s));
+  const int hg = heads_log2(s, v.warps);
+  const int TS = 16 * (v.warps >> hg);
+  const int groups = static_cast<int>(cdiv(rows_of(s), nh8_of(s) * 8));
+  const int64_t ctas_y = static_cast<int64_t>(s.num_kv_heads >> hg) * groups;
+  const int64_t max_n = static_cast<int64_t>(s.max_pages_per_seq) * s.page_size;
+  auto tiles = [&](int64_t L) {
+    return cdiv(s.window > 0 ? std::min<int64_t>(L, static_cast<int64_t>(s.window) + s.max_new - 1) : L, TS) +
+           (s.window > 0 ? 1 : 0);
   };
-  const int64_t max_n = keys(static_cast<int64_t>(s.max_pages_per_seq) * s.page_size);
-  const int64_t max_tiles = max_n > 0 ? cdiv(max_n, TS) + (s.window > 0 ? 1 : 0) : 1;
-  int64_t split_tiles = 0, per_max, max_splits;
-  if (s.num_splits > 0) {
-    max_splits = std::min<int64_t>(s.num_splits, max_tiles);
-    per_max = cdiv(max_tiles, max_splits);
+  int64_t units = 0;
+  if (lens) {
+    for (int b = 0; b < batch; ++b) units += tiles(lens[b]) * ctas_y;
   } else {
-    int64_t units = 0;
-    if (lens) {
-      for (int b = 0; b < batch; ++b) units += cdiv(keys(lens[b]), TS);
-      units *= ctas_y;
-    } else {
-      units = static_cast<int64_t>(s.max_batch) * ctas_y * max_tiles;
-    }
-    const int64_t slots = static_cast<int64_t>(num_sms) * 3;
-    split_tiles = std::max<int64_t>(8, cdiv(units, slots * 4));
-    split_tiles = std::min<int64_t>(split_tiles, max_tiles);
-    max_splits = cdiv(max_tiles, split_tiles);
-    per_max = split_tiles;
+    units = s.max_batch * ctas_y * tiles(max_n);
   }
-  // the last split of a (request, kv head, row group) merges, counted in the header: more of them than
-  // counters go unsplit
-  if (max_splits > 1 && s.max_batch * ctas_y > kMergeCounters) {
-    if (s.num_splits > 0) return PA_ERR_UNSUPPORTED;
-    max_splits = 1;
-    split_tiles = per_max = max_tiles;
-  }
-  const int64_t bt_cache = cdiv(per_max * TS, s.page_size) + 2;
-  if (bt_cache > 8192 || smem_bytes(s.head_dim, static_cast<int>(bt_cache)) > kMaxSmem) return PA_ERR_UNSUPPORTED;
+  // one wave, or fewer CTAs where the lengths (or capacities) give none of them its least share
+  const int64_t least = std::max<int64_t>(1, kLeastKeys / (v.warps * 16));
+  const int64_t wave = std::min<int64_t>(s.num_ctas > 0 ? s.num_ctas : static_cast<int64_t>(num_sms) * v.ctas,
+                                         kMergeCounters);
+  const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(wave, cdiv(units, least)));
   out->chunked = 0;
   out->tile_tokens = TS;
-  out->split_tiles = static_cast<int32_t>(split_tiles);
-  out->max_splits = static_cast<int32_t>(max_splits);
+  out->min_tiles = static_cast<int32_t>(least);
+  out->ctas = static_cast<int32_t>(ctas);
   out->row_groups = groups;
-  out->bt_cache = static_cast<int32_t>(bt_cache);
-  out->smem_bytes = smem_bytes(s.head_dim, out->bt_cache);
-  out->scratch_bytes = split_scratch(s, max_splits);
+  out->head_group = 1 << hg;
+  out->smem_bytes = v.smem;
+  out->scratch_bytes = split_scratch(s, ctas, hg);
   return PA_OK;
 }
 
@@ -907,7 +966,6 @@ pa_status plan_chunks(const pa_block_shape& s, pa_block_plan_t* out) {
   if (group * s.max_pages_per_seq > INT32_MAX) return PA_ERR_UNSUPPORTED;
   out->chunked = 1;
   out->group_requests = static_cast<int32_t>(group);
-  out->max_splits = 1;
   out->tile_tokens = 64;
   out->scratch_bytes = chunk_scratch(s, group).end;
   return PA_OK;
@@ -915,12 +973,10 @@ pa_status plan_chunks(const pa_block_shape& s, pa_block_plan_t* out) {
 
 template <int D>
 cudaError_t launch_rows(bool i8, int nh8, const CUtensorMap& tmk, const CUtensorMap& tmv, const BlockParams& p,
-                        dim3 grid, int smem, cudaStream_t st) {
+                        dim3 grid, cudaStream_t st) {
   if (i8)
-    return nh8 == 1 ? launch_split<D, true, 1>(tmk, tmv, p, grid, smem, st)
-                    : launch_split<D, true, 2>(tmk, tmv, p, grid, smem, st);
-  return nh8 == 1 ? launch_split<D, false, 1>(tmk, tmv, p, grid, smem, st)
-                  : launch_split<D, false, 2>(tmk, tmv, p, grid, smem, st);
+    return nh8 == 1 ? launch_split<D, true, 1>(tmk, tmv, p, grid, st) : launch_split<D, true, 2>(tmk, tmv, p, grid, st);
+  return nh8 == 1 ? launch_split<D, false, 1>(tmk, tmv, p, grid, st) : launch_split<D, false, 2>(tmk, tmv, p, grid, st);
 }
 
 template <int D>
@@ -989,6 +1045,8 @@ extern "C" pa_status pa_block_attend(
   if (chunked != (rows_of(s) > kSplitRows)) return PA_ERR_INVALID_ARG;
   const int NH = nh8_of(s) * 8;
   const int groups = static_cast<int>(cdiv(rows_of(s), NH));
+  const Variant v = variant_of(s.head_dim, NH / 8);
+  const int hg = heads_log2(s, v.warps);
   if (chunked) {
     if (plan->group_requests < 1 ||
         static_cast<int64_t>(plan->group_requests) * s.max_pages_per_seq > INT32_MAX ||
@@ -996,12 +1054,9 @@ extern "C" pa_status pa_block_attend(
       return PA_ERR_INVALID_ARG;
     if (!query_start_loc && batch > 0) return PA_ERR_INVALID_ARG;      // (one row a request: a plan of max_new 1)
   } else {
-    if (plan->max_splits < 1 || plan->split_tiles < 0 || (plan->split_tiles == 0 && s.num_splits == 0) ||
-        plan->bt_cache < 1 || plan->bt_cache > 8192 || plan->row_groups != groups ||
-        plan->tile_tokens != tile_of(s.head_dim) || plan->smem_bytes != smem_bytes(s.head_dim, plan->bt_cache) ||
-        plan->smem_bytes > kMaxSmem || plan->scratch_bytes < split_scratch(s, plan->max_splits) ||
-        (plan->max_splits > 1 &&
-         static_cast<int64_t>(s.max_batch) * s.num_kv_heads * groups > kMergeCounters))
+    if (plan->ctas < 1 || plan->ctas > kMergeCounters || plan->min_tiles < 1 || plan->row_groups != groups ||
+        plan->head_group != 1 << hg || plan->tile_tokens != 16 * (v.warps >> hg) || plan->smem_bytes != v.smem ||
+        plan->scratch_bytes < split_scratch(s, plan->ctas, hg))
       return PA_ERR_INVALID_ARG;
   }
   if (batch == 0 || total_q == 0) return PA_OK;
@@ -1030,11 +1085,11 @@ extern "C" pa_status pa_block_attend(
   if (!chunked) {
     const int box_rows = std::min(s.page_size, plan->tile_tokens);
     CUtensorMap tmk, tmv;
-    if ((st = make_kv_map(&tmk, k_cache, true, s.head_dim, s.num_kv_heads, s.page_size, num_pages, kv_stride_page,
-                          kv_stride_tok, kv_stride_head, box_rows)) != PA_OK)
+    if ((st = make_codes_map(&tmk, k_cache, s.head_dim, s.num_kv_heads, s.page_size, num_pages, kv_stride_page,
+                             kv_stride_tok, kv_stride_head, box_rows, 1 << hg)) != PA_OK)
       return st;
-    if ((st = make_kv_map(&tmv, v_cache, true, s.head_dim, s.num_kv_heads, s.page_size, num_pages, kv_stride_page,
-                          kv_stride_tok, kv_stride_head, box_rows)) != PA_OK)
+    if ((st = make_codes_map(&tmv, v_cache, s.head_dim, s.num_kv_heads, s.page_size, num_pages, kv_stride_page,
+                             kv_stride_tok, kv_stride_head, box_rows, 1 << hg)) != PA_OK)
       return st;
     BlockParams p{};
     p.q = static_cast<const uint16_t*>(q);
@@ -1065,22 +1120,19 @@ extern "C" pa_status pa_block_attend(
     p.out_stride_tok = out_stride_tok;
     p.out_stride_head = out_stride_head;
     p.lse = lse;
-    const int64_t rows = plan->max_splits > 1 ? partial_rows(s, plan->max_splits) : 0;
+    const int64_t rows = static_cast<int64_t>(2) * plan->ctas * NH << hg;
     p.o_part = reinterpret_cast<float*>(sc + kScratchHeaderBytes);
     p.lse_part = reinterpret_cast<float*>(sc + kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256));
-    p.max_splits = plan->max_splits;
-    p.split_tiles = plan->split_tiles;
-    p.fixed_splits = s.num_splits > 0 ? plan->max_splits : 0;
-    p.bt_cache = plan->bt_cache;
-    p.row_groups = groups;
+    p.min_tiles = plan->min_tiles;
+    p.hg_log2 = hg;
     p.merge_cnt = reinterpret_cast<uint32_t*>(sc + kMergeCounterOffset);
     p.err = reinterpret_cast<uint32_t*>(sc);
-    const dim3 grid(plan->max_splits, s.num_kv_heads * groups, batch);
+    const dim3 grid(plan->ctas);
     cudaError_t e;
     switch (s.head_dim) {
-      case 64: e = launch_rows<64>(i8, NH / 8, tmk, tmv, p, grid, plan->smem_bytes, strm); break;
-      case 128: e = launch_rows<128>(i8, NH / 8, tmk, tmv, p, grid, plan->smem_bytes, strm); break;
-      default: e = launch_rows<256>(i8, NH / 8, tmk, tmv, p, grid, plan->smem_bytes, strm); break;
+      case 64: e = launch_rows<64>(i8, NH / 8, tmk, tmv, p, grid, strm); break;
+      case 128: e = launch_rows<128>(i8, NH / 8, tmk, tmv, p, grid, strm); break;
+      default: e = launch_rows<256>(i8, NH / 8, tmk, tmv, p, grid, strm); break;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }

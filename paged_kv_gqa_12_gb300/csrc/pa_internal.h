@@ -75,6 +75,8 @@ pa_status check_kv(const pa_shape& s, const void* k, const void* v, int64_t st_p
                    int64_t st_head, int32_t num_pages);
 pa_status make_kv_map(CUtensorMap* map, const void* base, bool fp8, int D, int Hkv, int ps, int num_pages,
                       int64_t st_page, int64_t st_tok, int64_t st_head, int box_rows);
+pa_status make_codes_map(CUtensorMap* map, const void* base, int D, int Hkv, int ps, int num_pages, int64_t st_page,
+                         int64_t st_tok, int64_t st_head, int box_rows, int heads);
 pa_status make_q_map(CUtensorMap* map, const void* base, int D, int Hq, int rows, int64_t st_tok, int64_t st_head,
                      int group, int rows_per_box);
 

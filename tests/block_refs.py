@@ -87,10 +87,12 @@ def append(kind, x, cache, scales, table, seq, qsl, ps):
     return v, scales
 
 
-def attend(q, kc, vc, ks, vs, table, seq, qsl, scale, window=0, sinks=None, cap=0.0, num_pages=None):
+def attend(q, kc, vc, ks, vs, table, seq, qsl, scale, window=0, sinks=None, cap=0.0, chunked=False):
     """(out, lse, bounds of both) in float64 for packed rows (qsl None: one row a request).  The bounds are those of
-    the kernels' roundings: a weight in f16 (half a step, relative), fp32 sums of D products and of n keys (a step of
-    2^-23 for each addition), exponentials and logarithms good to 2^-20, and the output in bf16."""
+    the kernels' roundings: a weight in f16 (half a step, relative; and where it is subnormal half of f16's least step,
+    2^-25, which with weights of up to 2^14 -- 2^7 in chunks -- is 2^-39 -- 2^-32 -- of the row's largest weight times
+    V scale, for each code it meets), fp32 sums of D products and of n keys (a step of 2^-23 for each addition),
+    exponentials and logarithms good to 2^-20, and the output in bf16."""
     T, Hq, D = q.shape
     pool, ps, Hkv = kc.shape[0], kc.shape[1], kc.shape[2]
     G = Hq // Hkv
@@ -110,6 +112,8 @@ def attend(q, kc, vc, ks, vs, table, seq, qsl, scale, window=0, sinks=None, cap=
                          else torch.zeros(ps, D, dtype=torch.float64) for i in ids]
                 return torch.cat(parts)[:L]
             k, v = load(kc, ks), load(vc, vs)
+            size_v = torch.tensor([float(vs[i, h]) if 0 <= i < pool else 0.0 for i in ids],
+                                  dtype=torch.float64).repeat_interleave(ps)[:L].clamp(min=2.0 ** -100)
             for r in range(n):
                 pos = L - n + r
                 lo = max(0, pos - window + 1) if window else 0
@@ -121,7 +125,7 @@ def attend(q, kc, vc, ks, vs, table, seq, qsl, scale, window=0, sinks=None, cap=
                     x = cap * torch.tanh(x / cap)
                     eps += 2.0 ** -18 * cap      # tanh to a few units of 2^-23, by the cap
                 eps += 2.0 ** -22 * float(x.abs().max())
-                vv = v[lo:pos + 1]
+                vv, sv = v[lo:pos + 1], size_v[lo:pos + 1]
                 if sinks is not None:
                     x = torch.cat([x, sinks[rows, None].double()], 1)
                     vv = torch.cat([vv, torch.zeros(1, D, dtype=torch.float64)])
@@ -130,7 +134,11 @@ def attend(q, kc, vc, ks, vs, table, seq, qsl, scale, window=0, sinks=None, cap=
                 lse[begin + r, rows] = torch.logsumexp(x, 1)
                 keys = pos + 1 - lo
                 rel = HALF["f16"] + 2 * eps + 2.0 ** -23 * keys
-                tol_o[begin + r, rows] = rel * (w @ vv.abs()) + HALF["bf16"] * out[begin + r, rows].abs() + 2.0 ** -100
+                keyed = w[:, :keys] * sv
+                least = (2.0 ** -32 if chunked else 2.0 ** -39) * keyed.max(1, keepdim=True).values \
+                    * (vv[:keys].abs() / sv[:, None]).sum(0)
+                tol_o[begin + r, rows] = rel * (w @ vv.abs()) + least + HALF["bf16"] * out[begin + r, rows].abs() \
+                    + 2.0 ** -100
                 tol_l[begin + r, rows] = eps + 2.0 ** -23 * (keys + 16) + 2.0 ** -22 * lse[begin + r, rows].abs()
     return out, lse, tol_o, tol_l
 

@@ -32,11 +32,9 @@ def _plan(**kw):
     (dict(head_dim=96), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED), (dict(num_q_heads=129 * 8), UNSUPPORTED),
     (dict(window=-1), INVALID), (dict(soft_cap=-1.0), INVALID), (dict(soft_cap=float("nan")), INVALID),
     (dict(max_batch=-1), INVALID), (dict(max_batch=65536), UNSUPPORTED), (dict(max_total_q=-1), INVALID),
-    (dict(max_pages_per_seq=1 << 27), UNSUPPORTED), (dict(num_splits=-1), INVALID),
+    (dict(max_pages_per_seq=1 << 27), UNSUPPORTED), (dict(num_ctas=-1), INVALID),
     (dict(host_seq_lens=[5, -1]), INVALID), (dict(host_seq_lens=[512 * 16 + 1]), INVALID),
     (dict(host_seq_lens=[1] * 65), INVALID),
-    (dict(max_batch=20000, num_splits=4), UNSUPPORTED),                   # more merging groups than counters
-    (dict(max_pages_per_seq=1 << 20, num_splits=1), UNSUPPORTED),          # a split's pages beyond shared memory
 ])
 def test_plan_rejects(lib, bad, status):
     with pytest.raises(pb.PaError) as e:
@@ -46,8 +44,8 @@ def test_plan_rejects(lib, bad, status):
 
 def test_plans(lib):
     p = _plan()
-    assert p.chunked == 0 and p.row_groups == 1 and p.max_splits >= 1 and p.smem_bytes <= 232448
-    rows = 256 * 32 * p.max_splits
+    assert p.chunked == 0 and p.row_groups == 1 and p.ctas >= 152 and p.smem_bytes <= 232448
+    rows = 2 * p.ctas * p.head_group * 16                 # two parts a CTA, 16 rows a head
     assert p.scratch_bytes == pb.SCRATCH_HEADER_BYTES + rows * 128 * 4 + rows * 4
     assert _plan(max_new=1, max_total_q=64).row_groups == 1
     assert _plan(max_new=16).row_groups == 4 and _plan(max_new=16).chunked == 0
@@ -57,17 +55,22 @@ def test_plans(lib):
     assert c.group_requests * 512 * 16 * 8 * 128 * 4 <= 1 << 31
     one = _plan(max_new=100, max_pages_per_seq=1 << 17)
     assert one.group_requests == 1
-    # many requests without a merge counter each: unsplit
-    assert _plan(max_batch=20000, max_total_q=20000, max_new=1).max_splits == 1
-    # a sequence too long for the slice of the table a CTA stages is cut
-    long = _plan(max_batch=1, max_pages_per_seq=65536, max_new=1, max_total_q=1)
-    assert long.bt_cache <= 8192 and long.max_splits > 1
-    assert _plan(max_batch=0, max_total_q=0, max_pages_per_seq=0).max_splits == 1
+    # short contexts do not need a whole wave of CTAs; the lengths may say so
+    assert _plan(max_batch=1, max_pages_per_seq=8, max_total_q=1, max_new=1).ctas <= 8
+    assert _plan(host_seq_lens=[100] * 4).ctas < _plan(host_seq_lens=[8000] * 64).ctas == p.ctas
+    assert _plan(num_ctas=5).ctas == 5
+    # a CTA takes as many heads as divide Hkv, up to its warps, and then as many more keys; few requests: one head
+    def heads(h, batch=64):
+        q = _plan(num_kv_heads=h, num_q_heads=h, max_new=1, max_batch=batch)
+        return q.head_group, q.tile_tokens * q.head_group
+    assert [heads(h)[0] for h in (1, 2, 3, 4, 6, 8)] == [1, 2, 1, 4, 2, 4] and heads(8, 1)[0] == 1
+    assert len({heads(h)[1] for h in (1, 2, 3, 8)}) == 1
+    assert _plan(max_batch=0, max_total_q=0, max_pages_per_seq=0).ctas == 1
 
 
 def test_plan_uses_host_lengths(lib):
     a, b = _plan(host_seq_lens=[600] * 64), _plan(host_seq_lens=[8000] * 64)
-    assert b.split_tiles >= a.split_tiles
+    assert b.ctas >= a.ctas and a.scratch_bytes <= b.scratch_bytes
 
 
 def _attend(lib, plan, **over):
@@ -106,10 +109,10 @@ def test_chunked_attend_rejects_before_launch(lib, over, status):
 
 
 def test_attend_rejects_hand_edited_plans(lib):
-    for plan, edits in ((_plan(), dict(chunked=1)), (_plan(max_new=100), dict(chunked=0)), (_plan(), dict(max_splits=0)),
-                        (_plan(), dict(row_groups=2)), (_plan(), dict(tile_tokens=8)), (_plan(), dict(bt_cache=0)),
-                        (_plan(), dict(bt_cache=9000)), (_plan(), dict(smem_bytes=1000)), (_plan(), dict(split_tiles=0)),
-                        (_plan(), dict(split_tiles=-1)), (_plan(), dict(max_splits=10000)),
+    for plan, edits in ((_plan(), dict(chunked=1)), (_plan(max_new=100), dict(chunked=0)), (_plan(), dict(ctas=0)),
+                        (_plan(), dict(row_groups=2)), (_plan(), dict(tile_tokens=8)), (_plan(), dict(head_group=1)),
+                        (_plan(), dict(smem_bytes=1000)), (_plan(), dict(min_tiles=0)),
+                        (_plan(), dict(ctas=20000)), (_plan(), dict(ctas=10000)),
                         (_plan(max_new=100), dict(group_requests=0)), (_plan(max_new=100), dict(group_requests=60000))):
         for k, v in edits.items():
             setattr(plan, k, v)

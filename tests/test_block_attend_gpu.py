@@ -87,7 +87,8 @@ def _run(s, decode=False, plan=None):
 
 def _want(s, decode=False):
     return ref.attend(s["q"], s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["table"], s["seq"],
-                      None if decode else s["qsl"], s["scale"], s["window"], s["sinks"], s["cap"])
+                      None if decode else s["qsl"], s["scale"], s["window"], s["sinks"], s["cap"],
+                      chunked=max(s["new"]) * (s["Hq"] // s["Hkv"]) > 64)
 
 
 def _close(got, want, what=""):
@@ -120,11 +121,11 @@ def test_decode(kind, D, ps):
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 @pytest.mark.parametrize("opts", [dict(window=1), dict(window=40), dict(window=700, sinks=True), dict(sinks=True),
                                   dict(cap=30.0), dict(cap=5.0, window=100, sinks=True)])
-@pytest.mark.parametrize("splits", [0, 1, 3, 1000])
-def test_decode_options(kind, opts, splits):
+@pytest.mark.parametrize("ctas", [0, 1, 3, 17])
+def test_decode_options(kind, opts, ctas):
     n = len(LENS) - 1
     s = _problem(77, kind, 8, 2, 128, 16, [L - 1 for L in LENS[:-1]], [1] * n, **opts)
-    got = _run(s, decode=True, plan=_plan(s, num_splits=splits))
+    got = _run(s, decode=True, plan=_plan(s, num_ctas=ctas))
     assert got[2] == 0
     _close(got, _want(s, decode=True))
 
