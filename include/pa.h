@@ -574,7 +574,7 @@ pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_len
  * A length beyond the plan's capacity, a packing with more rows than tokens, than max_new or than
  * total_q leaves that request's rows untouched (PA_DEVICE_CAPACITY); a block-table entry outside
  * the pool reads as zeros (PA_DEVICE_PAGE_ID).  Rows behind query_start_loc[batch] are left as they
- * were.  The other arguments as for pa_extend.  Asynchronous on `stream`; one kernel launch, or
+ * were.  The other arguments as for pa_extend.  Asynchronous on `stream`; two kernel launches, or
  * three for each plan->group_requests requests of a chunked plan. */
 pa_status pa_block_attend(const pa_block_plan_t* plan,
                           const void* q, int64_t q_stride_tok, int64_t q_stride_head,

@@ -20,9 +20,9 @@
 // rows) evenly: a prefix sum over the requests gives each CTA its run of tiles, which
 // may end one request and begin the next.  W compute warps are HG heads x KW groups
 // of 16 keys of a tile; one more warp fetches a tile's codes, one TMA box for a page's
-// slots of all HG heads, a ring of stages ahead and across requests.  Parts of a
-// request that lie in several shares are merged by the CTA that is done last; what a
-// share costs once (prefix sum, q, merge) is why there is one wave.  (Every warp with a
+// slots of all HG heads, a ring of stages ahead and across requests.  Rows
+// whose tiles lie in several shares are merged by a second kernel; what a share costs
+// once (prefix sum, q, parts) is why there is one wave.  (Every warp with a
 // ring and tiles of its own, equal splits of each request: 119 us for 64 requests of
 // up to 8192 tokens, 59 for one of 131071.)
 //
@@ -53,6 +53,14 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightBias = 14.f;           // weights are at most 2^14 (f16 holds 65504)
 constexpr float kLeastScale = 0x1p-100f;      // V scales below count as this one: its log2 and inverse are finite
 
+// Rows whose parts lie in several shares: part 0 at place0, part i at place 2 (share + i).
+struct MergeRecord {
+  int n;                      // parts; 0: no record
+  int place0, share;
+  int qs, kvh0, row0, rows, pad;
+};
+static_assert(sizeof(MergeRecord) == 32, "two 16-byte loads a record");
+
 struct BlockParams {
   const uint16_t* q;
   int64_t q_stride_tok, q_stride_head;
@@ -73,9 +81,9 @@ struct BlockParams {
   float* lse;
   float* o_part;              // [2 grid][HG][HW][D] normalised parts of rows
   float* lse_part;            // [2 grid][HG][HW] their LSEs, log2
+  MergeRecord* records;       // [grid] the (request, heads, rows) that begins in a CTA's share and ends beyond, if any
   int min_tiles;              // fewest tiles a CTA is given
   int hg_log2;                // kv heads a CTA takes: 2^hg_log2
-  uint32_t* merge_cnt;        // [grid] arrivals at the (request, heads, rows) that begins in a CTA's share and ends beyond
   uint32_t* err;
 };
 
@@ -144,72 +152,23 @@ __device__ __forceinline__ void compute_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(W * 32) : "memory");
 }
 
-// Final value of four dims of a row: the sink, if any, joins the denominator.
-__device__ __forceinline__ void write_row(const BlockParams& p, int qs, int kvh, int row, int d, float4 v, float lse2) {
+// A finished row: where it goes, and the factor of its values (the sink, if any, joins the denominator);
+// `lead` writes its LSE.
+__device__ __forceinline__ uint16_t* finish_row(const BlockParams& p, int qs, int kvh, int row, float lse2, bool lead,
+                                                float& factor) {
   const int tq = row / p.group;
   const int hq = kvh * p.group + (row - tq * p.group);
   const int64_t orow = qs + tq;
+  factor = 1.f;
   if (p.sinks != nullptr) {
     const float sk = p.sinks[hq] * kLog2e;
     const float top = fmaxf(lse2, sk);
     const float own = ex2(lse2 - top), z = own + ex2(sk - top);
-    const float f = own / z;
-    v.x *= f; v.y *= f; v.z *= f; v.w *= f;
+    factor = own / z;
     lse2 = top + lg2(z);
   }
-  uint16_t* outp = p.out + orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head + d;
-  reinterpret_cast<uint32_t*>(outp)[0] = pack_bf16x2(v.x, v.y);     // (rows are 4-byte aligned)
-  reinterpret_cast<uint32_t*>(outp)[1] = pack_bf16x2(v.z, v.w);
-  if (d == 0 && p.lse != nullptr) p.lse[orow * p.num_q_heads + hq] = lse2 * kLn2;
-}
-
-// The n parts of the R rows of each of the heads of a group, merged by their LSEs: thread t
-// takes 4 consecutive dims of one row, eight parts' loads in flight together.  Part 0 lies at
-// place0, part i at place 2 (first + i).
-template <int D, int HW, int THREADS>
-__device__ __forceinline__ void merge_parts(const BlockParams& p, int place0, int first, int n, int R, int row0,
-                                            int kvh0, int heads, int qs) {
-  constexpr int C = D / 4;
-  constexpr int U = 8;
-  for (int e = threadIdx.x; e < heads * R * C; e += THREADS) {
-    const int hr = e / C;
-    const int d = (e - hr * C) * 4;
-    const int head = hr / R;
-    const int rr = hr - head * R;
-    float M = -INFINITY, Z = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < n; s0 += U) {
-      float l[U];
-      float4 o[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool ok = s0 + u < n;
-        const int place = s0 + u == 0 ? place0 : 2 * (first + s0 + u);
-        const int64_t pa = (static_cast<int64_t>(place) * heads + head) * HW + rr;
-        l[u] = ok ? __ldcg(p.lse_part + pa) : -INFINITY;
-        o[u] = ok ? __ldcg(reinterpret_cast<const float4*>(p.o_part + pa * D + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float mx = l[0];
-#pragma unroll
-      for (int u = 1; u < U; ++u) mx = fmaxf(mx, l[u]);
-      if (mx > M) {
-        const float f = ex2(M - mx);
-        Z *= f;
-        acc.x *= f; acc.y *= f; acc.z *= f; acc.w *= f;
-        M = mx;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (l[u] == -INFINITY) continue;      // padding, or a part with no key for this row
-        const float w = ex2(l[u] - M);
-        Z += w;
-        acc.x += w * o[u].x; acc.y += w * o[u].y; acc.z += w * o[u].z; acc.w += w * o[u].w;
-      }
-    }
-    const float inv = Z == 0.f ? 0.f : 1.f / Z;
-    write_row(p, qs, kvh0 + head, row0 + rr, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv),
-              Z == 0.f ? -INFINITY : M + lg2(Z));
-  }
+  if (lead && p.lse != nullptr) p.lse[orow * p.num_q_heads + hq] = lse2 * kLn2;
+  return p.out + orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head;
 }
 
 template <int D, bool I8, int NH8, int W, int NS, bool CAP>
@@ -234,9 +193,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   float* wl = wm + W * T::HW;
   uint64_t* full = reinterpret_cast<uint64_t*>(wl + W * T::HW);
   uint64_t* empty = full + NS;
-  __shared__ long long s_sum[W + 1];
-  __shared__ long long s_at;
-  __shared__ int s_first, s_last;
+  __shared__ int s_sum[W + 1];
+  __shared__ int s_first, s_at;
 
   if (tid == W * 32) {
     for (int i = 0; i < NS; ++i) {
@@ -246,14 +204,15 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     fence_mbar_init();
   }
 
+  if (tid == 0) p.records[cta].n = 0;
   // ---- this CTA's share of all requests' units --------------------------------
   const int per = (p.batch + T::THREADS - 1) / T::THREADS;
   const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-  long long mine = 0;
+  int mine = 0;                                          // (the plan keeps all sums below 2^31)
   for (int b = b0; b < b1; ++b) {
     Request r;
     if (!load_request(p, b, TS, T::HW, hgroups, r) && cta == 0) atomicOr(p.err, kErrCapacity);
-    mine += static_cast<long long>(r.n_tiles) * r.ys;
+    mine += r.n_tiles * r.ys;
   }
   // (decode of an empty request: no key, O = 0 and the LSE the sink's or -inf)
   if (p.qsl == nullptr)
@@ -267,32 +226,39 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
           p.lse[static_cast<int64_t>(b) * p.num_q_heads + hq] = p.sinks != nullptr ? p.sinks[hq] : -INFINITY;
       }
     }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, m);
+    const int v = __shfl_up_sync(0xffffffffu, incl, m);
     if (lane >= m) incl += v;
   }
   if (lane == 31) s_sum[warp] = incl;
   __syncthreads();
-  long long total = 0, before = incl - mine;
+  int total = 0, before = incl - mine;
 #pragma unroll
   for (int w = 0; w <= W; ++w) {
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
-  // shares of at least min_tiles units each; share c is [total c / C, total (c + 1) / C)
-  const long long C = min(static_cast<long long>(gridDim.x), (total + p.min_tiles - 1) / p.min_tiles);
+  // shares of at least min_tiles units: the first `more` of one unit more than the others
+  const int C = min(static_cast<int>(gridDim.x), (total + p.min_tiles - 1) / p.min_tiles);
+  pdl_launch_dependents();             // (the merge kernel waits for this grid's end)
   if (cta >= C) return;
-  long long at = total * cta / C;
-  long long left = total * (cta + 1) / C - at;
+  const int share = total / C, more = total - share * C;
+  const int begin = share * cta + min(cta, more);
+  auto share_of = [&](int u) {
+    const int m = more * (share + 1);
+    return u < m ? u / (share + 1) : more + (u - m) / share;
+  };
+  int at = begin;
+  int left = share + (cta < more ? 1 : 0);
   if (before <= at && at < before + mine) {
-    long long u = before;
+    int u = before;
     int b = b0;
     for (;; ++b) {
       Request r;
       load_request(p, b, TS, T::HW, hgroups, r);
-      const long long n = static_cast<long long>(r.n_tiles) * r.ys;
+      const int n = r.n_tiles * r.ys;
       if (at < u + n) break;
       u += n;
     }
@@ -305,8 +271,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   int b = s_first;
   Request r;
   load_request(p, b, TS, T::HW, hgroups, r);
-  int y = static_cast<int>(s_at / r.n_tiles);
-  int tile = static_cast<int>(s_at - static_cast<long long>(y) * r.n_tiles);
+  int y = s_at / r.n_tiles;
+  int tile = s_at - y * r.n_tiles;
   auto advance = [&](int n) {            // n tiles of a (request, y) done
     at += n;
     left -= n;
@@ -338,7 +304,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     const int box = br * T::RB << p.hg_log2;
     int it = 0;
     while (left > 0) {
-      const int n = static_cast<int>(min(left, static_cast<long long>(r.n_tiles - tile)));
+      const int n = min(left, r.n_tiles - tile);
       const int kvh0 = (y % hgroups) << p.hg_log2;
       const int tile_begin = r.tile0 + tile;
       const int tok_lo = max(r.lo, tile_begin * TS), tok_hi = min(r.L, (tile_begin + n) * TS);
@@ -391,7 +357,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   bool dead = false;                                     // a wait ran out: no more results
   int it = 0;
   while (left > 0) {
-    const int n = static_cast<int>(min(left, static_cast<long long>(r.n_tiles - tile)));
+    const int n = min(left, r.n_tiles - tile);
     const int kvh0 = (y % hgroups) << p.hg_log2;
     const int kvh = kvh0 + hw;
     const int row0 = (y / hgroups) * T::HW;              // first (token, head) row
@@ -639,7 +605,14 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
 
-    // ---- the warps' states, merged over a head's KW warps ----------------------------
+    // ---- the rows' values, merged over a head's KW warps -----------------------------
+    // the shares that hold parts of this (request, y): first .. last; a share's first part goes to place 2 share,
+    // its last to 2 share + 1
+    const int pair0 = at - tile, pair1 = pair0 + r.n_tiles;
+    const int first = share_of(pair0), last = share_of(pair1 - 1);
+    const bool direct = first == last;
+    const int place = 2 * cta + (at != begin ? 1 : 0);
+    float lse2[NH8][2];
 #pragma unroll
     for (int j = 0; j < NH8; ++j)
 #pragma unroll
@@ -648,74 +621,252 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
         l += __shfl_xor_sync(0xffffffffu, l, 4);
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int rr = j * 8 + 2 * c + h;
-        if (g == 0) {
-          wm[warp * T::HW + rr] = m_run[j][h];
-          wl[warp * T::HW + rr] = l;
-        }
+        l_run[j][h] = l;
+      }
+    if (KW > 1) {
+      // the head's first warp takes the others' states from shared memory
+      compute_sync<W>();                                 // (an earlier part's are read)
 #pragma unroll
-        for (int i = 0; i < T::KS; ++i)
-          *reinterpret_cast<float2*>(states + (warp * T::HW + rr) * D + 16 * i + 2 * g) =
-              make_float2(o[i][j][h], o[i][j][h + 2]);
-      }
-    compute_sync<W>();
-    // the shares that hold parts of this (request, y): first .. last; a share's first part goes to place 2 share,
-    // its last to 2 share + 1
-    const long long pair0 = at - tile, pair1 = pair0 + r.n_tiles;
-    const int first = static_cast<int>(((pair0 + 1) * C - 1) / total);
-    const int last = static_cast<int>((pair1 * C - 1) / total);
-    const bool direct = first == last;
-    const int place = 2 * cta + (at != total * cta / C ? 1 : 0);
-    for (int e = tid; e < HG * R * (D / 4); e += W * 32) {
-      const int hr = e / (D / 4);
-      const int d = (e - hr * (D / 4)) * 4;
-      const int head = hr / R;
-      const int rr = hr - head * R;
-      float M = -INFINITY;
-      for (int w = 0; w < KW; ++w) M = fmaxf(M, wm[((w << p.hg_log2) + head) * T::HW + rr]);
-      if (M == -INFINITY) M = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f;
-      for (int w = 0; w < KW; ++w) {
-        const int sa = ((w << p.hg_log2) + head) * T::HW + rr;
-        const float f = ex2(wm[sa] - M);
-        const float4 x = *reinterpret_cast<const float4*>(states + sa * D + d);
-        num.x += x.x * f; num.y += x.y * f; num.z += x.z * f; num.w += x.w * f;
-        den += wl[sa] * f;
-      }
-      // den = sum 2^(x - M + 14) / vs: the row's LSE is M - 14 + log2 den
-      const float lse2 = den == 0.f ? -INFINITY : M - kWeightBias + lg2(den);
-      const float inv = den == 0.f ? 0.f : 1.f / den;
-      const float4 v = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
-      if (direct) {
-        write_row(p, r.qs, kvh0 + head, row0 + rr, d, v, lse2);
-      } else {
-        const int64_t pa = (static_cast<int64_t>(place) * HG + head) * T::HW + rr;
-        *reinterpret_cast<float4*>(p.o_part + pa * D + d) = v;
-        if (d == 0) p.lse_part[pa] = lse2;
-      }
-    }
-    if (!direct) {
-      // the part of this (request, y) that is done last merges them all; no CTA waits for another, and the last
-      // one resets the counter
+      for (int j = 0; j < NH8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rr = j * 8 + 2 * c + h;
+          if (g == 0) {
+            wm[warp * T::HW + rr] = m_run[j][h];
+            wl[warp * T::HW + rr] = l_run[j][h];
+          }
+#pragma unroll
+          for (int i = 0; i < T::KS; ++i)
+            *reinterpret_cast<float2*>(states + (warp * T::HW + rr) * D + 16 * i + 2 * g) =
+                make_float2(o[i][j][h], o[i][j][h + 2]);
+        }
       compute_sync<W>();
-      if (tid == 0) {
-        __threadfence();
-        const uint32_t prev = atomicAdd(p.merge_cnt + first, 1u);
-        s_last = prev == static_cast<uint32_t>(last - first);
-        if (s_last) {
-          atomicExch(p.merge_cnt + first, 0u);
-          __threadfence();
+      // KW warps a head: each takes dims of its own, 16 i with i % KW == kw
+#pragma unroll
+      for (int j = 0; j < NH8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rr = j * 8 + 2 * c + h;
+          float M = -INFINITY, den = 0.f;
+          for (int w = 0; w < KW; ++w) M = fmaxf(M, wm[((w << p.hg_log2) + hw) * T::HW + rr]);
+          const float m_use = M == -INFINITY ? 0.f : M;
+          for (int w = 0; w < KW; ++w) {
+            const int sa = ((w << p.hg_log2) + hw) * T::HW + rr;
+            den += wl[sa] * ex2(wm[sa] - m_use);
+          }
+          m_run[j][h] = M;
+          l_run[j][h] = den;
+#pragma unroll
+          for (int i = 0; i < T::KS; ++i) {
+            if ((i & (KW - 1)) != kw) continue;
+            float2 v = make_float2(0.f, 0.f);
+            for (int w = 0; w < KW; ++w) {
+              const int sa = ((w << p.hg_log2) + hw) * T::HW + rr;
+              const float f = ex2(wm[sa] - m_use);
+              const float2 x = *reinterpret_cast<const float2*>(states + sa * D + 16 * i + 2 * g);
+              v.x = fmaf(x.x, f, v.x);
+              v.y = fmaf(x.y, f, v.y);
+            }
+            o[i][j][h] = v.x;
+            o[i][j][h + 2] = v.y;
+          }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NH8; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int rr = j * 8 + 2 * c + h;
+        if (rr >= R) continue;
+        // l = sum 2^(x - m + 14) / vs: the row's LSE is m - 14 + log2 l
+        const float den = l_run[j][h];
+        lse2[j][h] = den == 0.f ? -INFINITY : m_run[j][h] - kWeightBias + lg2(den);
+        float f = den == 0.f ? 0.f : 1.f / den;
+        const bool lead = g == 0 && kw == 0;
+        if (direct) {
+          float sink;
+          uint16_t* outp = finish_row(p, r.qs, kvh, row0 + rr, lse2[j][h], lead, sink) + 2 * g;
+          f *= sink;
+#pragma unroll
+          for (int i = 0; i < T::KS; ++i)
+            if ((i & (KW - 1)) == kw)
+              *reinterpret_cast<uint32_t*>(outp + 16 * i) = pack_bf16x2(o[i][j][h] * f, o[i][j][h + 2] * f);
+        } else {
+          const int64_t pa = (static_cast<int64_t>(place) * HG + hw) * T::HW + rr;
+          if (lead) p.lse_part[pa] = lse2[j][h];
+          float* part = p.o_part + pa * D + 2 * g;
+#pragma unroll
+          for (int i = 0; i < T::KS; ++i)
+            if ((i & (KW - 1)) == kw)
+              *reinterpret_cast<float2*>(part + 16 * i) = make_float2(o[i][j][h] * f, o[i][j][h + 2] * f);
         }
       }
-      compute_sync<W>();
-      if (s_last) {
-        const int place0 = 2 * first + (pair0 != total * first / C ? 1 : 0);
-        merge_parts<D, T::HW, W * 32>(p, place0, first, last - first + 1, R, row0, kvh0, HG, r.qs);
+    if (!direct && cta == first && tid == 0)
+      p.records[cta] = MergeRecord{last - first + 1, place, first, r.qs, kvh0, row0, R, 0};
+    advance(n);
+  }
+}
+
+// ---- rows in several shares, merged by their LSEs ------------------------------------
+// One warp a row where rows have at most 32 parts, else all warps of a CTA.  (The last CTA of a row's
+// shares as the merging one took 8 to 16 us: a few warps, each waiting for L2 row after row, often
+// with tiles of the next request to come.)
+constexpr int kMergeThreads = 256;
+
+// Parts [i0, i1) of a row: v = sum 2^(lse - M) part, Z likewise of 1; 16 parts' loads in flight together.
+template <int D>
+__device__ __forceinline__ void merge_range(const BlockParams& p, const MergeRecord& rec, int row_in_place, int place_rows,
+                                            int i0, int i1, int lane, float& M, float& Z, float4 (&v)[(D + 127) / 128]) {
+  constexpr int U = 16;
+  constexpr int K = (D + 127) / 128;
+  M = -INFINITY;
+  Z = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int d = (lane * 4) % D;
+  auto row_of = [&](int i) {
+    return static_cast<int64_t>(i == 0 ? rec.place0 : 2 * (rec.share + i)) * place_rows + row_in_place;
+  };
+  for (int base = i0; base < i1; base += U) {
+    const int n = min(U, i1 - base);
+    float l = __ldcg(p.lse_part + row_of(base + min(lane, n - 1)));
+    if (lane >= n) l = -INFINITY;
+    float4 o[U];
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < U; ++i)        // (behind the last part the last again, with weight 0)
+        o[i] = __ldcg(reinterpret_cast<const float4*>(p.o_part + row_of(base + min(i, n - 1)) * D + d + 128 * k));
+    };
+    fetch(0);
+    float m = l;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float top = fmaxf(M, m);
+    const float old = M == -INFINITY ? 0.f : ex2(M - top);
+    const float w = l == -INFINITY ? 0.f : ex2(l - top);   // (a part with no key for this row)
+    float z = w;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
+    Z = fmaf(Z, old, z);
+    M = top;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k > 0) fetch(k);
+      v[k].x *= old; v[k].y *= old; v[k].z *= old; v[k].w *= old;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        v[k].x = fmaf(f, o[i].x, v[k].x);
+        v[k].y = fmaf(f, o[i].y, v[k].y);
+        v[k].z = fmaf(f, o[i].z, v[k].z);
+        v[k].w = fmaf(f, o[i].w, v[k].w);
       }
     }
-    compute_sync<W>();                                   // (the states, s_last are read)
-    advance(n);
+  }
+}
+
+template <int D, int HW>
+__global__ void __launch_bounds__(kMergeThreads) block_merge_kernel(const BlockParams p, int ctas) {
+  constexpr int K = (D + 127) / 128;
+  constexpr int WARPS = kMergeThreads / 32;
+  extern __shared__ int s_off[];         // [ctas + 1] rows of the records before
+  __shared__ int s_sum[WARPS], s_most[WARPS];
+  __shared__ float s_v[WARPS][D];
+  __shared__ float s_m[WARPS], s_z[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int heads = 1 << p.hg_log2;
+  pdl_wait_primary();
+  const int per = (ctas + kMergeThreads - 1) / kMergeThreads;
+  const int c0 = min(tid * per, ctas), c1 = min(c0 + per, ctas);
+  int mine = 0, most = 0;
+  for (int i = c0; i < c1; ++i) {
+    const int n = p.records[i].n;
+    if (n > 0) mine += p.records[i].rows << p.hg_log2;
+    most = max(most, n);
+  }
+  int incl = mine;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, m);
+    if (lane >= m) incl += x;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 0) s_most[warp] = most;
+  __syncthreads();
+  int run = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) run += s_sum[w];
+    total += s_sum[w];
+    most = max(most, s_most[w]);
+  }
+  for (int i = c0; i < c1; ++i) {
+    s_off[i] = run;
+    if (p.records[i].n > 0) run += p.records[i].rows << p.hg_log2;
+  }
+  if (tid == 0) s_off[ctas] = total;
+  __syncthreads();
+  const bool alone = most <= 32;         // a warp a row
+  const int step = alone ? gridDim.x * WARPS : gridDim.x;
+  for (int item = alone ? blockIdx.x * WARPS + warp : blockIdx.x; item < total; item += step) {
+    int lo = 0, hi = ctas;               // the last record that begins at or before the item
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_off[mid] <= item) lo = mid;
+      else hi = mid;
+    }
+    const MergeRecord rec = p.records[lo];
+    const int hr = item - s_off[lo];
+    const int head = hr / rec.rows;
+    const int rr = hr - head * rec.rows;
+    const int i0 = alone ? 0 : rec.n * warp / WARPS, i1 = alone ? rec.n : rec.n * (warp + 1) / WARPS;
+    float M, Z;
+    float4 v[K];
+    merge_range<D>(p, rec, head * HW + rr, heads * HW, i0, i1, lane, M, Z, v);
+    if (!alone) {
+      __syncthreads();                   // (an earlier row's values are read)
+      if (lane == 0) {
+        s_m[warp] = M;
+        s_z[warp] = Z;
+      }
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (lane * 4 < D) *reinterpret_cast<float4*>(&s_v[warp][lane * 4 + 128 * k]) = v[k];
+      __syncthreads();
+      if (warp != 0) continue;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_m[w]);
+      M = top;
+      Z = 0.f;
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - top);
+        Z = fmaf(s_z[w], f, Z);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_v[w][(lane * 4) % D + 128 * k]);
+          v[k].x = fmaf(x.x, f, v[k].x);
+          v[k].y = fmaf(x.y, f, v[k].y);
+          v[k].z = fmaf(x.z, f, v[k].z);
+          v[k].w = fmaf(x.w, f, v[k].w);
+        }
+      }
+    }
+    float f;
+    uint16_t* outp = finish_row(p, rec.qs, rec.kvh0 + head, rec.row0 + rr, Z == 0.f ? -INFINITY : M + lg2(Z), lane == 0, f);
+    f = Z == 0.f ? 0.f : f / Z;
+    if (lane * 4 < D) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        uint32_t* w32 = reinterpret_cast<uint32_t*>(outp + lane * 4 + 128 * k);            // (rows are 4-byte aligned)
+        w32[0] = pack_bf16x2(v[k].x * f, v[k].y * f);
+        w32[1] = pack_bf16x2(v[k].z * f, v[k].w * f);
+      }
+    }
   }
 }
 
@@ -745,7 +896,19 @@ cudaError_t launch_split(const CUtensorMap& tmk, const CUtensorMap& tmv, const B
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, T::THREADS, T::SMEM, stream>>>(tmk, tmv, p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || grid.x == 1) return e;         // (one share holds every row whole)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(std::min(grid.x, 304u));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = (grid.x + 1) * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, block_merge_kernel<D, NH8 * 8>, p, static_cast<int>(grid.x));
 }
 
 // ---- chunks ------------------------------------------------------------------
@@ -893,27 +1056,25 @@ ChunkScratch chunk_scratch(const pa_block_shape& s, int64_t group) {
 int rows_of(const pa_block_shape& s) { return std::max(s.max_new, 1) * (s.num_q_heads / s.num_kv_heads); }
 int nh8_of(const pa_block_shape& s) { return rows_of(s) <= 8 ? 1 : 2; }
 
-// kv heads a CTA takes, as a log2: a power of two that divides Hkv, at most its warps, and no more than
-// leave kGroups groups of heads over all requests: the splits of a group are merged by one CTA.
-constexpr int kGroups = 64;
-
+// kv heads a CTA takes, as a log2: a power of two that divides Hkv, at most its warps
 int heads_log2(const pa_block_shape& s, int warps) {
   int l = 0;
-  while ((2 << l) <= warps && s.num_kv_heads % (2 << l) == 0 &&
-         static_cast<int64_t>(s.max_batch) * (s.num_kv_heads >> (l + 1)) >= kGroups)
-    ++l;
+  while ((2 << l) <= warps && s.num_kv_heads % (2 << l) == 0) ++l;
   return l;
 }
 
 // Above this many rows a kv head (of one request) the chunked form is taken.
 constexpr int kSplitRows = 64;
 
+constexpr int64_t kMaxCtas = 4096;
+
 // Fewest keys of one head that a CTA of the split kernel is given, so that what a share costs once stays small.
-constexpr int kLeastKeys = 512;
+constexpr int kLeastKeys = 128;
 
 int64_t split_scratch(const pa_block_shape& s, int64_t ctas, int hg) {
   const int64_t rows = 2 * ctas * nh8_of(s) * 8 << hg;
-  return kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256) + align_up(rows * 4, 256);
+  return kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256) + align_up(rows * 4, 256) +
+         ctas * static_cast<int64_t>(sizeof(MergeRecord));
 }
 
 pa_status validate(const pa_block_shape& s) {
@@ -945,7 +1106,8 @@ pa_status plan_split(const pa_block_shape& s, const int32_t* lens, int32_t batch
   // one wave, or fewer CTAs where the lengths (or capacities) give none of them its least share
   const int64_t least = std::max<int64_t>(1, kLeastKeys / (v.warps * 16));
   const int64_t wave = std::min<int64_t>(s.num_ctas > 0 ? s.num_ctas : static_cast<int64_t>(num_sms) * v.ctas,
-                                         kMergeCounters);
+                                         kMaxCtas);
+  if (s.max_batch * ctas_y * tiles(max_n) > INT32_MAX) return PA_ERR_UNSUPPORTED;      // (the kernel counts in 32 bits)
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(wave, cdiv(units, least)));
   out->chunked = 0;
   out->tile_tokens = TS;
@@ -1054,7 +1216,7 @@ extern "C" pa_status pa_block_attend(
       return PA_ERR_INVALID_ARG;
     if (!query_start_loc && batch > 0) return PA_ERR_INVALID_ARG;      // (one row a request: a plan of max_new 1)
   } else {
-    if (plan->ctas < 1 || plan->ctas > kMergeCounters || plan->min_tiles < 1 || plan->row_groups != groups ||
+    if (plan->ctas < 1 || plan->ctas > kMaxCtas || plan->min_tiles < 1 || plan->row_groups != groups ||
         plan->head_group != 1 << hg || plan->tile_tokens != 16 * (v.warps >> hg) || plan->smem_bytes != v.smem ||
         plan->scratch_bytes < split_scratch(s, plan->ctas, hg))
       return PA_ERR_INVALID_ARG;
@@ -1123,9 +1285,9 @@ extern "C" pa_status pa_block_attend(
     const int64_t rows = static_cast<int64_t>(2) * plan->ctas * NH << hg;
     p.o_part = reinterpret_cast<float*>(sc + kScratchHeaderBytes);
     p.lse_part = reinterpret_cast<float*>(sc + kScratchHeaderBytes + align_up(rows * s.head_dim * 4, 256));
+    p.records = reinterpret_cast<MergeRecord*>(reinterpret_cast<uint8_t*>(p.lse_part) + align_up(rows * 4, 256));
     p.min_tiles = plan->min_tiles;
     p.hg_log2 = hg;
-    p.merge_cnt = reinterpret_cast<uint32_t*>(sc + kMergeCounterOffset);
     p.err = reinterpret_cast<uint32_t*>(sc);
     const dim3 grid(plan->ctas);
     cudaError_t e;

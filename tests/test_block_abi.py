@@ -46,7 +46,7 @@ def test_plans(lib):
     p = _plan()
     assert p.chunked == 0 and p.row_groups == 1 and p.ctas >= 152 and p.smem_bytes <= 232448
     rows = 2 * p.ctas * p.head_group * 16                 # two parts a CTA, 16 rows a head
-    assert p.scratch_bytes == pb.SCRATCH_HEADER_BYTES + rows * 128 * 4 + rows * 4
+    assert p.scratch_bytes == pb.SCRATCH_HEADER_BYTES + rows * 128 * 4 + rows * 4 + 32 * p.ctas
     assert _plan(max_new=1, max_total_q=64).row_groups == 1
     assert _plan(max_new=16).row_groups == 4 and _plan(max_new=16).chunked == 0
     c = _plan(max_new=17)
@@ -59,11 +59,11 @@ def test_plans(lib):
     assert _plan(max_batch=1, max_pages_per_seq=8, max_total_q=1, max_new=1).ctas <= 8
     assert _plan(host_seq_lens=[100] * 4).ctas < _plan(host_seq_lens=[8000] * 64).ctas == p.ctas
     assert _plan(num_ctas=5).ctas == 5
-    # a CTA takes as many heads as divide Hkv, up to its warps, and then as many more keys; few requests: one head
+    # a CTA takes as many heads as divide Hkv, up to its warps, and then as many more keys
     def heads(h, batch=64):
         q = _plan(num_kv_heads=h, num_q_heads=h, max_new=1, max_batch=batch)
         return q.head_group, q.tile_tokens * q.head_group
-    assert [heads(h)[0] for h in (1, 2, 3, 4, 6, 8)] == [1, 2, 1, 4, 2, 4] and heads(8, 1)[0] == 1
+    assert [heads(h)[0] for h in (1, 2, 3, 4, 6, 8)] == [1, 2, 1, 4, 2, 4] and heads(8, 1)[0] == 4
     assert len({heads(h)[1] for h in (1, 2, 3, 8)}) == 1
     assert _plan(max_batch=0, max_total_q=0, max_pages_per_seq=0).ctas == 1
 
