@@ -53,11 +53,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kWeightBias = 14.f;           // weights are at most 2^14 (f16 holds 65504)
 constexpr float kLeastScale = 0x1p-100f;      // V scales below count as this one: its log2 and inverse are finite
 
-// Rows whose parts lie in several shares: part 0 at place0, part i at place 2 (share + i).
+// Rows whose parts lie in several shares: part 0 at place 2 share + 1, part i at place 2 (share + i).
 struct MergeRecord {
   int n;                      // parts; 0: no record
-  int place0, share;
-  int qs, kvh0, row0, rows, pad;
+  int share;
+  int qs, kvh0, row0, rows, pad[2];
 };
 static_assert(sizeof(MergeRecord) == 32, "two 16-byte loads a record");
 
@@ -92,7 +92,7 @@ template <int D, int NH8> struct Choice;
 template <> struct Choice<64, 1> { static constexpr int W = 8, NS = 4, CPS = 2; };
 template <> struct Choice<64, 2> { static constexpr int W = 4, NS = 4, CPS = 3; };
 template <> struct Choice<128, 1> { static constexpr int W = 4, NS = 3, CPS = 3; };
-template <> struct Choice<128, 2> { static constexpr int W = 4, NS = 2, CPS = 3; };
+template <> struct Choice<128, 2> { static constexpr int W = 4, NS = 3, CPS = 2; };
 template <> struct Choice<256, 1> { static constexpr int W = 4, NS = 2, CPS = 2; };
 template <> struct Choice<256, 2> { static constexpr int W = 4, NS = 4, CPS = 1; };
 
@@ -105,7 +105,7 @@ struct Traits {
   static constexpr int KS = D / 16;                 // 16-code units per row
   static constexpr int HW = NH8 * 8;
   static constexpr int THREADS = (W + 1) * 32;
-  static constexpr int STATES = W * HW * (D + 2) * 4;
+  static constexpr int STATES = W * (8 * D + 2 * HW) * 4;
   static constexpr int SMEM = 1024 + NS * STAGE + STATES + 2 * NS * 8;
   static_assert(RB == 128 || RB == 64, "row bytes must use the 128B or 64B swizzle");
 
@@ -118,12 +118,21 @@ struct Traits {
   }
 };
 
-// What a request brings: its rows, the tiles of TS keys they attend to, and units = tiles x groups of
-// heads x groups of rows.
+// What a request brings: its rows, the tiles of TS keys they attend to, its (group of heads, group of rows)
+// pairs y, and how much of a CTA's share they take.  A tile of more than 8 rows costs 1.4 to 1.5 times one of
+// up to 8 (two products instead of one under the same conversions); a y begun costs about a tile and a half
+// (q, scales, parts).
+constexpr int kTileWeight = 4, kWideWeight = 6, kStartWeight = 6;
+
 struct Request {
   int L, qs, n_new;
   int lo, tile0, n_tiles;
   int ys;                // groups of heads x groups of rows
+  int weight;            // of a tile in a CTA's share
+  __device__ __forceinline__ int units() const { return n_tiles > 0 ? n_tiles * weight + kStartWeight : 0; }   // a y
+  // the first tile of a y that begins at or behind position `at` of its units: a tile belongs to the share that
+  // holds its last unit, and what a y costs once comes with its first
+  __device__ __forceinline__ int tile_at(int at) const { return max(0, at - kStartWeight) / weight; }
 };
 
 // (false: a length or packing beyond the plan)
@@ -132,6 +141,7 @@ __device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts
   r.qs = p.qsl != nullptr ? p.qsl[b] : b;
   r.n_new = p.qsl != nullptr ? p.qsl[b + 1] - r.qs : 1;
   r.lo = r.tile0 = r.n_tiles = r.ys = 0;
+  r.weight = hw > 8 && r.n_new * p.group > 8 ? kWideWeight : kTileWeight;
   if (r.n_new == 0) return true;
   if (r.n_new < 0 || r.n_new > p.max_new || r.qs < 0 || static_cast<int64_t>(r.qs) + r.n_new > p.total_q || r.L < 0 ||
       r.L > p.max_kv || (p.qsl != nullptr && r.L < r.n_new)) {
@@ -188,8 +198,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* states = reinterpret_cast<float*>(smem + NS * T::STAGE);   // [W][HW][D], then [W][HW] maxima and sums
-  float* wm = states + W * T::HW * D;
+  float* states = reinterpret_cast<float*>(smem + NS * T::STAGE);   // [W][8][D], then [W][HW] maxima and sums
+  float* wm = states + W * 8 * D;
   float* wl = wm + W * T::HW;
   uint64_t* full = reinterpret_cast<uint64_t*>(wl + W * T::HW);
   uint64_t* empty = full + NS;
@@ -212,7 +222,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   for (int b = b0; b < b1; ++b) {
     Request r;
     if (!load_request(p, b, TS, T::HW, hgroups, r) && cta == 0) atomicOr(p.err, kErrCapacity);
-    mine += r.n_tiles * r.ys;
+    mine += r.units() * r.ys;
   }
   // (decode of an empty request: no key, O = 0 and the LSE the sink's or -inf)
   if (p.qsl == nullptr)
@@ -240,8 +250,10 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     if (w < warp) before += s_sum[w];
     total += s_sum[w];
   }
-  // shares of at least min_tiles units: the first `more` of one unit more than the others
-  const int C = min(static_cast<int>(gridDim.x), (total + p.min_tiles - 1) / p.min_tiles);
+  // shares of at least min_tiles tiles (and a wide one: a share between two others of a y then holds a tile of
+  // it): the first `more` of one unit more than the others
+  const int least = max(p.min_tiles * kTileWeight, kWideWeight);
+  const int C = min(static_cast<int>(gridDim.x), max(total > 0 ? 1 : 0, total / least));
   pdl_launch_dependents();             // (the merge kernel waits for this grid's end)
   if (cta >= C) return;
   const int share = total / C, more = total - share * C;
@@ -250,41 +262,41 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     const int m = more * (share + 1);
     return u < m ? u / (share + 1) : more + (u - m) / share;
   };
-  int at = begin;
-  int left = share + (cta < more ? 1 : 0);
-  if (before <= at && at < before + mine) {
+  const int end = begin + share + (cta < more ? 1 : 0);
+  if (before <= begin && begin < before + mine) {
     int u = before;
     int b = b0;
     for (;; ++b) {
       Request r;
       load_request(p, b, TS, T::HW, hgroups, r);
-      const int n = r.n_tiles * r.ys;
-      if (at < u + n) break;
+      const int n = r.units() * r.ys;
+      if (begin < u + n) break;
       u += n;
     }
     s_first = b;
-    s_at = at - u;
+    s_at = u;
   }
   __syncthreads();
-  // place of the walk over the share: request, group of heads and rows, tile; both the fetching warp and the
+  // place of the walk over the share: request and y, whose units begin at `pair0`; both the fetching warp and the
   // compute warps walk it, the former a ring ahead
   int b = s_first;
   Request r;
   load_request(p, b, TS, T::HW, hgroups, r);
-  int y = s_at / r.n_tiles;
-  int tile = s_at - y * r.n_tiles;
-  auto advance = [&](int n) {            // n tiles of a (request, y) done
-    at += n;
-    left -= n;
-    tile += n;
-    if (left <= 0 || tile < r.n_tiles) return;
-    tile = 0;
-    if (++y < r.ys) return;
+  int y = (begin - s_at) / r.units();
+  int pair0 = s_at + y * r.units();
+  // its tiles that belong to this share
+  auto tile_begin_of = [&]() { return r.tile_at(begin - pair0); };
+  auto tile_end_of = [&]() { return min(r.n_tiles, r.tile_at(end - pair0)); };
+  auto advance = [&]() {                 // to the next y; whether it begins in this share
+    pair0 += r.units();
+    if (pair0 >= end) return false;
+    if (++y < r.ys) return true;
     y = 0;
     do {
       ++b;
       load_request(p, b, TS, T::HW, hgroups, r);
     } while (r.n_tiles == 0);            // (units are left, so a request with some follows)
+    return true;
   };
   const int ps = p.page_size;
   const int ps_log2 = __ffs(ps) - 1;
@@ -303,8 +315,9 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     // ---- the fetching warp: a stage's boxes lie one after the other, [head][slot] rows each ----
     const int box = br * T::RB << p.hg_log2;
     int it = 0;
-    while (left > 0) {
-      const int n = min(left, r.n_tiles - tile);
+    do {
+      const int tile = tile_begin_of(), n = tile_end_of() - tile;
+      if (n <= 0) continue;
       const int kvh0 = (y % hgroups) << p.hg_log2;
       const int tile_begin = r.tile0 + tile;
       const int tok_lo = max(r.lo, tile_begin * TS), tok_hi = min(r.L, (tile_begin + n) * TS);
@@ -338,8 +351,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
           }
         }
       }
-      advance(n);
-    }
+    } while (advance());
     return;
   }
 
@@ -356,32 +368,34 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       (static_cast<uint32_t>(key0 / br) * (br << p.hg_log2) + hw * br + key0 % br) * T::RB;
   bool dead = false;                                     // a wait ran out: no more results
   int it = 0;
-  while (left > 0) {
-    const int n = min(left, r.n_tiles - tile);
+  do {
+    const int tile = tile_begin_of(), n = tile_end_of() - tile;
+    if (n <= 0) continue;
     const int kvh0 = (y % hgroups) << p.hg_log2;
     const int kvh = kvh0 + hw;
     const int row0 = (y / hgroups) * T::HW;              // first (token, head) row
     const int R = min(r.n_new * G - row0, T::HW);
     const int tile_begin = r.tile0 + tile;
     const int tok_lo = max(r.lo, tile_begin * TS), tok_hi = min(r.L, (tile_begin + n) * TS);
-    // scales of this head's pages: lane i holds those of page base + i; a page wholly before the window
-    // adds nothing, whatever its scales hold by now
-    float page_k, page_v;
-    auto scales_of = [&](int i) {
+    // scales of this head's pages: lane i holds those of page base + i, and the next 32 pages' are on their way;
+    // a page wholly before the window adds nothing, whatever its scales hold by now
+    auto scales_of = [&](int i, float& ks, float& vs) {
       const int id = page_coord(i, tok_lo, tok_hi, false);
       const bool in = id < p.num_pages && ((i + 1) << ps_log2) > tok_lo;
       const int64_t sa = static_cast<int64_t>(in ? id : 0) * p.scale_stride + kvh;
-      page_k = in ? p.k_scales[sa] : 0.f;
-      page_v = lg2(in ? fmaxf(p.v_scales[sa], kLeastScale) : kLeastScale);
+      ks = in ? p.k_scales[sa] : 0.f;
+      vs = in ? p.v_scales[sa] : 0.f;
     };
     int base = (tile_begin * TS) >> ps_log2;
-    scales_of(base + lane);
+    float page_k, page_v, next_k, next_v;
+    scales_of(base + lane, page_k, page_v);
+    scales_of(base + 32 + lane, next_k, next_v);
+    page_v = lg2(fmaxf(page_v, kLeastScale));
 
     // Q^T fragments (B operand): unit ks of a row holds dims 16 ks ..; thread c has
     // codes 4c .. 4c + 3 of it.  Each row times 2^e with its largest value in [2^14, 2^15).
     uint32_t qf[T::KS][NH8][2];
     float rsl[NH8][2];         // the score factor of this thread's two accumulator rows
-    int rpos[NH8][2];          // and their positions
 #pragma unroll
     for (int j = 0; j < NH8; ++j) {
       const int rr = j * 8 + g;
@@ -415,7 +429,6 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       for (int h = 0; h < 2; ++h) {
         const uint32_t er = __shfl_sync(0xffffffffu, e, (2 * c + h) * 4);
         rsl[j][h] = (CAP ? p.scale_over_cap : p.scale_log2) * __uint_as_float((er - 14u) << 23);
-        rpos[j][h] = r.L - r.n_new + (row0 + min(j * 8 + 2 * c + h, R - 1)) / G;
       }
     }
     float m_run[NH8][2], l_run[NH8][2];
@@ -432,6 +445,9 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     // keys [full_lo, full_hi) are seen by every row: other 16-key groups mask each element
     const int full_lo = max(tok_lo, p.window > 0 ? r.L - p.window : 0);
     const int full_hi = min(tok_hi, r.L - r.n_new + 1);
+    // (a request that brings at most 8 rows beside others of up to 16: NJ = 1 leaves the second 8 out)
+    auto tiles = [&](auto nj_tag) {
+    constexpr int NJ = decltype(nj_tag)::value;
     for (int k = 0; k < n; ++k, ++it) {
       const int stage = it % NS;
       const int t0 = (tile_begin + k) * TS + key0;         // this warp's first key
@@ -439,7 +455,9 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       const int pg = t0 >> ps_log2;
       if (pg - base >= 32) {
         base += 32;
-        scales_of(base + lane);
+        page_k = next_k;
+        page_v = lg2(fmaxf(next_v, kLeastScale));
+        scales_of(base + 32 + lane, next_k, next_v);
       }
       const float ks = __shfl_sync(0xffffffffu, page_k, pg - base);
       const float lv = __shfl_sync(0xffffffffu, page_v, pg - base);
@@ -449,9 +467,9 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       const uint32_t vst_u = kst_u + T::TILE;
       const bool partial = (t0 < full_lo) || (t0 + 16 > full_hi);
       // ---- S^T = K Q^T over the codes ----------------------------------------
-      float s[NH8][4];
+      float s[NJ][4];
 #pragma unroll
-      for (int j = 0; j < NH8; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
 #pragma unroll
@@ -474,14 +492,14 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
             a[3] = e4m3x2_to_f16x2<1>(w[2 * v + 1]);
           }
 #pragma unroll
-          for (int j = 0; j < NH8; ++j) mma_f16(s[j], a, qf[u + v][j][0], qf[u + v][j][1]);
+          for (int j = 0; j < NJ; ++j) mma_f16(s[j], a, qf[u + v][j][0], qf[u + v][j][1]);
         }
       }
 
       // ---- scales, soft-cap, mask; online softmax (log2 domain) --------------
-      float mx[NH8][2];
+      float mx[NJ][2];
 #pragma unroll
-      for (int j = 0; j < NH8; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         const float f[2] = {ks * rsl[j][0], ks * rsl[j][1]};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -494,18 +512,18 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       }
       if (partial) {
 #pragma unroll
-        for (int j = 0; j < NH8; ++j)
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int tok = t0 + g + ((e >> 1) << 3);
-            const int pos = rpos[j][e & 1];
+            const int pos = r.L - r.n_new + (row0 + min(j * 8 + 2 * c + (e & 1), R - 1)) / G;
             if (tok < tok_lo || tok >= tok_hi || tok > pos || (p.window > 0 && tok <= pos - p.window))
               s[j][e] = -INFINITY;
           }
       }
       bool grew = false;
 #pragma unroll
-      for (int j = 0; j < NH8; ++j)
+      for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float m = fmaxf(s[j][h], s[j][h + 2]);
@@ -518,7 +536,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       // the accumulators need rescaling only after a maximum rose somewhere in the warp
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-        for (int j = 0; j < NH8; ++j) {
+        for (int j = 0; j < NJ; ++j) {
           float alpha[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -537,9 +555,9 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
         }
       }
       const float iv = ex2(-lv);
-      uint32_t pb[NH8][2];
+      uint32_t pb[NJ][2];
 #pragma unroll
-      for (int j = 0; j < NH8; ++j) {
+      for (int j = 0; j < NJ; ++j) {
         float mu[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) mu[h] = m_run[j][h] == -INFINITY ? 0.f : m_run[j][h] - kWeightBias;
@@ -591,7 +609,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
               a[3] &= vm_hi;
             }
 #pragma unroll
-            for (int j = 0; j < NH8; ++j) mma_f16(o[u + v][j], a, pb[j][0], pb[j][1]);
+            for (int j = 0; j < NJ; ++j) mma_f16(o[u + v][j], a, pb[j][0], pb[j][1]);
           }
         }
       };
@@ -604,14 +622,19 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
+    };
+    if (NH8 == 2 && R <= 8) {
+      tiles(std::integral_constant<int, 1>{});
+    } else {
+      tiles(std::integral_constant<int, NH8>{});
+    }
 
     // ---- the rows' values, merged over a head's KW warps -----------------------------
-    // the shares that hold parts of this (request, y): first .. last; a share's first part goes to place 2 share,
-    // its last to 2 share + 1
-    const int pair0 = at - tile, pair1 = pair0 + r.n_tiles;
-    const int first = share_of(pair0), last = share_of(pair1 - 1);
+    // the shares that hold parts of this (request, y): first .. last; a part that begins it goes to place
+    // 2 share + 1, any other to 2 share
+    const int first = share_of(pair0 + kStartWeight + r.weight - 1), last = share_of(pair0 + r.units() - 1);
     const bool direct = first == last;
-    const int place = 2 * cta + (at != begin ? 1 : 0);
+    const int place = 2 * cta + (tile == 0 ? 1 : 0);
     float lse2[NH8][2];
 #pragma unroll
     for (int j = 0; j < NH8; ++j)
@@ -624,53 +647,49 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
         l_run[j][h] = l;
       }
     if (KW > 1) {
-      // the head's first warp takes the others' states from shared memory
-      compute_sync<W>();                                 // (an earlier part's are read)
+      // the states of a head's KW warps meet in shared memory, 8 rows at a time; each warp then has the units
+      // of 16 dims i with i % KW == kw
 #pragma unroll
-      for (int j = 0; j < NH8; ++j)
+      for (int j = 0; j < NH8; ++j) {
+        compute_sync<W>();                               // (earlier states are read)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int rr = j * 8 + 2 * c + h;
+          const int rr = 2 * c + h;
           if (g == 0) {
-            wm[warp * T::HW + rr] = m_run[j][h];
-            wl[warp * T::HW + rr] = l_run[j][h];
+            wm[warp * T::HW + j * 8 + rr] = m_run[j][h];
+            wl[warp * T::HW + j * 8 + rr] = l_run[j][h];
           }
 #pragma unroll
           for (int i = 0; i < T::KS; ++i)
-            *reinterpret_cast<float2*>(states + (warp * T::HW + rr) * D + 16 * i + 2 * g) =
+            *reinterpret_cast<float2*>(states + (warp * 8 + rr) * D + 16 * i + 2 * g) =
                 make_float2(o[i][j][h], o[i][j][h + 2]);
         }
-      compute_sync<W>();
-      // KW warps a head: each takes dims of its own, 16 i with i % KW == kw
-#pragma unroll
-      for (int j = 0; j < NH8; ++j)
+        compute_sync<W>();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int rr = j * 8 + 2 * c + h;
+          const int rr = 2 * c + h;
           float M = -INFINITY, den = 0.f;
-          for (int w = 0; w < KW; ++w) M = fmaxf(M, wm[((w << p.hg_log2) + hw) * T::HW + rr]);
+          for (int w = 0; w < KW; ++w) M = fmaxf(M, wm[((w << p.hg_log2) + hw) * T::HW + j * 8 + rr]);
           const float m_use = M == -INFINITY ? 0.f : M;
-          for (int w = 0; w < KW; ++w) {
-            const int sa = ((w << p.hg_log2) + hw) * T::HW + rr;
-            den += wl[sa] * ex2(wm[sa] - m_use);
-          }
           m_run[j][h] = M;
-          l_run[j][h] = den;
 #pragma unroll
-          for (int i = 0; i < T::KS; ++i) {
-            if ((i & (KW - 1)) != kw) continue;
-            float2 v = make_float2(0.f, 0.f);
-            for (int w = 0; w < KW; ++w) {
-              const int sa = ((w << p.hg_log2) + hw) * T::HW + rr;
-              const float f = ex2(wm[sa] - m_use);
-              const float2 x = *reinterpret_cast<const float2*>(states + sa * D + 16 * i + 2 * g);
-              v.x = fmaf(x.x, f, v.x);
-              v.y = fmaf(x.y, f, v.y);
+          for (int i = 0; i < T::KS; ++i)
+            if ((i & (KW - 1)) == kw) o[i][j][h] = o[i][j][h + 2] = 0.f;
+          for (int w = 0; w < KW; ++w) {
+            const int sw = (w << p.hg_log2) + hw;
+            const float f = ex2(wm[sw * T::HW + j * 8 + rr] - m_use);
+            den = fmaf(wl[sw * T::HW + j * 8 + rr], f, den);
+#pragma unroll
+            for (int i = 0; i < T::KS; ++i) {
+              if ((i & (KW - 1)) != kw) continue;
+              const float2 x = *reinterpret_cast<const float2*>(states + (sw * 8 + rr) * D + 16 * i + 2 * g);
+              o[i][j][h] = fmaf(x.x, f, o[i][j][h]);
+              o[i][j][h + 2] = fmaf(x.y, f, o[i][j][h + 2]);
             }
-            o[i][j][h] = v.x;
-            o[i][j][h + 2] = v.y;
           }
+          l_run[j][h] = den;
         }
+      }
     }
 #pragma unroll
     for (int j = 0; j < NH8; ++j)
@@ -702,9 +721,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
         }
       }
     if (!direct && cta == first && tid == 0)
-      p.records[cta] = MergeRecord{last - first + 1, place, first, r.qs, kvh0, row0, R, 0};
-    advance(n);
-  }
+      p.records[cta] = MergeRecord{last - first + 1, first, r.qs, kvh0, row0, R, {0, 0}};
+  } while (advance());
 }
 
 // ---- rows in several shares, merged by their LSEs ------------------------------------
@@ -725,7 +743,7 @@ __device__ __forceinline__ void merge_range(const BlockParams& p, const MergeRec
   for (int k = 0; k < K; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int d = (lane * 4) % D;
   auto row_of = [&](int i) {
-    return static_cast<int64_t>(i == 0 ? rec.place0 : 2 * (rec.share + i)) * place_rows + row_in_place;
+    return static_cast<int64_t>(2 * (rec.share + i) + (i == 0 ? 1 : 0)) * place_rows + row_in_place;
   };
   for (int base = i0; base < i1; base += U) {
     const int n = min(U, i1 - base);
@@ -1107,7 +1125,8 @@ pa_status plan_split(const pa_block_shape& s, const int32_t* lens, int32_t batch
   const int64_t least = std::max<int64_t>(1, kLeastKeys / (v.warps * 16));
   const int64_t wave = std::min<int64_t>(s.num_ctas > 0 ? s.num_ctas : static_cast<int64_t>(num_sms) * v.ctas,
                                          kMaxCtas);
-  if (s.max_batch * ctas_y * tiles(max_n) > INT32_MAX) return PA_ERR_UNSUPPORTED;      // (the kernel counts in 32 bits)
+  // (the kernel counts weighted tiles in 32 bits)
+  if (s.max_batch * ctas_y * (tiles(max_n) * kWideWeight + kStartWeight) > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(wave, cdiv(units, least)));
   out->chunked = 0;
   out->tile_tokens = TS;
