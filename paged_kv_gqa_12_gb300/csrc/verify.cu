@@ -107,26 +107,98 @@ __device__ __forceinline__ Pair lane_sums(Pair x, int lane) {
   return x;
 }
 
-// NaN and what is below 0 count as 0; the bound keeps sums of 2^20 entries finite.
-__device__ __forceinline__ float weight(float x) { return fminf(fmaxf(x, 0.f), 0x1p100f); }
+// NaN and what is below 0 count as 0.
+__device__ __forceinline__ float weight(float x) { return fmaxf(x, 0.f); }
 
-// How a row's entries become weights y.
+// Two sums side by side, in packed arithmetic (each instruction does both).
+struct Pairs {
+  float2 hi = {0.f, 0.f}, lo = {0.f, 0.f};
+  // adds max(p - q, 0) = max(p, q) - q (q >= 0): the difference and its rounding error, then both to the sum
+  __device__ __forceinline__ void add(float2 p, float2 q) {
+    const float2 m = make_float2(fmaxf(p.x, q.x), fmaxf(p.y, q.y));
+    const float2 nq = make_float2(-q.x, -q.y);
+    const float2 d = __fadd2_rn(m, nq);
+    const float2 t = __fadd2_rn(d, make_float2(-m.x, -m.y));                                   // -q as it was taken
+    const float2 e = __fadd2_rn(__fadd2_rn(m, sub(t, d)), sub(nq, t));
+    const float2 s = __fadd2_rn(hi, d);
+    const float2 u = sub(s, hi);
+    lo = __fadd2_rn(lo, __fadd2_rn(__fadd2_rn(sub(hi, sub(s, u)), sub(d, u)), e));
+    hi = s;
+  }
+  static __device__ __forceinline__ float2 sub(float2 a, float2 b) { return __fadd2_rn(a, make_float2(-b.x, -b.y)); }
+  __device__ __forceinline__ Pair both() const {
+    Pair r;
+    r.hi = hi.x;
+    r.lo = lo.x;
+    Pair o;
+    o.hi = hi.y;
+    o.lo = lo.y;
+    r.add(o);
+    return r;
+  }
+};
+
+// How a row's entries become weights y = max(p - q, 0).
 struct Row {
   const float* p;
   const float* q;       // null: nothing is taken off
   int taken;            // the certain draft whose entry loses 1, or -1
 
-  // adds y of entry v; whether it weighs anything
-  __device__ __forceinline__ bool add(Pair& sum, float pv, float qv, int v) const {
-    pv = weight(pv);
-    qv = q != nullptr ? weight(qv) : (v == taken ? 1.f : 0.f);
-    const float d = __fsub_rn(pv, qv);
-    if (d > 0.f) {
-      const float t = __fsub_rn(d, pv);
-      sum.add(d);
-      sum.lo = __fadd_rn(sum.lo, __fsub_rn(__fsub_rn(pv, __fsub_rn(d, t)), __fadd_rn(qv, t)));
+  __device__ __forceinline__ float less(int v) const {
+    return q != nullptr ? weight(__ldg(q + v)) : (v == taken ? 1.f : 0.f);
+  }
+  // the sum of a warp's entries [v, v1), v a multiple of kUnit; Q: there is a q
+  template <bool Q>
+  __device__ __forceinline__ Pair sum(int v, int v1, int lane) const {
+    Pairs s;
+    if (((reinterpret_cast<uintptr_t>(p) | (Q ? reinterpret_cast<uintptr_t>(q) : 0)) & 15u) == 0) {
+      constexpr int U = 4;               // 16 entries of p and q a lane in flight
+      for (; v + U * kUnit <= v1; v += U * kUnit) {
+        float4 a[U], c[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int at = v + u * kUnit + lane * 4;
+          a[u] = __ldg(reinterpret_cast<const float4*>(p + at));
+          if constexpr (Q) c[u] = __ldg(reinterpret_cast<const float4*>(q + at));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if constexpr (Q) {
+            x = make_float4(weight(c[u].x), weight(c[u].y), weight(c[u].z), weight(c[u].w));
+          } else {
+            const int at = taken - (v + u * kUnit + lane * 4);
+            if (static_cast<unsigned>(at) < 4u)
+              x = make_float4(at == 0 ? 1.f : 0.f, at == 1 ? 1.f : 0.f, at == 2 ? 1.f : 0.f, at == 3 ? 1.f : 0.f);
+          }
+          s.add(make_float2(a[u].x, a[u].y), make_float2(x.x, x.y));
+          s.add(make_float2(a[u].z, a[u].w), make_float2(x.z, x.w));
+        }
+      }
     }
-    return d > 0.f;
+    for (v += lane; v < v1; v += 8 * 32) {
+      float a[8], x[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int at = v + 32 * u;
+        a[u] = at < v1 ? __ldg(p + at) : 0.f;
+        x[u] = at < v1 ? less(at) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; u += 2) s.add(make_float2(a[u], a[u + 1]), make_float2(x[u], x[u + 1]));
+    }
+    return s.both();
+  }
+  // entry v to a sum; whether it weighs anything
+  __device__ __forceinline__ bool add(Pair& sum, int v) const {
+    Pairs one;
+    const float a = __ldg(p + v), x = less(v);
+    one.add(make_float2(a, 0.f), make_float2(x, 0.f));
+    Pair y;
+    y.hi = one.hi.x;
+    y.lo = one.lo.x;
+    sum.add(y);
+    return a > x;
   }
 };
 
@@ -200,32 +272,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   const int parts = C * kWarps;
   auto part_begin = [&](int w) { return static_cast<int>(static_cast<int64_t>(units) * w / parts) * kUnit; };
   for (int pass = 0; pass < 2; ++pass) {
-    Pair sum;
-    const int v1 = min(part_begin(rank * kWarps + warp + 1), p.vocab);
-    int v = part_begin(rank * kWarps + warp);
-    const bool wide = (reinterpret_cast<uintptr_t>(row.p) & 15u) == 0 && (reinterpret_cast<uintptr_t>(row.q) & 15u) == 0;
-    if (wide) {
-      constexpr int U = 4;               // 16 entries of p and q a lane in flight
-      for (; v + U * kUnit <= v1; v += U * kUnit) {
-        float4 a[U], c[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = v + u * kUnit + lane * 4;
-          a[u] = __ldg(reinterpret_cast<const float4*>(row.p + at));
-          c[u] = row.q != nullptr ? __ldg(reinterpret_cast<const float4*>(row.q + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int at = v + u * kUnit + lane * 4;
-          row.add(sum, a[u].x, c[u].x, at);
-          row.add(sum, a[u].y, c[u].y, at + 1);
-          row.add(sum, a[u].z, c[u].z, at + 2);
-          row.add(sum, a[u].w, c[u].w, at + 3);
-        }
-      }
-    }
-#pragma unroll 4
-    for (v += lane; v < v1; v += 32) row.add(sum, __ldg(row.p + v), row.q != nullptr ? __ldg(row.q + v) : 0.f, v);
+    const int v0 = part_begin(rank * kWarps + warp), v1 = min(part_begin(rank * kWarps + warp + 1), p.vocab);
+    Pair sum = row.q != nullptr ? row.sum<true>(v0, v1, lane) : row.sum<false>(v0, v1, lane);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
       Pair y;
@@ -317,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   int last = -1;
 #pragma unroll 4
   for (int v = a0; v < a1; ++v) {
-    if (row.add(own, row.p[v], row.q != nullptr ? row.q[v] : 0.f, v)) last = v;
+    if (row.add(own, v)) last = v;
   }
   const Pair incl = lane_sums(own, lane);
   if (lane == 31) s_scan[warp] = make_float2(incl.hi, incl.lo);
@@ -344,10 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   } else if (tid == best) {
     int pick = last;
     for (int v = a0; v < a1; ++v) {
-      Pair y;
-      const bool any = row.add(y, row.p[v], row.q != nullptr ? row.q[v] : 0.f, v);
-      before.add(y);
-      if (any && before.above(rest)) {
+      if (row.add(before, v) && before.above(rest)) {
         pick = v;
         break;
       }
