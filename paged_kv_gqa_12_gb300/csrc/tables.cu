@@ -25,7 +25,6 @@ namespace cg = cooperative_groups;
 namespace pa {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kMaxRequests = 8192;
 constexpr uint32_t kErrNoPages = PA_DEVICE_NO_PAGES;
 
@@ -33,6 +32,7 @@ struct TablesParams {
   const int32_t* ctx;
   const int32_t* fresh;
   int batch, page_size;
+  int ps_log2;                 // log2(page_size) where it is a power of two, else -1
   const int32_t* held;
   int32_t* held_out;
   int32_t* free_pages;
@@ -62,6 +62,13 @@ __device__ __forceinline__ int find(const int* off, int n, int x) {
   return lo;
 }
 
+// Sums stop at 2^30, which no limit of the call reaches: such a step is refused.
+constexpr int kFull = 1 << 30;
+__device__ __forceinline__ int capped(int a, int b) {
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), static_cast<unsigned>(kFull)));
+}
+
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x;
@@ -73,13 +80,13 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesParam
   int* back_off = need_off + B + 1;      // [B + 1] pages they return
   int* ctx_s = back_off + B + 1;
   int* held_s = ctx_s + B;
-  __shared__ long long s_sum[3][kThreads / 32];
+  __shared__ int s_sum[3][kThreads / 32];
 
   // ---- lengths and their prefix sums -------------------------------------
   const int count = *p.free_count;
   const int per = (B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  long long sum[3] = {0, 0, 0};
+  int sum[3] = {0, 0, 0};
   uint32_t bad = count < 0 || count > p.free_capacity ? kErrCapacity : 0u;
   for (int b = b0; b < b1; ++b) {
     const int ctx = p.ctx[b], fresh = p.fresh[b], held = p.held[b];
@@ -103,33 +110,38 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesParam
     tok_off[b] = n;
     need_off[b] = need;
     back_off[b] = back;
-    sum[0] += n;
-    sum[1] += need;
-    sum[2] += back;
+    sum[0] = capped(sum[0], n);
+    sum[1] = capped(sum[1], need);
+    sum[2] = capped(sum[2], back);
   }
-  long long incl[3] = {sum[0], sum[1], sum[2]};
+  int incl[3] = {sum[0], sum[1], sum[2]};
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl[k], m);
-      if (lane >= m) incl[k] += v;
+      const int v = __shfl_up_sync(0xffffffffu, incl[k], m);
+      if (lane >= m) incl[k] = capped(incl[k], v);
     }
   if (lane == 31)
 #pragma unroll
     for (int k = 0; k < 3; ++k) s_sum[k][warp] = incl[k];
   __syncthreads();
-  long long total[3] = {0, 0, 0};
-  long long run[3] = {incl[0] - sum[0], incl[1] - sum[1], incl[2] - sum[2]};
+  int total[3] = {0, 0, 0};
+  int run[3] = {0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w)
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      if (w < warp) run[k] += s_sum[k][w];
-      total[k] += s_sum[k][w];
+      const int v = s_sum[k][w];
+      if (w < warp) run[k] = capped(run[k], v);
+      total[k] = capped(total[k], v);
     }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) run[k] += incl[k] - sum[k];
+  // (count and the sums are at most 2^30: 64 bits for their sum)
   const long long top_l = static_cast<long long>(count) + total[2];
-  if (total[0] > p.max_tokens || top_l - total[1] > p.free_capacity) bad |= kErrCapacity;
+  if (total[0] > p.max_tokens || max(total[1], total[2]) >= kFull || top_l - total[1] > p.free_capacity)
+    bad |= kErrCapacity;
   if (total[1] > top_l) bad |= kErrNoPages;
   bad = __syncthreads_or(bad & kErrCapacity) ? kErrCapacity : (bad & kErrNoPages);   // (the rest is the same in all threads)
   const bool ok = bad == 0;
@@ -137,17 +149,17 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesParam
     // lengths in place become the sums before them (all fit: they are at most the totals checked above)
     for (int b = b0; b < b1; ++b) {
       const int n = tok_off[b], need = need_off[b], back = back_off[b];
-      tok_off[b] = static_cast<int>(run[0]);
-      need_off[b] = static_cast<int>(run[1]);
-      back_off[b] = static_cast<int>(run[2]);
+      tok_off[b] = run[0];
+      need_off[b] = run[1];
+      back_off[b] = run[2];
       run[0] += n;
       run[1] += need;
       run[2] += back;
     }
     if (tid == 0) {
-      tok_off[B] = static_cast<int>(total[0]);
-      need_off[B] = static_cast<int>(total[1]);
-      back_off[B] = static_cast<int>(total[2]);
+      tok_off[B] = total[0];
+      need_off[B] = total[1];
+      back_off[B] = total[2];
     }
   } else if (tid == 0 && cluster.block_rank() == 0 && p.err != nullptr) {
     atomicOr(p.err, bad);
@@ -158,34 +170,58 @@ __global__ void __launch_bounds__(kThreads) step_tables_kernel(const TablesParam
 
   const int gt = static_cast<int>(cluster.block_rank()) * kThreads + tid;
   const int stride = static_cast<int>(cluster.num_blocks()) * kThreads;
-  const int tokens = ok ? static_cast<int>(total[0]) : 0;
+  const int tokens = ok ? total[0] : 0;
   if (ok) {
-    const int need = static_cast<int>(total[1]);
+    const int need = total[1];
     const int top = static_cast<int>(top_l);
-    // entry `at` of the stack: what ended requests held lies in their rows, which this call does not write
-    auto stack = [&](int at) {
-      if (at < count) return p.free_pages[at];
+    // where entry `at` of the stack lies: what ended requests held is in their rows, which this call does not write
+    auto stack = [&](int at) -> const int32_t* {
+      if (at < count) return p.free_pages + at;
       const int e = at - count;
       const int b = find(back_off, B, e);
-      return p.block_table[static_cast<int64_t>(b) * p.bt_stride + (e - back_off[b])];
+      return p.block_table + static_cast<int64_t>(b) * p.bt_stride + (e - back_off[b]);
     };
+    // four consecutive tokens a thread: one search, and mostly one page
+    constexpr int U = 4;
+    for (int t0 = gt * U; t0 < tokens; t0 += stride * U) {
+      int b = find(tok_off, B, t0);
+      const int32_t* where[U];
+      int pos[U], rest[U];
+      int last_pg = -1, last_b = -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = min(t0 + u, tokens - 1);
+        while (t >= tok_off[b + 1]) ++b;
+        pos[u] = ctx_s[b] + (t - tok_off[b]);
+        const int pg = p.ps_log2 >= 0 ? pos[u] >> p.ps_log2 : pos[u] / p.page_size;
+        rest[u] = pos[u] - pg * p.page_size;
+        if (u > 0 && pg == last_pg && b == last_b) {
+          where[u] = where[u - 1];
+        } else {
+          where[u] = pg < held_s[b] ? p.block_table + static_cast<int64_t>(b) * p.bt_stride + pg
+                                    : stack(top - 1 - (need_off[b] + pg - held_s[b]));
+        }
+        last_pg = pg;
+        last_b = b;
+      }
+      int id[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) id[u] = *where[u];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t0 + u >= tokens) break;
+        const bool in = static_cast<unsigned>(id[u]) < static_cast<unsigned>(p.num_pages);
+        if (!in && p.err != nullptr) atomicOr(p.err, kErrPageId);
+        p.slots[t0 + u] = in ? static_cast<int64_t>(id[u]) * p.page_size + rest[u] : -1;
+        p.positions[t0 + u] = pos[u];
+      }
+    }
     for (int k = gt; k < need; k += stride) {
       const int b = find(need_off, B, k);
-      p.block_table[static_cast<int64_t>(b) * p.bt_stride + held_s[b] + (k - need_off[b])] = stack(top - 1 - k);
+      p.block_table[static_cast<int64_t>(b) * p.bt_stride + held_s[b] + (k - need_off[b])] = *stack(top - 1 - k);
     }
     // what is left of the returned pages goes behind the entries that stay (entries below `count` are only read)
-    for (int at = count + gt; at < top - need; at += stride) p.free_pages[at] = stack(at);
-    for (int t = gt; t < tokens; t += stride) {
-      const int b = find(tok_off, B, t);
-      const int pos = ctx_s[b] + (t - tok_off[b]);
-      const int pg = pos / p.page_size;
-      const int id = pg < held_s[b] ? p.block_table[static_cast<int64_t>(b) * p.bt_stride + pg]
-                                    : stack(top - 1 - (need_off[b] + pg - held_s[b]));
-      const bool in = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages);
-      if (!in && p.err != nullptr) atomicOr(p.err, kErrPageId);
-      p.slots[t] = in ? static_cast<int64_t>(id) * p.page_size + (pos - pg * p.page_size) : -1;
-      p.positions[t] = pos;
-    }
+    for (int at = count + gt; at < top - need; at += stride) p.free_pages[at] = *stack(at);
   }
   for (int t = tokens + gt; t < p.max_tokens; t += stride) {
     p.slots[t] = -1;
@@ -242,6 +278,7 @@ extern "C" pa_status pa_step_tables(const int32_t* context_lens, const int32_t* 
   p.fresh = new_lens;
   p.batch = batch;
   p.page_size = page_size;
+  p.ps_log2 = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(static_cast<unsigned>(page_size)) : -1;
   p.held = page_counts;
   p.held_out = page_counts_out;
   p.free_pages = free_pages;
@@ -258,13 +295,16 @@ extern "C" pa_status pa_step_tables(const int32_t* context_lens, const int32_t* 
   p.positions = positions;
   p.max_tokens = max_tokens;
   p.err = static_cast<uint32_t*>(scratch);
+  // few requests and tokens: one small CTA, whose barriers are short; many: a cluster of eight
+  const bool small = batch <= 128 && max_tokens <= 512;
+  const int ctas = max_tokens + batch > 4096 ? 8 : 1;
+  auto kern = small ? step_tables_kernel<128> : step_tables_kernel<512>;
   constexpr int kMaxSmem = (5 * kMaxRequests + 3) * 4;
-  if (cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  const int ctas = max_tokens + batch > 4096 ? 8 : 1;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(small ? 128 : 512);
   cfg.dynamicSmemBytes = static_cast<size_t>(5 * batch + 3) * 4;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -273,6 +313,6 @@ extern "C" pa_status pa_step_tables(const int32_t* context_lens, const int32_t* 
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_tables_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  cfg.numAttrs = ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
