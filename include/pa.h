@@ -494,8 +494,8 @@ typedef enum { PA_CODE_E4M3 = 0, PA_CODE_INT8 = 1 } pa_code;
 
 /* Append new tokens' K and V to an 8-bit cache with a scale for each page and kv head.  The last
  * n_b tokens of request b's seq_lens[b] are new (n_b = query_start_loc[b+1] - query_start_loc[b];
- * 1 with query_start_loc NULL, then num_tokens == batch), packed rows query_start_loc[b] .. of
- * k_new / v_new.  For each page and kv head that gets some of them
+ * with query_start_loc NULL 1, or 0 where seq_lens[b] is 0, and num_tokens == batch), packed rows
+ * query_start_loc[b] .. of k_new / v_new.  For each page and kv head that gets some of them
  *   scale = fp32(max |x| over its new tokens / Q), Q = 448 or 127,
  *           or the page's old scale if that is larger and the page keeps older tokens
  *   code  = x / scale, rounded to the nearest code (ties to even), never beyond +-Q
@@ -600,8 +600,8 @@ pa_status pa_block_attend(const pa_block_plan_t* plan,
  * 44 bits.  out_tokens[b] gets the accepted drafts, the drawn token and then -1 (to its width), num_tokens[b] the accepted drafts + 1.  n_b = 1 is plain
  * sampling; n_b = 0 gives no token.  If no probability of the row is positive the token is -1.
  *   tokens, accept_u  device int32 / fp32 [total_rows]; sample_u device fp32 [batch]; u in [0, 1)
- *   target_probs, draft_probs  device fp32 [total_rows, vocab], rows their stride apart; NaN and
- *                  negative values count as 0
+ *   target_probs, draft_probs  device fp32 [total_rows, vocab] (at most 2^20 entries), rows their stride
+ *                  apart; finite: NaN and negative values count as 0
  *   out_tokens     device int32 [batch, out_width], rows out_stride apart; num_tokens device int32 [batch]
  *   scratch        optional (may be NULL), as for pa_append_kv: PA_DEVICE_CAPACITY where a request's rows are more
  *                  than out_width or lie outside total_rows (its outputs are left untouched)

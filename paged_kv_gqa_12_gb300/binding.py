@@ -727,8 +727,8 @@ def block_attend(p: PaBlockPlan, q, k_cache, v_cache, k_scales, v_scales, block_
     of codes with scales per page and kv head.  out: bf16 like q, lse: fp32 [rows, Hq]."""
     dev, s = _device(q), p.shape
     qs, os_ = q.stride(), out.stride()
-    if q.dtype is not _BF16 or out.dtype is not _BF16 or out.get_device() != dev or len(qs) != 3 or qs[-1] != 1 \
-            or len(os_) != 3 or os_[-1] != 1:
+    if q.dtype is not _BF16 or out.dtype is not _BF16 or q.get_device() != dev or out.get_device() != dev \
+            or len(qs) != 3 or qs[-1] != 1 or len(os_) != 3 or os_[-1] != 1:
         _typed("q", q, _BF16, 3, dev)
         _typed("out", out, _BF16, 3, dev)
     rows, hq, D = q.shape
@@ -763,7 +763,7 @@ def verify_tokens(tokens, target_probs, query_start_loc, accept_u, sample_u, out
     [batch])."""
     dev = _device(target_probs)
     B, (T, V), ts = num_tokens.shape[0], target_probs.shape, target_probs.stride()
-    if target_probs.dtype is not _F32 or ts[-1] != 1:
+    if target_probs.dtype is not _F32 or target_probs.get_device() != dev or ts[-1] != 1:
         _typed("target_probs", target_probs, _F32, 2, dev)
     dp, ds = None, (0, 0)
     if draft_probs is not None:

@@ -87,7 +87,11 @@ struct BlockParams {
   uint32_t* err;
 };
 
-// Compute warps a CTA, stages of its ring, CTAs an SM.
+// Compute warps a CTA, stages of its ring, CTAs an SM.  Measured (64 requests of 512 to 8191 tokens, e4m3, us):
+// heads of 64, up to 8 rows (8, 4, 2) 60.6, (4, 5, 3) 64.1, (8, 3, 3) 74.4, (4, 6, 4) 85.0; of 128 (4, 3, 3) 99.3,
+// (8, 3, 1) 105.8, (8, 2, 2) 109.6, (4, 4, 3: two fit) 123.7; of 256 (4, 2, 2) 179.3, (8, 2, 1) 181.8, (4, 3, 1) 195.6;
+// up to 16 rows, one to four tokens each: heads of 64 (4, 4, 3) 67.7, (8, 4, 2) 77.0; of 128 (4, 3, 2) 120.8, (4, 2, 2)
+// 139.4 ((4, 2, 3) spills 400 bytes: 236); of 256 (4, 4, 1) 271, (8, 2, 1: 168 registers, spills) 435.
 template <int D, int NH8> struct Choice;
 template <> struct Choice<64, 1> { static constexpr int W = 8, NS = 4, CPS = 2; };
 template <> struct Choice<64, 2> { static constexpr int W = 4, NS = 4, CPS = 3; };
@@ -1081,12 +1085,19 @@ int heads_log2(const pa_block_shape& s, int warps) {
   return l;
 }
 
-// Above this many rows a kv head (of one request) the chunked form is taken.
-constexpr int kSplitRows = 64;
+// Above this many rows a kv head (of one request) the chunked form is taken.  It copies the codes and has no
+// parts of a context, so it wants requests enough to fill the card (two CTAs an SM).  Measured, split / chunked, groups
+// of 4, int8, us: 64 requests of up to 8192 tokens, 12 rows each 435 / 485, 16 rows 571 / 487; 4 such requests, 32
+// rows (128 a kv head) 141 / 165; one of 131071 tokens, 32 rows 495 / 1803.
+bool chunked_form(const pa_block_shape& s) {
+  const bool fills = static_cast<int64_t>(s.max_batch) * s.num_kv_heads >= 2 * static_cast<int64_t>(s.num_sms);
+  return rows_of(s) > (fills ? 48 : 128);
+}
 
 constexpr int64_t kMaxCtas = 4096;
 
-// Fewest keys of one head that a CTA of the split kernel is given, so that what a share costs once stays small.
+// Fewest keys of one head that a CTA of the split kernel is given (four requests of 60 to 1000 tokens: 11.6 us with 128,
+// 12.3 with 256, 15.1 with 512).
 constexpr int kLeastKeys = 128;
 
 int64_t split_scratch(const pa_block_shape& s, int64_t ctas, int hg) {
@@ -1198,8 +1209,7 @@ extern "C" pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* h
   std::memset(&p, 0, sizeof p);
   p.shape = *shape;
   p.shape.num_sms = num_sms;
-  st = rows_of(*shape) <= kSplitRows ? plan_split(*shape, host_seq_lens, batch, num_sms, &p)
-                                     : plan_chunks(*shape, &p);
+  st = chunked_form(p.shape) ? plan_chunks(*shape, &p) : plan_split(*shape, host_seq_lens, batch, num_sms, &p);
   if (st != PA_OK) return st;
   *plan = p;
   return PA_OK;
@@ -1223,7 +1233,7 @@ extern "C" pa_status pa_block_attend(
   if (!aligned(scratch, 256)) return PA_ERR_UNSUPPORTED;
   // a plan edited by hand must match what its shape lays out
   const bool chunked = plan->chunked != 0;
-  if (chunked != (rows_of(s) > kSplitRows)) return PA_ERR_INVALID_ARG;
+  if (chunked != chunked_form(s)) return PA_ERR_INVALID_ARG;
   const int NH = nh8_of(s) * 8;
   const int groups = static_cast<int>(cdiv(rows_of(s), NH));
   const Variant v = variant_of(s.head_dim, NH / 8);

@@ -83,6 +83,19 @@ def test_decode(kind, B, Hkv):
     _same(s, got)
 
 
+def test_decode_of_a_padded_batch():
+    # requests of length 0 bring nothing, and are no error
+    s = _problem(31, "int8", 2, 128, 16, [30, 0, 5, 0], [1, 1, 1, 1])
+    s["seq"][1] = s["seq"][3] = 0
+    got, code = _run(s, decode=True)
+    assert code == 0
+    H = s["Hkv"]
+    for name, x in (("k", s["kv"][:, :H]), ("v", s["kv"][:, H:])):
+        v, sc = ref.append("int8", x[[0, 2]], s[name + "_cache"], s[name + "_scales"], s["table"][[0, 2]], [31, 6],
+                           [0, 1, 2], 16)
+        assert torch.equal(ref.values(got[name + "_cache"]), v) and torch.equal(got[name + "_scales"], sc)
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_many_rows(kind):
     s = _problem(3, kind, 8, 128, 16, [0, 300, 17, 0, 1000, 3], [700, 1, 1200, 0, 333, 16])

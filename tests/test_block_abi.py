@@ -48,9 +48,11 @@ def test_plans(lib):
     rows = 2 * p.ctas * p.head_group * 16                 # two parts a CTA, 16 rows a head
     assert p.scratch_bytes == pb.SCRATCH_HEADER_BYTES + rows * 128 * 4 + rows * 4 + 32 * p.ctas
     assert _plan(max_new=1, max_total_q=64).row_groups == 1
-    assert _plan(max_new=16).row_groups == 4 and _plan(max_new=16).chunked == 0
-    c = _plan(max_new=17)
+    assert _plan(max_new=12).row_groups == 3 and _plan(max_new=12).chunked == 0
+    c = _plan(max_new=13)
     assert c.chunked == 1 and 1 <= c.group_requests <= 64
+    # requests too few to fill the card in chunks: up to 128 rows a kv head are split
+    assert _plan(max_new=32, max_batch=4).row_groups == 8 and _plan(max_new=33, max_batch=4).chunked == 1
     # a copy of at most 2 GiB, or of one request
     assert c.group_requests * 512 * 16 * 8 * 128 * 4 <= 1 << 31
     one = _plan(max_new=100, max_pages_per_seq=1 << 17)
