@@ -636,7 +636,7 @@ def _vector(name, t, dtype, n, dev):
     """Pointer of a contiguous [n] tensor."""
     if t.dtype is not dtype or t.get_device() != dev or t.stride() != (1,):
         _typed(name, t, dtype, 1, dev)
-    if t.shape[0] != n:
+    if t.numel() != n:
         raise ValueError(f"{name} must be [{n}]")
     return t.data_ptr()
 
@@ -649,18 +649,18 @@ def step_tables(context_lens, new_lens, page_counts, free_pages, free_count, blo
     free_pages / free_count: the pool's stack (int32 [capacity] / [1]).  Without page_counts_out / free_count_out the
     counts are updated in place."""
     dev = _device(context_lens)
-    B, bts, (rows, width) = context_lens.shape[0], block_table.stride(), block_table.shape
+    B, bts, (rows, width) = context_lens.numel(), block_table.stride(), block_table.shape
     if block_table.dtype is not _I32 or block_table.get_device() != dev or bts[-1] != 1:
         _typed("block_table", block_table, _I32, 2, dev)
     if rows < B:
         raise ValueError("block_table must have a row per request")
     held = _vector("page_counts", page_counts, _I32, B, dev)
     count = _vector("free_count", free_count, _I32, 1, dev)
-    tokens = slots.shape[0]
+    tokens, pool = slots.numel(), free_pages.numel()
     status = load().pa_step_tables(
         _vector("context_lens", context_lens, _I32, B, dev), _vector("new_lens", new_lens, _I32, B, dev), B, page_size,
         held, held if page_counts_out is None else _vector("page_counts_out", page_counts_out, _I32, B, dev),
-        _vector("free_pages", free_pages, _I32, free_pages.shape[0], dev), free_pages.shape[0], count,
+        _vector("free_pages", free_pages, _I32, pool, dev), pool, count,
         count if free_count_out is None else _vector("free_count_out", free_count_out, _I32, 1, dev), num_pages,
         block_table.data_ptr(), bts[0], width, _vector("seq_lens", seq_lens, _I32, B, dev),
         _vector("query_start_loc", query_start_loc, _I32, B + 1, dev), _vector("slots", slots, _I64, tokens, dev),
@@ -762,7 +762,7 @@ def verify_tokens(tokens, target_probs, query_start_loc, accept_u, sample_u, out
     target_probs and draft_probs (fp32 [T, vocab]; None: drafts are certain), accept_u (fp32 [T]), sample_u (fp32
     [batch])."""
     dev = _device(target_probs)
-    B, (T, V), ts = num_tokens.shape[0], target_probs.shape, target_probs.stride()
+    B, (T, V), ts = num_tokens.numel(), target_probs.shape, target_probs.stride()
     if target_probs.dtype is not _F32 or target_probs.get_device() != dev or ts[-1] != 1:
         _typed("target_probs", target_probs, _F32, 2, dev)
     dp, ds = None, (0, 0)

@@ -346,7 +346,7 @@ __device__ __forceinline__ void dequant_tile(uint8_t* tile, float scale, int lan
 
 // BLK: K and V hold 8-bit codes (exact, K as bf16, V as f16) with a scale for each page and kv
 // head.  The softmax folds both in: x = s (scale ks) log2 e + log2 vs, weights p = 2^(x - m + 7)
-// (f16, at most 2^15 with the lazy maximum; half a step 2^-12) meet the codes of V, and the
+// (f16, at most 2^15 with the lazy maximum; half a step 2^-11) meet the codes of V, and the
 // denominator sums p / vs.  Such weights need no second part.
 constexpr float kBlkBias = 7.f;
 

@@ -9,9 +9,13 @@
 // A call moves kilobytes: what bounds it is the launch and two trips to memory
 // (the lengths, then the tables).  So it is one kernel whose CTAs (one, or a
 // cluster of eight where there are many tokens) each make all prefix sums for
-// themselves in shared memory and then share tokens and pages; a token finds its
-// request by bisection.  The counts and lengths are written behind a cluster
-// barrier, because they may lie where the inputs do.
+// themselves in shared memory and then share tokens and pages; a thread finds the
+// request of four consecutive tokens by bisection.  The counts and lengths are
+// written behind a cluster barrier, because they may lie where the inputs do.
+//
+// Measured (one GB300, CUDA-graph replay): 4 requests of one token 4.1 us (an empty
+// launch is about 2.5), 250 requests with 40 prompts, 10214 tokens, 8.9 us; there a CTA
+// takes 26 us of searches for all tokens, so clusters of 4 / 2 / 1 take 13.7 / 19 / 30.
 #include <cstdint>
 
 #include <cooperative_groups.h>
@@ -299,13 +303,16 @@ extern "C" pa_status pa_step_tables(const int32_t* context_lens, const int32_t* 
   const bool small = batch <= 128 && max_tokens <= 512;
   const int ctas = max_tokens + batch > 4096 ? 8 : 1;
   auto kern = small ? step_tables_kernel<128> : step_tables_kernel<512>;
+  // (a kernel's limit is set to its most, and only by calls that need more than 48 KB)
   constexpr int kMaxSmem = (5 * kMaxRequests + 3) * 4;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
+  const size_t smem = static_cast<size_t>(5 * batch + 3) * 4;
+  if (smem > 49152 - 512 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess)
     return PA_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(small ? 128 : 512);
-  cfg.dynamicSmemBytes = static_cast<size_t>(5 * batch + 3) * 4;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

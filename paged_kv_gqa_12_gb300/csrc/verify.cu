@@ -16,6 +16,12 @@
 // A request has a cluster of CTAs: every warp sums a contiguous part of the row, the
 // parts' sums go to all CTAs over distributed shared memory, and the CTA whose warp
 // holds the crossing sums that part again, a few entries a thread.
+//
+// Measured (one GB300, CUDA-graph replay): 64 requests of up to four drafts, 131072
+// entries, 46 MB read on average (a request whose drafts are all accepted needs no q)
+// 16.0 us; 19.8 with one entry an instruction instead of two.  One request of 32000
+// entries 6.2 us: what is left is latency (lengths, tokens, their probabilities, the
+// row, two cluster barriers).
 #include <cstdint>
 
 #include <cooperative_groups.h>
