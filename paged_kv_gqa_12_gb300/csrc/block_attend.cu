@@ -36,8 +36,8 @@
 // requests of 512 to 8191 tokens int8 99.9 us, 5.7 TB/s; one of 131071 e4m3 54 us, eight
 // of them 325 us, 6.6 TB/s (97 % of the copy bandwidth); of each call about 15 us are
 // prefix sum and first loads (5 us), uneven shares (5) and the merge (5).  Up to four
-// rows a request (16 a kv head) 121 us: 168 registers leave 8 compute warps an SM, whose
-// dependent instructions are not hidden.
+// rows a request (16 a kv head) 114 us: 168 registers leave 8 compute warps an SM, whose
+// dependent instructions are not hidden (two groups of 16 keys a warp at a time hide some).
 //
 // Many rows a request (chunks): see "chunks" below.
 #include <algorithm>
@@ -94,27 +94,39 @@ struct BlockParams {
   uint32_t* err;
 };
 
-// Compute warps a CTA, stages of its ring, CTAs an SM.  Measured (64 requests of 512 to 8191 tokens, e4m3, us):
-// heads of 64, up to 8 rows (8, 4, 2) 60.6, (4, 5, 3) 64.1, (8, 3, 3) 74.4, (4, 6, 4) 85.0; of 128 (4, 3, 3) 99.3,
-// (8, 3, 1) 105.8, (8, 2, 2) 109.6, (4, 4, 3: two fit) 123.7; of 256 (4, 2, 2) 179.3, (8, 2, 1) 181.8, (4, 3, 1) 195.6;
-// up to 16 rows, one to four tokens each: heads of 64 (4, 4, 3) 67.7, (8, 4, 2) 77.0; of 128 (4, 3, 2) 120.8, (4, 2, 2)
-// 139.4 ((4, 2, 3) spills 400 bytes: 236); of 256 (4, 4, 1) 271, (8, 2, 1: 168 registers, spills) 435.
+// Compute warps a CTA, stages of its ring, CTAs an SM, groups of 16 keys a warp and stage.  Measured with one group
+// (64 requests of 512 to 8191 tokens, e4m3, us): heads of 64, up to 8 rows (8, 4, 2) 60.6, (4, 5, 3) 64.1, (8, 3, 3)
+// 74.4, (4, 6, 4) 85.0; of 128 (4, 3, 3) 99.3, (8, 3, 1) 105.8, (8, 2, 2) 109.6, (4, 4, 3: two fit) 123.7; of 256 (4,
+// 2, 2) 179.3, (8, 2, 1) 181.8, (4, 3, 1) 195.6; up to 16 rows, one to four tokens each: heads of 64 (4, 4, 3) 67.7,
+// (8, 4, 2) 77.0; of 128 (4, 3, 2) 120.8, (4, 2, 2) 139.4 ((4, 2, 3) spills 400 bytes: 236); of 256 (4, 4, 1) 271, (8,
+// 2, 1: 168 registers, spills) 435.
+// Two groups: one maximum, rescaling and wait for 32 keys, and the second group's products beside the first's softmax.
+// Up to 16 rows, heads of 64 67.4 -> 66.0 ((4, 3, 2): 156 registers), of 128 120.2 -> 114 ((4, 2, 2): 168, and up to 140
+// bytes spilled); 16 requests of 2 to 8 K tokens 47.8 -> 48.6 (a tile is longer).  Up to 8 rows as they were (heads of
+// 128 99.1, one long request 54.4 for 54.2): one group.
 template <int D, int NH8> struct Choice;
-template <> struct Choice<64, 1> { static constexpr int W = 8, NS = 4, CPS = 2; };
-template <> struct Choice<64, 2> { static constexpr int W = 4, NS = 4, CPS = 3; };
-template <> struct Choice<128, 1> { static constexpr int W = 4, NS = 3, CPS = 3; };
-template <> struct Choice<128, 2> { static constexpr int W = 4, NS = 3, CPS = 2; };
-template <> struct Choice<256, 1> { static constexpr int W = 4, NS = 2, CPS = 2; };
-template <> struct Choice<256, 2> { static constexpr int W = 4, NS = 4, CPS = 1; };
+template <> struct Choice<64, 1> { static constexpr int W = 8, NS = 4, CPS = 2, MT = 1; };
+template <> struct Choice<64, 2> { static constexpr int W = 4, NS = 3, CPS = 2, MT = 2; };
+template <> struct Choice<128, 1> { static constexpr int W = 4, NS = 3, CPS = 3, MT = 1; };
+template <> struct Choice<128, 2> { static constexpr int W = 4, NS = 2, CPS = 2, MT = 2; };
+template <> struct Choice<256, 1> { static constexpr int W = 4, NS = 2, CPS = 2, MT = 1; };
+template <> struct Choice<256, 2> { static constexpr int W = 4, NS = 4, CPS = 1, MT = 1; };
 
-template <int D, int NH8, int W, int NS>
+// How much of a CTA's share a tile takes, and a (group of heads, group of rows) begun.  A tile of more than 8 rows costs
+// 1.4 to 1.5 times one of up to 8 (two products instead of one under the same conversions), with two groups 1.25
+// times (64 requests of 4 to 16 rows, us: 4 122, 5 114, 6 116); a beginning about a tile and a half (q, scales, parts).
+constexpr int kTileWeight = 4, kStartWeight = 6;
+constexpr int wide_weight(int groups) { return groups > 1 ? 5 : 6; }
+
+template <int D, int NH8, int W, int NS, int MT>
 struct Traits {
   static constexpr int RB = D < 128 ? D : 128;      // bytes per TMA box row
   static constexpr int NCC = D / RB;                // column chunks per key row
-  static constexpr int TILE = W * 16 * D;           // K (or V) bytes per stage
+  static constexpr int TILE = W * MT * 16 * D;      // K (or V) bytes per stage
   static constexpr int STAGE = 2 * TILE;
   static constexpr int KS = D / 16;                 // 16-code units per row
   static constexpr int HW = NH8 * 8;
+  static constexpr int WIDE = wide_weight(MT);      // units of a tile of more than 8 rows
   static constexpr int THREADS = (W + 1) * 32;
   static constexpr int STATES = W * (8 * D + 2 * HW) * 4;
   static constexpr int SMEM = 1024 + NS * STAGE + STATES + 2 * NS * 8;
@@ -129,12 +141,7 @@ struct Traits {
   }
 };
 
-// What a request brings: its rows, the tiles of TS keys they attend to, its (group of heads, group of rows)
-// pairs y, and how much of a CTA's share they take.  A tile of more than 8 rows costs 1.4 to 1.5 times one of
-// up to 8 (two products instead of one under the same conversions); a y begun costs about a tile and a half
-// (q, scales, parts).
-constexpr int kTileWeight = 4, kWideWeight = 6, kStartWeight = 6;
-
+// What a request brings: its rows, the tiles of TS keys they attend to, its (group of heads, group of rows) pairs y.
 struct Request {
   int L, qs, n_new;
   int lo, tile0, n_tiles;
@@ -147,12 +154,14 @@ struct Request {
 };
 
 // (false: a length or packing beyond the plan)
-__device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts, int hw, int hgroups, Request& r) {
+template <class T>
+__device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts, int hgroups, Request& r) {
+  constexpr int hw = T::HW;
   r.L = p.seq_lens[b];
   r.qs = p.qsl != nullptr ? p.qsl[b] : b;
   r.n_new = p.qsl != nullptr ? p.qsl[b + 1] - r.qs : 1;
   r.lo = r.tile0 = r.n_tiles = r.ys = 0;
-  r.weight = hw > 8 && r.n_new * p.group > 8 ? kWideWeight : kTileWeight;
+  r.weight = hw > 8 && r.n_new * p.group > 8 ? T::WIDE : kTileWeight;
   if (r.n_new == 0) return true;
   if (r.n_new < 0 || r.n_new > p.max_new || r.qs < 0 || static_cast<int64_t>(r.qs) + r.n_new > p.total_q || r.L < 0 ||
       r.L > p.max_kv || (p.qsl != nullptr && r.L < r.n_new)) {
@@ -165,6 +174,10 @@ __device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts
   r.n_tiles = (r.L + ts - 1) / ts - r.tile0;
   r.ys = hgroups * ((r.n_new * p.group + hw - 1) / hw);
   return true;
+}
+
+__device__ __forceinline__ void st_shared_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(addr), "r"(0) : "memory");
 }
 
 // All W compute warps of the CTA (the fetching warp does not take part).
@@ -192,14 +205,14 @@ __device__ __forceinline__ uint16_t* finish_row(const BlockParams& p, int qs, in
   return p.out + orow * p.out_stride_tok + static_cast<int64_t>(hq) * p.out_stride_head;
 }
 
-template <int D, bool I8, int NH8, int W, int NS, bool CAP>
+template <int D, bool I8, int NH8, int W, int NS, int MT, bool CAP>
 __global__ void __launch_bounds__((W + 1) * 32, (Choice<D, NH8>::CPS))
 block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                    const BlockParams p) {
-  using T = Traits<D, NH8, W, NS>;
+  using T = Traits<D, NH8, W, NS, MT>;
   const int HG = 1 << p.hg_log2;
   const int KW = W >> p.hg_log2;                         // groups of 16 keys a stage
-  const int TS = 16 * KW;
+  const int TS = 16 * MT * KW;
   const int hgroups = p.num_kv_heads >> p.hg_log2;
   const int G = p.group;
   const int tid = threadIdx.x;
@@ -232,7 +245,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   int mine = 0;                                          // (the plan keeps all sums below 2^31)
   for (int b = b0; b < b1; ++b) {
     Request r;
-    if (!load_request(p, b, TS, T::HW, hgroups, r) && cta == 0) atomicOr(p.err, kErrCapacity);
+    if (!load_request<T>(p, b, TS, hgroups, r) && cta == 0) atomicOr(p.err, kErrCapacity);
     mine += r.units() * r.ys;
   }
   // (decode of an empty request: no key, O = 0 and the LSE the sink's or -inf)
@@ -263,7 +276,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   }
   // shares of at least min_tiles tiles (and a wide one: a share between two others of a y then holds a tile of
   // it): the first `more` of one unit more than the others
-  const int least = max(p.min_tiles * kTileWeight, kWideWeight);
+  const int least = max(p.min_tiles * kTileWeight, T::WIDE);
   const int C = min(static_cast<int>(gridDim.x), max(total > 0 ? 1 : 0, total / least));
   pdl_launch_dependents();             // (the merge kernel waits for this grid's end)
   if (cta >= C) return;
@@ -279,7 +292,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     int b = b0;
     for (;; ++b) {
       Request r;
-      load_request(p, b, TS, T::HW, hgroups, r);
+      load_request<T>(p, b, TS, hgroups, r);
       const int n = r.units() * r.ys;
       if (begin < u + n) break;
       u += n;
@@ -292,7 +305,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   // compute warps walk it, the former a ring ahead
   int b = s_first;
   Request r;
-  load_request(p, b, TS, T::HW, hgroups, r);
+  load_request<T>(p, b, TS, hgroups, r);
   int y = (begin - s_at) / r.units();
   int pair0 = s_at + y * r.units();
   // its tiles that belong to this share
@@ -305,7 +318,7 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     y = 0;
     do {
       ++b;
-      load_request(p, b, TS, T::HW, hgroups, r);
+      load_request<T>(p, b, TS, hgroups, r);
     } while (r.n_tiles == 0);            // (units are left, so a request with some follows)
     return true;
   };
@@ -370,13 +383,17 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
   const int g = lane >> 2;
   const int c = lane & 3;
   const int hw = warp & (HG - 1);                        // head of the group
-  const int kw = warp >> p.hg_log2;                      // 16-key group of a stage
+  const int kw = warp >> p.hg_log2;                      // MT 16-key groups of a stage
   const int mi = lane >> 3, mr = lane & 7;
   const int row = mr + ((mi & 1) << 3);
-  // where this warp's 16 rows lie in a stage
-  const int key0 = kw * 16;
-  const uint32_t smem_u = smem_u32(smem) +
-      (static_cast<uint32_t>(key0 / br) * (br << p.hg_log2) + hw * br + key0 % br) * T::RB;
+  // where this warp's groups of 16 rows lie in a stage
+  const int key0 = kw * MT * 16;
+  uint32_t place_u[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int key = key0 + 16 * mt;
+    place_u[mt] = smem_u32(smem) + (static_cast<uint32_t>(key / br) * (br << p.hg_log2) + hw * br + key % br) * T::RB;
+  }
   bool dead = false;                                     // a wait ran out: no more results
   int it = 0;
   do {
@@ -457,87 +474,104 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     const int full_lo = max(tok_lo, p.window > 0 ? r.L - p.window : 0);
     const int full_hi = min(tok_hi, r.L - r.n_new + 1);
     // (a request that brings at most 8 rows beside others of up to 16: NJ = 1 leaves the second 8 out)
+    const int pos0 = r.L - r.n_new;                     // position of the first row's token
     auto tiles = [&](auto nj_tag) {
     constexpr int NJ = decltype(nj_tag)::value;
     for (int k = 0; k < n; ++k, ++it) {
       const int stage = it % NS;
-      const int t0 = (tile_begin + k) * TS + key0;         // this warp's first key
-      // (a page beyond the sequence's last holds only masked keys, any scale will do)
-      const int pg = t0 >> ps_log2;
-      if (pg - base >= 32) {
+      // (kept from the compiler, or it holds every offset from it in a register of its own: 200 bytes spilled)
+      int t0 = (tile_begin + k) * TS + key0;
+      asm volatile("" : "+r"(t0));         // this warp's first key
+      // (a tile's pages lie in one run of 32; a page beyond the sequence's last holds only masked keys, any
+      // scale will do)
+      if ((t0 >> ps_log2) - base >= 32) {
         base += 32;
         page_k = next_k;
         page_v = lg2(fmaxf(next_v, kLeastScale));
         scales_of(base + 32 + lane, next_k, next_v);
       }
-      const float ks = __shfl_sync(0xffffffffu, page_k, pg - base);
-      const float lv = __shfl_sync(0xffffffffu, page_v, pg - base);
+      float ks[MT], lv[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int from = ((t0 + 16 * mt) >> ps_log2) - base;
+        ks[mt] = __shfl_sync(0xffffffffu, page_k, from);
+        lv[mt] = __shfl_sync(0xffffffffu, page_v, from);
+      }
       dead = dead || !__all_sync(0xffffffffu, mbar_wait(&full[stage], (it / NS) & 1, p.err));
       if (dead) continue;
-      const uint32_t kst_u = smem_u + stage * T::STAGE;
-      const uint32_t vst_u = kst_u + T::TILE;
-      const bool partial = (t0 < full_lo) || (t0 + 16 > full_hi);
+      const bool partial = (t0 < full_lo) || (t0 + 16 * MT > full_hi);
+
       // ---- S^T = K Q^T over the codes ----------------------------------------
-      float s[NJ][4];
+      float s[MT][NJ][4];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
+      for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+        for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int u = 0; u < T::KS; u += 2) {
-        uint32_t w[4];               // keys 0-7 and 8-15 of unit u, then of unit u + 1
-        ldsm_x4(w, kst_u + T::unit(row, u + (mi >> 1)));
+          for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
+        const uint32_t kst_u = place_u[mt] + stage * T::STAGE;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          uint32_t a[4];
-          if constexpr (I8) {
-            const uint32_t x0 = w[2 * v] ^ 0x80808080u, x1 = w[2 * v + 1] ^ 0x80808080u;
-            a[0] = int8x2_to_f16x2<0x4140>(x0);
-            a[1] = int8x2_to_f16x2<0x4140>(x1);
-            a[2] = int8x2_to_f16x2<0x4342>(x0);
-            a[3] = int8x2_to_f16x2<0x4342>(x1);
-          } else {
-            a[0] = e4m3x2_to_f16x2<0>(w[2 * v]);
-            a[1] = e4m3x2_to_f16x2<0>(w[2 * v + 1]);
-            a[2] = e4m3x2_to_f16x2<1>(w[2 * v]);
-            a[3] = e4m3x2_to_f16x2<1>(w[2 * v + 1]);
+        for (int u = 0; u < T::KS; u += 2) {
+          uint32_t w[4];               // keys 0-7 and 8-15 of unit u, then of unit u + 1
+          ldsm_x4(w, kst_u + T::unit(row, u + (mi >> 1)));
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            uint32_t a[4];
+            if constexpr (I8) {
+              const uint32_t x0 = w[2 * v] ^ 0x80808080u, x1 = w[2 * v + 1] ^ 0x80808080u;
+              a[0] = int8x2_to_f16x2<0x4140>(x0);
+              a[1] = int8x2_to_f16x2<0x4140>(x1);
+              a[2] = int8x2_to_f16x2<0x4342>(x0);
+              a[3] = int8x2_to_f16x2<0x4342>(x1);
+            } else {
+              a[0] = e4m3x2_to_f16x2<0>(w[2 * v]);
+              a[1] = e4m3x2_to_f16x2<0>(w[2 * v + 1]);
+              a[2] = e4m3x2_to_f16x2<1>(w[2 * v]);
+              a[3] = e4m3x2_to_f16x2<1>(w[2 * v + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) mma_f16(s[mt][j], a, qf[u + v][j][0], qf[u + v][j][1]);
           }
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) mma_f16(s[j], a, qf[u + v][j][0], qf[u + v][j][1]);
         }
       }
 
       // ---- scales, soft-cap, mask; online softmax (log2 domain) --------------
       float mx[NJ][2];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const float f[2] = {ks * rsl[j][0], ks * rsl[j][1]};
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (CAP) {
-            s[j][e] = fmaf(p.cap_log2, tanhf(s[j][e] * f[e & 1]), lv);
-          } else {
-            s[j][e] = fmaf(s[j][e], f[e & 1], lv);
-          }
-        }
-      }
-      if (partial) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < NJ; ++j) {
+          const float f[2] = {ks[mt] * rsl[j][0], ks[mt] * rsl[j][1]};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int tok = t0 + g + ((e >> 1) << 3);
-            const int pos = r.L - r.n_new + (row0 + min(j * 8 + 2 * c + (e & 1), R - 1)) / G;
-            if (tok < tok_lo || tok >= tok_hi || tok > pos || (p.window > 0 && tok <= pos - p.window))
-              s[j][e] = -INFINITY;
+            if constexpr (CAP) {
+              s[mt][j][e] = fmaf(p.cap_log2, tanhf(s[mt][j][e] * f[e & 1]), lv[mt]);
+            } else {
+              s[mt][j][e] = fmaf(s[mt][j][e], f[e & 1], lv[mt]);
+            }
           }
+        }
+      if (partial) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int tok = t0 + 16 * mt + g + ((e >> 1) << 3);
+              const int pos = pos0 + (row0 + min(j * 8 + 2 * c + (e & 1), R - 1)) / G;
+              if (tok < tok_lo || tok >= tok_hi || tok > pos || (p.window > 0 && tok <= pos - p.window))
+                s[mt][j][e] = -INFINITY;
+            }
       }
       bool grew = false;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float m = fmaxf(s[j][h], s[j][h + 2]);
+          float m = fmaxf(s[0][j][h], s[0][j][h + 2]);
+#pragma unroll
+          for (int mt = 1; mt < MT; ++mt) m = fmaxf(m, fmaxf(s[mt][j][h], s[mt][j][h + 2]));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -565,36 +599,46 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
           }
         }
       }
-      const float iv = ex2(-lv);
-      uint32_t pb[NJ][2];
+      uint32_t pb[MT][NJ][2];
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        float mu[2];
+      for (int mt = 0; mt < MT; ++mt) {
+        const float iv = ex2(-lv[mt]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) mu[h] = m_run[j][h] == -INFINITY ? 0.f : m_run[j][h] - kWeightBias;
+        for (int j = 0; j < NJ; ++j) {
+          float mu[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][e] = ex2(s[j][e] - mu[e & 1]);
-        l_run[j][0] = fmaf(s[j][0] + s[j][2], iv, l_run[j][0]);
-        l_run[j][1] = fmaf(s[j][1] + s[j][3], iv, l_run[j][1]);
-        pb[j][0] = movmatrix_t(pack_f16x2(s[j][0], s[j][1]));
-        pb[j][1] = movmatrix_t(pack_f16x2(s[j][2], s[j][3]));
+          for (int h = 0; h < 2; ++h) mu[h] = m_run[j][h] == -INFINITY ? 0.f : m_run[j][h] - kWeightBias;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][j][e] = ex2(s[mt][j][e] - mu[e & 1]);
+          l_run[j][0] = fmaf(s[mt][j][0] + s[mt][j][2], iv, l_run[j][0]);
+          l_run[j][1] = fmaf(s[mt][j][1] + s[mt][j][3], iv, l_run[j][1]);
+          pb[mt][j][0] = movmatrix_t(pack_f16x2(s[mt][j][0], s[mt][j][1]));
+          pb[mt][j][1] = movmatrix_t(pack_f16x2(s[mt][j][2], s[mt][j][3]));
+        }
       }
 
       // ---- O^T += V^T P^T over the codes ---------------------------------------
-      auto pv = [&](auto mask_tag) {
-        constexpr bool MASK = decltype(mask_tag)::value;
-        // masked keys have P = 0, but their codes may be stale (NaN in e4m3): zeroed
-        uint32_t vm_lo = 0xffffffffu, vm_hi = 0xffffffffu;
-        if constexpr (MASK) {
-          const int tk = t0 + 2 * c;
-          auto valid = [&](int t) { return t >= tok_lo && t < tok_hi; };
-          vm_lo = (valid(tk) ? 0x0000ffffu : 0u) | (valid(tk + 1) ? 0xffff0000u : 0u);
-          vm_hi = (valid(tk + 8) ? 0x0000ffffu : 0u) | (valid(tk + 9) ? 0xffff0000u : 0u);
+      const uint32_t vst_u = stage * T::STAGE + T::TILE;
+      // masked keys have P = 0, but their codes may be stale, NaN in e4m3: zeroed, in this warp's own rows (of int8
+      // every code is finite).  (A second form of the products, with masks, is code that requests of up to 8 and of up
+      // to 16 rows alternate between: 250 such requests 127 us for 126 here, int8 157 for 141.)
+      if (!I8 && partial) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int tok = t0 + 16 * mt + (lane & 15);
+          if (tok < tok_lo || tok >= tok_hi)
+#pragma unroll
+            for (int u = 0; u < T::KS; u += 2) st_shared_zero(place_u[mt] + vst_u + T::unit(lane & 15, u + (lane >> 4)));
         }
+        fence_proxy_async_smem();      // (the stage's next codes come by TMA)
+        __syncwarp();
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int u = 0; u < T::KS; u += 2) {
-          uint32_t w[4];             // of unit u: keys 0-7, 8-15; then of unit u + 1
-          ldsm_x4_t(w, vst_u + T::unit(row, u + (mi >> 1)));
+          uint32_t w[4];               // of unit u: keys 0-7, 8-15; then of unit u + 1
+          ldsm_x4_t(w, place_u[mt] + vst_u + T::unit(row, u + (mi >> 1)));
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             // bytes of w: dims 2g, 2g + 1 of key 2c, then of key 2c + 1.  Row g of the
@@ -613,23 +657,10 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
               a[2] = e4m3x2_to_f16x2<0>(x1);
               a[3] = e4m3x2_to_f16x2<1>(x1);
             }
-            if constexpr (MASK) {
-              a[0] &= vm_lo;
-              a[1] &= vm_lo;
-              a[2] &= vm_hi;
-              a[3] &= vm_hi;
-            }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) mma_f16(o[u + v][j], a, pb[j][0], pb[j][1]);
+            for (int j = 0; j < NJ; ++j) mma_f16(o[u + v][j], a, pb[mt][j][0], pb[mt][j][1]);
           }
         }
-      };
-      if (partial) {
-        pv(std::true_type{});
-      } else {
-        pv(std::false_type{});
-      }
-
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
@@ -639,6 +670,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     } else {
       tiles(std::integral_constant<int, NH8>{});
     }
+
+    if (MT > 1) load_request<T>(p, b, TS, hgroups, r);   // (again, rather than in registers over the tiles)
 
     // ---- the rows' values, merged over a head's KW warps -----------------------------
     // the shares that hold parts of this (request, y): first .. last; a part that begins it goes to place
@@ -904,13 +937,13 @@ __global__ void __launch_bounds__(kMergeThreads) block_merge_kernel(const BlockP
 }
 
 struct Variant {
-  int warps, smem, ctas;
+  int warps, smem, ctas, groups;        // groups: of 16 keys a warp and stage
 };
 
 template <int D, int NH8>
 Variant variant() {
   using C = Choice<D, NH8>;
-  return {C::W, Traits<D, NH8, C::W, C::NS>::SMEM, C::CPS};
+  return {C::W, Traits<D, NH8, C::W, C::NS, C::MT>::SMEM, C::CPS, C::MT};
 }
 
 Variant variant_of(int D, int nh8) {
@@ -923,9 +956,9 @@ template <int D, bool I8, int NH8>
 cudaError_t launch_split(const CUtensorMap& tmk, const CUtensorMap& tmv, const BlockParams& p, dim3 grid,
                          cudaStream_t stream) {
   using C = Choice<D, NH8>;
-  using T = Traits<D, NH8, C::W, C::NS>;
-  auto kern = p.cap_log2 > 0.f ? block_split_kernel<D, I8, NH8, C::W, C::NS, true>
-                               : block_split_kernel<D, I8, NH8, C::W, C::NS, false>;
+  using T = Traits<D, NH8, C::W, C::NS, C::MT>;
+  auto kern = p.cap_log2 > 0.f ? block_split_kernel<D, I8, NH8, C::W, C::NS, C::MT, true>
+                               : block_split_kernel<D, I8, NH8, C::W, C::NS, C::MT, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<grid, T::THREADS, T::SMEM, stream>>>(tmk, tmv, p);
@@ -1129,7 +1162,7 @@ pa_status validate(const pa_block_shape& s) {
 pa_status plan_split(const pa_block_shape& s, const int32_t* lens, int32_t batch, int num_sms, pa_block_plan_t* out) {
   const Variant v = variant_of(s.head_dim, nh8_of(s));
   const int hg = heads_log2(s, v.warps);
-  const int TS = 16 * (v.warps >> hg);
+  const int TS = 16 * v.groups * (v.warps >> hg);
   const int groups = static_cast<int>(cdiv(rows_of(s), nh8_of(s) * 8));
   const int64_t ctas_y = static_cast<int64_t>(s.num_kv_heads >> hg) * groups;
   const int64_t max_n = static_cast<int64_t>(s.max_pages_per_seq) * s.page_size;
@@ -1144,11 +1177,11 @@ pa_status plan_split(const pa_block_shape& s, const int32_t* lens, int32_t batch
     units = s.max_batch * ctas_y * tiles(max_n);
   }
   // one wave, or fewer CTAs where the lengths (or capacities) give none of them its least share
-  const int64_t least = std::max<int64_t>(1, kLeastKeys / (v.warps * 16));
+  const int64_t least = std::max<int64_t>(1, kLeastKeys / (v.warps * v.groups * 16));
   const int64_t wave = std::min<int64_t>(s.num_ctas > 0 ? s.num_ctas : static_cast<int64_t>(num_sms) * v.ctas,
                                          kMaxCtas);
   // (the kernel counts weighted tiles in 32 bits)
-  if (s.max_batch * ctas_y * (tiles(max_n) * kWideWeight + kStartWeight) > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (s.max_batch * ctas_y * (tiles(max_n) * wide_weight(v.groups) + kStartWeight) > INT32_MAX) return PA_ERR_UNSUPPORTED;
   const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(wave, cdiv(units, least)));
   out->chunked = 0;
   out->tile_tokens = TS;
@@ -1257,7 +1290,7 @@ extern "C" pa_status pa_block_attend(
     if (!query_start_loc && batch > 0) return PA_ERR_INVALID_ARG;      // (one row a request: a plan of max_new 1)
   } else {
     if (plan->ctas < 1 || plan->ctas > kMaxCtas || plan->min_tiles < 1 || plan->row_groups != groups ||
-        plan->head_group != 1 << hg || plan->tile_tokens != 16 * (v.warps >> hg) || plan->smem_bytes != v.smem ||
+        plan->head_group != 1 << hg || plan->tile_tokens != 16 * v.groups * (v.warps >> hg) || plan->smem_bytes != v.smem ||
         plan->scratch_bytes < split_scratch(s, plan->ctas, hg))
       return PA_ERR_INVALID_ARG;
   }
@@ -1380,8 +1413,9 @@ extern "C" pa_status pa_block_attend(
       }
       if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     }
-    st = extend_over_copy(as_shape(s, PA_MODE_EXTEND), tmq, cp.kc, cp.vc, cp.page_scales, static_cast<int32_t>(n * maxp), cp.bt_copy, cp.seq_lens, cp.qsl, n, total_q, scale, sinks,
-                          out, out_stride_tok, out_stride_head, lse, sc, sc + at.work, stream);
+    st = extend_over_copy(as_shape(s, PA_MODE_EXTEND), tmq, cp.kc, cp.vc, cp.page_scales, static_cast<int32_t>(n * maxp),
+                          cp.bt_copy, cp.seq_lens, cp.qsl, n, total_q, scale, sinks, out, out_stride_tok,
+                          out_stride_head, lse, sc, sc + at.work, stream);
     if (st != PA_OK) return st;
   }
   return PA_OK;
