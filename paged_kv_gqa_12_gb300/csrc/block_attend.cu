@@ -1131,8 +1131,10 @@ int heads_log2(const pa_block_shape& s, int warps) {
 
 // Above this many rows a kv head (of one request) the chunked form is taken.  It copies the codes and has no
 // parts of a context, so it wants requests enough to fill the card (two CTAs an SM).  Measured, split / chunked, groups
-// of 4, int8, us: 64 requests of up to 8192 tokens, 12 rows each 435 / 485, 16 rows 571 / 487; 4 such requests, 32
-// rows (128 a kv head) 141 / 165; one of 131071 tokens, 32 rows 495 / 1803.
+// of 4, heads of 128, us, e4m3 and int8: 64 requests of up to 8192 tokens, 12 rows each (48 a kv head) 323 / 485 and
+// 348 / 485, 16 rows 423 / 489 and 454 / 486, 20 rows 518 / 487 and 562 / 488; 4 such requests, 32 rows (128 a kv head)
+// 68 / 143 and 75 / 137; one of 131071 tokens, 32 rows, int8 376 / 1973.  (Between 48 and 64 rows the split form is
+// ahead at heads of 128; 64 and 256 were not measured there.)
 bool chunked_form(const pa_block_shape& s) {
   const bool fills = static_cast<int64_t>(s.max_batch) * s.num_kv_heads >= 2 * static_cast<int64_t>(s.num_sms);
   return rows_of(s) > (fills ? 48 : 128);
