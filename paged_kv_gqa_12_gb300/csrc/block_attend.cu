@@ -9,7 +9,8 @@
 //   x_j = s_j log2 e + log2 vs_j,  m = max x_j,  p_j = 2^(x_j - m + 14)
 // the output is sum p_j code_j / sum p_j / vs_j: the weight that meets the codes
 // is p itself, the addition of log2 vs rides in the score's multiply-add, and the
-// denominator's 1 / vs in its own.  m bounds every term of the output, so p <= 2^14
+// denominator's 1 / vs in its own, in units that keep a long row of tiny scales
+// finite.  m bounds every term of the output, so p <= 2^14
 // whatever the pages' scales are, and a weight in f16 is off by half a step,
 // 2^-11, down to 2^-28 of the row's largest.  q enters in f16 as well, scaled by a
 // power of two a row (largest value in [2^14, 2^15): exact to 2^-32 of it).
@@ -610,8 +611,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
           for (int h = 0; h < 2; ++h) mu[h] = m_run[j][h] == -INFINITY ? 0.f : m_run[j][h] - kWeightBias;
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[mt][j][e] = ex2(s[mt][j][e] - mu[e & 1]);
-          l_run[j][0] = fmaf(s[mt][j][0] + s[mt][j][2], iv, l_run[j][0]);
-          l_run[j][1] = fmaf(s[mt][j][1] + s[mt][j][3], iv, l_run[j][1]);
+          l_run[j][0] = fmaf((s[mt][j][0] + s[mt][j][2]) * kDenScale, iv, l_run[j][0]);
+          l_run[j][1] = fmaf((s[mt][j][1] + s[mt][j][3]) * kDenScale, iv, l_run[j][1]);
           pb[mt][j][0] = movmatrix_t(pack_f16x2(s[mt][j][0], s[mt][j][1]));
           pb[mt][j][1] = movmatrix_t(pack_f16x2(s[mt][j][2], s[mt][j][3]));
         }
@@ -741,10 +742,10 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       for (int h = 0; h < 2; ++h) {
         const int rr = j * 8 + 2 * c + h;
         if (rr >= R) continue;
-        // l = sum 2^(x - m + 14) / vs: the row's LSE is m - 14 + log2 l
+        // l = 2^-20 sum 2^(x - m + 14) / vs: the row's LSE is m - 14 + 20 + log2 l
         const float den = l_run[j][h];
-        lse2[j][h] = den == 0.f ? -INFINITY : m_run[j][h] - kWeightBias + lg2(den);
-        float f = den == 0.f ? 0.f : 1.f / den;
+        lse2[j][h] = den == 0.f ? -INFINITY : m_run[j][h] - (kWeightBias - kDenBias) + lg2_den(den);
+        float f = den == 0.f ? 0.f : kDenScale / den;
         const bool lead = g == 0 && kw == 0;
         if (direct) {
           float sink;

@@ -8,6 +8,14 @@
 
 namespace pa {
 
+// Denominators sum a weight over its V scale, up to 2^15 times 2^100 (kLeastScale) a key; counted in units of 2^20
+// they stay below 2^127 for 2^30 keys of one row.
+constexpr float kDenScale = 0x1p-20f;
+constexpr float kDenBias = 20.f;
+
+// log2 of such a denominator, which under the largest V scales is subnormal (lg2 takes those for 0).
+__device__ __forceinline__ float lg2_den(float l) { return l < 1.f ? lg2(l * 0x1p60f) - 60.f : lg2(l); }
+
 // Two e4m3 codes (the low or high half of w) as f16x2, exactly.
 template <int HALF>
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {

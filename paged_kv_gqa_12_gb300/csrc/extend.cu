@@ -347,7 +347,7 @@ __device__ __forceinline__ void dequant_tile(uint8_t* tile, float scale, int lan
 // BLK: K and V hold 8-bit codes (exact, K as bf16, V as f16) with a scale for each page and kv
 // head.  The softmax folds both in: x = s (scale ks) log2 e + log2 vs, weights p = 2^(x - m + 7)
 // (f16, at most 2^15 with the lazy maximum; half a step 2^-11) meet the codes of V, and the
-// denominator sums p / vs.  Such weights need no second part.
+// denominator sums p / vs (in units of 2^20).  Such weights need no second part.
 constexpr float kBlkBias = 7.f;
 
 // Two CTAs per SM cap a thread at 128 registers (allocation counts 8 warps).
@@ -797,13 +797,18 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       };
       if constexpr (BLK) {
         const float2 nb2 = make_float2(kBlkBias - m_base, kBlkBias - m_base);
+        float2 of16 = make_float2(0.f, 0.f);       // the weights of 16 keys of one V scale
 #pragma unroll
         for (int i = 0; i < BN / 2; ++i) {
-          const float iv = ex2(-ksv[i / 8].y);
           const float2 x = __fadd2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), nb2);
           const float2 ev = make_float2(ex2(x.x), ex2(x.y));
-          ls2[i & 1] = __ffma2_rn(ev, make_float2(iv, iv), ls2[i & 1]);
+          of16 = i % 8 == 0 ? ev : __fadd2_rn(of16, ev);
           sr[i] = pack_f16x2(ev.x, ev.y);
+          if (i % 8 == 7) {
+            const float iv = ex2(-ksv[i / 8].y);
+            const float2 units = __fmul2_rn(of16, make_float2(kDenScale, kDenScale));
+            ls2[0] = __ffma2_rn(units, make_float2(iv, iv), ls2[0]);
+          }
           if (i == 15) release(0);
         }
       } else if (hot) {
@@ -851,12 +856,13 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       const int hq = kvh * G + hh;
       float M2 = m_run, f = 1.f, Z = l_run;
       if constexpr (BLK) {
-        // the row's own LSE is m - 7 + log2 l; against the sink everything is in units of 2^M2
-        M2 = l_run == 0.f ? -INFINITY : m_run - kBlkBias + lg2(l_run);
+        // the row's own LSE is m - 7 + 20 + log2 l; against the sink everything is in units of 2^M2
+        M2 = l_run == 0.f ? -INFINITY : m_run - (kBlkBias - kDenBias) + lg2_den(l_run);
         const float sk = p.sinks != nullptr ? p.sinks[hq] * kLog2e : -INFINITY;
         const float top = fmaxf(M2, sk);
         const float own = M2 == -INFINITY ? 0.f : ex2(M2 - top);
-        f = own / l_run;            // (no key: 0 / 0, and Z = 0 or the sink's 1 decides below)
+        // (2^-20 in two steps: neither end leaves the range; no key: 0 / 0, and Z = 0 or the sink's 1 decides below)
+        f = own * 0x1p-10f / l_run * 0x1p-10f;
         Z = own + (sk == -INFINITY ? 0.f : ex2(sk - top));
         if (own == 0.f) f = 0.f;
         M2 = top;
