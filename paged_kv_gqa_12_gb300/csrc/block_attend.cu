@@ -775,8 +775,11 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
 // shares as the merging one took 8 to 16 us: a few warps, each waiting for L2 row after row, often
 // with tiles of the next request to come.)
 constexpr int kMergeThreads = 256;
+// The parts' weights count 2^-13 of themselves in the sum of values: of up to kMaxCtas parts next to fp32's largest
+// number it stays finite.
+constexpr float kPartScale = 0x1p-13f;
 
-// Parts [i0, i1) of a row: v = sum 2^(lse - M) part, Z likewise of 1; U parts' loads in flight together.
+// Parts [i0, i1) of a row: v = kPartScale sum 2^(lse - M) part, Z = sum 2^(lse - M); U parts' loads in flight together.
 template <int D, int U>
 __device__ __forceinline__ void merge_range(const BlockParams& p, const MergeRecord& rec, int row_in_place, int place_rows,
                                             int i0, int i1, int lane, float& M, float& Z, float4 (&v)[(D + 127) / 128]) {
@@ -805,12 +808,13 @@ __device__ __forceinline__ void merge_range(const BlockParams& p, const MergeRec
     for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     const float top = fmaxf(M, m);
     const float old = M == -INFINITY ? 0.f : ex2(M - top);
-    const float w = l == -INFINITY ? 0.f : ex2(l - top);   // (a part with no key for this row)
+    float w = l == -INFINITY ? 0.f : ex2(l - top);   // (a part with no key for this row)
     float z = w;
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
     Z = fmaf(Z, old, z);
     M = top;
+    w *= kPartScale;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (k > 0) fetch(k);
@@ -925,7 +929,7 @@ __global__ void __launch_bounds__(kMergeThreads) block_merge_kernel(const BlockP
     }
     float f;
     uint16_t* outp = finish_row(p, rec.qs, rec.kvh0 + head, rec.row0 + rr, Z == 0.f ? -INFINITY : M + lg2(Z), lane == 0, f);
-    f = Z == 0.f ? 0.f : f / Z;
+    f = Z == 0.f ? 0.f : f / (Z * kPartScale);
     if (lane * 4 < D) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
