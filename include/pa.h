@@ -570,7 +570,8 @@ pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_len
  * q and out rows are 4-byte aligned for a plan that is not chunked, 16-byte aligned for one that
  * is.  Few rows: the codes enter the products exactly and the scales in fp32; q is scaled by a
  * power of two a row and exact in f16 down to 2^-32 of its row's largest value, weights are rounded to
- * f16 (half a step 2^-11).  Chunks: the same with q as it is.
+ * f16 (half a step 2^-11).  Chunks: the same with q as it is.  NaN among V's e4m3 codes reaches the rows
+ * that attend to its key, in its dimension, and no others.
  * A length beyond the plan's capacity, a packing with more rows than tokens, than max_new or than
  * total_q leaves that request's rows untouched (PA_DEVICE_CAPACITY); a block-table entry outside
  * the pool reads as zeros (PA_DEVICE_PAGE_ID).  Rows behind query_start_loc[batch] are left as they

@@ -75,6 +75,8 @@ struct BlockParams {
   const float* k_scales;
   const float* v_scales;
   int64_t scale_stride;
+  const uint8_t* v;           // the V codes and their strides (read here for NaN alone)
+  int64_t v_stride_page, v_stride_tok, v_stride_head;
   const int32_t* block_table;
   int64_t bt_stride;
   const int32_t* seq_lens;
@@ -177,8 +179,13 @@ __device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts
   return true;
 }
 
-__device__ __forceinline__ void st_shared_zero(uint32_t addr) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" :: "r"(addr), "r"(0) : "memory");
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(addr) : "memory");
+  return w;
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
 }
 
 // All W compute warps of the CTA (the fetching warp does not take part).
@@ -476,9 +483,41 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
     const int full_hi = min(tok_hi, r.L - r.n_new + 1);
     // (a request that brings at most 8 rows beside others of up to 16: NJ = 1 leaves the second 8 out)
     const int pos0 = r.L - r.n_new;                     // position of the first row's token
-    auto tiles = [&](auto nj_tag) {
+    uint32_t nan_codes = 0;              // e4m3: NaN met in V of keys that only some rows see
+    // masked keys have P = 0, but their codes may be stale, NaN in e4m3 (of int8 every code is finite): V of the former
+    // is zeroed, in this warp's own rows.  Of keys that some rows see and others do not, NaN codes alone become zeros;
+    // the rows that see them get their NaN after the last tile.  (A second form of the products, with masks, is code that
+    // requests of up to 8 and of up to 16 rows alternate between: 250 such requests 127 us for 126, int8 157 for 141.)
+    auto clean = [&](int stage, int t0) {
+      int ln = lane;                       // (kept from the compiler, as t0 below)
+      asm volatile("" : "+r"(ln));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int tok = t0 + 16 * mt + (ln & 15);
+        const uint32_t rows = place_u[mt] + stage * T::STAGE + T::TILE;
+        if (tok < tok_lo || tok >= tok_hi) {
+#pragma unroll
+          for (int u = 0; u < T::KS; u += 2) st_shared(rows + T::unit(ln & 15, u + (ln >> 4)), make_uint4(0, 0, 0, 0));
+        } else if (tok < full_lo || tok >= full_hi) {
+#pragma unroll 1
+          for (int u = 0; u < T::KS; u += 2) {
+            const uint32_t at = rows + T::unit(ln & 15, u + (ln >> 4));
+            const uint4 w = ld_shared(at);
+            const uint4 nan = make_uint4(e4m3_nan4(w.x), e4m3_nan4(w.y), e4m3_nan4(w.z), e4m3_nan4(w.w));
+            const uint32_t any = nan.x | nan.y | nan.z | nan.w;
+            if (any != 0) {
+              st_shared(at, make_uint4(w.x & ~nan.x, w.y & ~nan.y, w.z & ~nan.z, w.w & ~nan.w));
+              nan_codes |= any;
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();            // (the stage's next codes come by TMA)
+      __syncwarp();
+    };
+    auto tiles = [&](auto nj_tag, int k0, int k1) {
     constexpr int NJ = decltype(nj_tag)::value;
-    for (int k = 0; k < n; ++k, ++it) {
+    for (int k = k0; k < k1; ++k, ++it) {
       const int stage = it % NS;
       // (kept from the compiler, or it holds every offset from it in a register of its own: 200 bytes spilled)
       int t0 = (tile_begin + k) * TS + key0;
@@ -620,19 +659,8 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
 
       // ---- O^T += V^T P^T over the codes ---------------------------------------
       const uint32_t vst_u = stage * T::STAGE + T::TILE;
-      // masked keys have P = 0, but their codes may be stale, NaN in e4m3: zeroed, in this warp's own rows (of int8
-      // every code is finite).  (A second form of the products, with masks, is code that requests of up to 8 and of up
-      // to 16 rows alternate between: 250 such requests 127 us for 126 here, int8 157 for 141.)
-      if (!I8 && partial) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int tok = t0 + 16 * mt + (lane & 15);
-          if (tok < tok_lo || tok >= tok_hi)
-#pragma unroll
-            for (int u = 0; u < T::KS; u += 2) st_shared_zero(place_u[mt] + vst_u + T::unit(lane & 15, u + (lane >> 4)));
-        }
-        fence_proxy_async_smem();      // (the stage's next codes come by TMA)
-        __syncwarp();
+      if constexpr (!I8 && MT > 1) {
+        if (partial) clean(stage, t0);
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -666,13 +694,60 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
     };
-    if (NH8 == 2 && R <= 8) {
-      tiles(std::integral_constant<int, 1>{});
-    } else {
-      tiles(std::integral_constant<int, NH8>{});
+    for (int k = 0, k1; k < n; k = k1) {
+      k1 = n;
+      // (a tile with masked keys by itself: with one group of keys a warp the loop over the others holds fewer registers
+      // without that code, 16 rows of heads of 256 312 us for 329; with two groups one loop is better, 115 for 117)
+      if constexpr (!I8 && MT == 1) {
+        const int t0 = (tile_begin + k) * TS + key0;
+        if (t0 < full_lo || t0 + 16 > full_hi) {
+          dead = dead || !__all_sync(0xffffffffu, mbar_wait(&full[it % NS], (it / NS) & 1, p.err));
+          if (!dead) clean(it % NS, t0);
+          k1 = k + 1;
+        } else {
+          k1 = min(n, (full_hi - 16 - key0) / TS - tile_begin + 1);          // up to the next with masked keys
+        }
+      }
+      if (NH8 == 2 && R <= 8) {
+        tiles(std::integral_constant<int, 1>{}, k, k1);
+      } else {
+        tiles(std::integral_constant<int, NH8>{}, k, k1);
+      }
     }
 
     if (MT > 1) load_request<T>(p, b, TS, hgroups, r);   // (again, rather than in registers over the tiles)
+
+    if (!I8 && __any_sync(0xffffffffu, nan_codes != 0)) {
+      const int lo = max(r.lo, (r.tile0 + tile) * TS), hi = min(r.L, (r.tile0 + tile + n) * TS);
+      const int seen_lo = max(lo, p.window > 0 ? r.L - p.window : 0), seen_hi = min(hi, r.L - r.n_new + 1);
+      for (int tok = lo; tok < hi; ++tok) {
+        if (tok >= seen_lo && tok < seen_hi) tok = seen_hi;              // (these codes were left as they are)
+        if (tok >= hi) break;
+        const int id = p.block_table[static_cast<int64_t>(b) * p.bt_stride + (tok >> ps_log2)];
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_pages)) continue;
+        const uint8_t* vp = p.v + static_cast<int64_t>(id) * p.v_stride_page + (tok & (ps - 1)) * p.v_stride_tok +
+                            static_cast<int64_t>(kvh) * p.v_stride_head + 2 * g;
+        bool sees[NH8][2];
+#pragma unroll
+        for (int j = 0; j < NH8; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int pos = r.L - r.n_new + (row0 + min(j * 8 + 2 * c + h, R - 1)) / G;
+            sees[j][h] = tok <= pos && (p.window <= 0 || tok > pos - p.window);
+          }
+#pragma unroll
+        for (int i = 0; i < T::KS; ++i) {
+          const uint32_t w = e4m3_nan4(*reinterpret_cast<const uint16_t*>(vp + 16 * i));     // dims 16 i + 2 g and the next
+#pragma unroll
+          for (int j = 0; j < NH8; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (sees[j][h] && (w & 0xffu) != 0) o[i][j][h] = __uint_as_float(0x7fffffffu);
+              if (sees[j][h] && (w & 0xff00u) != 0) o[i][j][h + 2] = __uint_as_float(0x7fffffffu);
+            }
+        }
+      }
+    }
 
     // ---- the rows' values, merged over a head's KW warps -----------------------------
     // the shares that hold parts of this (request, y): first .. last; a part that begins it goes to place
@@ -1007,7 +1082,7 @@ struct CopyParams {
   uint16_t* kc;
   uint16_t* vc;
   float2* page_scales;        // [copy page][Hkv]: K scale, log2 of the V scale
-  int32_t* bt_copy;
+  int32_t* bt_copy;           // a request's copy pages; the sign bit is set where a V code is NaN
   uint32_t* err;
 };
 
@@ -1038,13 +1113,27 @@ __device__ __forceinline__ void widen_unit(const uint4& w, uint4* dst) {
   dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
+// V codes without NaN, which a product would carry from its key's rows to all of a tile: NaN becomes minus zero, and
+// minus zero zero.  Whether there was one.
+__device__ __forceinline__ bool mark_nan(uint4& w) {
+  uint32_t any = 0;
+  uint32_t* x[4] = {&w.x, &w.y, &w.z, &w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t nan = e4m3_nan4(*x[k]), zero = __vcmpeq4(*x[k], 0x80808080u);
+    *x[k] = (*x[k] & ~(nan | zero)) | (nan & 0x80808080u);
+    any |= nan;
+  }
+  return any != 0;
+}
+
 // One CTA a (page of a request, request).
 template <int D, bool I8>
 __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
   const int i = blockIdx.x;
   const int b = blockIdx.y;
   const int64_t dst_page = static_cast<int64_t>(b) * p.maxp + i;
-  if (threadIdx.x == 0) p.bt_copy[dst_page] = static_cast<int32_t>(dst_page);
+  if (threadIdx.x == 0) p.bt_copy[dst_page] = static_cast<int32_t>(dst_page);   // (the same thread marks it below)
   const int L = p.seq_lens[b];
   const int qs = p.qsl[b];
   const int n = p.qsl[b + 1] - qs;
@@ -1073,6 +1162,7 @@ __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
     const int64_t at = static_cast<int64_t>(src) * p.scale_stride + h;
     p.page_scales[dst_page * p.num_kv_heads + h] = make_float2(p.k_scales[at], lg2(fmaxf(p.v_scales[at], kLeastScale)));
   }
+  bool nan = false;
   for (int u = threadIdx.x; u < units; u += blockDim.x) {
     const int tok = u / (p.num_kv_heads * UPH);
     const int rem = u - tok * (p.num_kv_heads * UPH);
@@ -1080,7 +1170,13 @@ __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
     const int64_t off = static_cast<int64_t>(src) * p.stride_page + static_cast<int64_t>(tok) * p.stride_tok +
                         static_cast<int64_t>(head) * p.stride_head + (rem - head * UPH) * 16;
     widen_unit<I8, true>(*reinterpret_cast<const uint4*>(p.k + off), kd + 2 * u);
-    widen_unit<I8, false>(*reinterpret_cast<const uint4*>(p.v + off), vd + 2 * u);
+    uint4 w = *reinterpret_cast<const uint4*>(p.v + off);
+    if constexpr (!I8) nan |= mark_nan(w) && i * ps + tok >= first && i * ps + tok < L;       // (of a key of the request)
+    widen_unit<I8, false>(w, vd + 2 * u);
+  }
+  if constexpr (!I8) {
+    nan = __syncthreads_or(nan);
+    if (nan && threadIdx.x == 0) p.bt_copy[dst_page] = static_cast<int32_t>(dst_page) | INT32_MIN;
   }
 }
 
@@ -1340,6 +1436,10 @@ extern "C" pa_status pa_block_attend(
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     p.scale_stride = scale_stride;
+    p.v = static_cast<const uint8_t*>(v_cache);
+    p.v_stride_page = kv_stride_page;
+    p.v_stride_tok = kv_stride_tok;
+    p.v_stride_head = kv_stride_head;
     p.block_table = block_table;
     p.bt_stride = bt_stride;
     p.seq_lens = seq_lens;

@@ -28,6 +28,9 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   return r;
 }
 
+// A byte of ones for each NaN among four e4m3 codes.
+__device__ __forceinline__ uint32_t e4m3_nan4(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 // Two int8 codes as f16x2, exactly.  x holds the codes with their sign bits
 // flipped (u = code + 128); SEL picks two bytes and puts 0x64 above each:
 // 0x6400 + u is the f16 number 1024 + u, and 1152 = 0x6480 taken off leaves the code.

@@ -90,6 +90,7 @@ struct ExtendParams {
   int64_t out_stride_tok, out_stride_head;
   float* lse;
   const float2* page_scales;   // cache of codes: [copy page][Hkv] (K scale, log2 of the V scale)
+  const uint16_t* v_codes;     // their copy of V: [copy page][slot][Hkv][D] f16, minus zero for NaN
   int4* work;               // [work_cap][2]: WorkItem
   int* work_count;
   int work_cap;
@@ -280,9 +281,9 @@ struct ExtTraits {
   }
   // mbarriers: q_full, six per ring stage, s_full/2 x p_half/o_done per S
   // buffer, q_moved (Q in TMEM)
-  // then the TMEM address and 4 exact-P flag bytes per S buffer (one per
-  // softmax warp)
-  static constexpr int BAR_BYTES = ((1 + 6 * NST + 4 * NSB + (QT ? 1 : 0)) * 8 + 4 + 4 * NSB + 15) / 16 * 16;
+  // then the TMEM address, 4 exact-P flag bytes per S buffer (one per
+  // softmax warp) and the word that says whether a page holds NaN codes
+  static constexpr int BAR_BYTES = ((1 + 6 * NST + 4 * NSB + (QT ? 1 : 0)) * 8 + 4 + 4 * NSB + 4 + 15) / 16 * 16;
   static constexpr int SMEM = 1024 + SMEM_DATA + BAR_BYTES;   // 1024: alignment slack for SW128
   static_assert(CPS * SMEM <= 232448, "shared memory for CPS CTAs per SM");
   static_assert(BN % 64 == 0, "P is stored 32 columns (64 keys) at a time");
@@ -347,7 +348,9 @@ __device__ __forceinline__ void dequant_tile(uint8_t* tile, float scale, int lan
 // BLK: K and V hold 8-bit codes (exact, K as bf16, V as f16) with a scale for each page and kv
 // head.  The softmax folds both in: x = s (scale ks) log2 e + log2 vs, weights p = 2^(x - m + 7)
 // (f16, at most 2^15 with the lazy maximum; half a step 2^-11) meet the codes of V, and the
-// denominator sums p / vs (in units of 2^20).  Such weights need no second part.
+// denominator sums p / vs (in units of 2^20).  Such weights need no second part.  A NaN among V's
+// codes is left out of the products, which would give it to every row of the tile (0 x NaN is NaN),
+// and written to its rows at the end: the table's entry of its page has the sign bit set.
 constexpr float kBlkBias = 7.f;
 
 // Two CTAs per SM cap a thread at 128 registers (allocation counts 8 warps).
@@ -408,6 +411,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
   uint64_t* q_moved = o_done + T::NSB;   // Q in TMEM: the softmax warps copied it (4 arrivals)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_moved + (T::QT ? 1 : 0));
   uint8_t* vflag = reinterpret_cast<uint8_t*>(tmem_slot + 1);   // [NSB][4]: softmax warp wants exact P
+  volatile uint32_t* nan_seen = tmem_slot + 1 + T::NSB;         // BLK: a page of the item holds NaN codes of V
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -423,6 +427,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
     const bool outside = (pg * ps >= L) || ((pg + 1) * ps <= lo_min);
     if (outside) return p.num_pages;
     const int id = bt_row[pg];
+    if (BLK) return id;                // (the copy's pages: in range, the sign a mark)
     if (static_cast<unsigned>(id) < static_cast<unsigned>(p.num_pages)) return id;
     atomicOr(p.err, kErrPageId);
     return p.num_pages;
@@ -449,6 +454,7 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
       mbar_init(&o_done[i], 1);
     }
     if (T::QT) mbar_init(q_moved, 4);
+    if (BLK) *nan_seen = 0;
     fence_mbar_init();
     // Q right away (the other threads wait on q_full after the barrier below)
     mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(T::NCH * p.tm * G * 128));
@@ -484,7 +490,11 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
         if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(T::TILE));
         __syncwarp();
         if (lane < npg) {
-          const int coord = j == 0 ? coord0 : page_coord(j);
+          int coord = j == 0 ? coord0 : page_coord(j);
+          if constexpr (BLK) {
+            if (coord < 0) *nan_seen = 1;      // (read by the softmax warps behind the last tile's barriers)
+            coord &= INT_MAX;
+          }
           uint8_t* dst = ring + stage * T::TILE + lane * ps * 128;
 #pragma unroll
           for (int c = 0; c < T::NCH; ++c) tma_load_4d(dst + c * T::KV_CHUNK, map, c * 64, kvh, 0, coord, &full[stage]);
@@ -899,6 +909,25 @@ extend_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constan
           }
         }
       }
+      if constexpr (BLK) {
+        if (row_ok && *nan_seen != 0) {
+          for (int page = max(lo, 0) >> ps_log2; page <= pos >> ps_log2; ++page) {
+            if (bt_row[page] >= 0) continue;
+            for (int k = max(page << ps_log2, lo); k <= min((page << ps_log2) + ps - 1, pos); ++k) {
+              const int64_t slot = ((static_cast<int64_t>(b) * p.bt_stride + page) << ps_log2) + (k & (ps - 1));
+              const uint4* v = reinterpret_cast<const uint4*>(p.v_codes + (slot * p.num_kv_heads + kvh) * D);
+#pragma unroll 1
+              for (int d = 0; d < D / 8; ++d) {
+                const uint4 w = v[d];
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (((x[e / 2] >> (16 * (e & 1))) & 0xffffu) == 0x8000u) op[8 * d + e] = 0x7fffu;
+              }
+            }
+          }
+        }
+      }
       if (row_ok && p.lse != nullptr) {
         p.lse[orow * p.num_q_heads + hq] = (Z > 0.f) ? (M2 + lg2(Z)) * kLn2 : -INFINITY;
       }
@@ -1155,6 +1184,7 @@ pa_status run_tiles(const pa_shape& s, const CUtensorMap& tmq, const ExtendCall&
   p.k_scales = c.k_scales;
   p.v_scales = c.v_scales;
   p.page_scales = c.page_scales;
+  p.v_codes = static_cast<const uint16_t*>(c.vbase);
   p.out = static_cast<uint16_t*>(c.out);
   p.out_stride_tok = c.out_stride_tok;
   p.out_stride_head = c.out_stride_head;

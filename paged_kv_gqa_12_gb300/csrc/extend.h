@@ -19,7 +19,8 @@ pa_status extend_q_map(CUtensorMap* map, const pa_shape& s, const void* q, int64
 
 // Extend over a dense copy of the codes in the requests' pages, K as bf16 and V as f16 (page i of
 // request b at copy page table[b * max_pages_per_seq + i] = b * max_pages_per_seq + i), with
-// page_scales [copy page][Hkv] = (K scale, log2 of the V scale): the scheduler and the attention
+// page_scales [copy page][Hkv] = (K scale, log2 of the V scale); a NaN of V is minus zero in the copy,
+// and its page's entry of the table has the sign bit set: the scheduler and the attention
 // kernel.  `work` holds the work list, `header` is a scratch header.
 pa_status extend_over_copy(const pa_shape& s, const CUtensorMap& tmq, const void* k_copy, const void* v_copy,
                            const float2* page_scales, int32_t copy_pages, const int32_t* table,
