@@ -597,8 +597,8 @@ pa_status pa_block_attend(const pa_block_plan_t* plan,
  * At the first row whose draft is not accepted -- or the last row -- one token is drawn: the first v with
  *   sum_{i <= v} y_i  >  sample_u[b] * sum_i y_i
  * where y = max(target_probs[r] - draft_probs[r], 0) after a rejection (draft_probs NULL: 1 at the
- * draft, 0 elsewhere; where every y is 0, target_probs[r]), else y = target_probs[r].  The products are exact, the sums keep at least
- * 44 bits.  out_tokens[b] gets the accepted drafts, the drawn token and then -1 (to its width), num_tokens[b] the accepted drafts + 1.  n_b = 1 is plain
+ * draft, 0 elsewhere; where every y is 0, target_probs[r]), else y = target_probs[r].  The products are exact; the sums are
+ * off by less than 2^-36 of the whole, whatever its entries.  out_tokens[b] gets the accepted drafts, the drawn token and then -1 (to its width), num_tokens[b] the accepted drafts + 1.  n_b = 1 is plain
  * sampling; n_b = 0 gives no token.  If no probability of the row is positive the token is -1.
  *   tokens, accept_u  device int32 / fp32 [total_rows]; sample_u device fp32 [batch]; u in [0, 1)
  *   target_probs, draft_probs  device fp32 [total_rows, vocab] (at most 2^20 entries), rows their stride

@@ -9,7 +9,11 @@
 //
 // Which v the sum crosses at depends on sums next to a border: in 32 bits a row of
 // 10^5 entries has errors of the order of an entry.  The differences p - q and all
-// sums are therefore pairs of floats (Knuth's two-sum, Dekker's pairs: about 47 bits).
+// sums are therefore pairs of floats (Knuth's two-sum, Dekker's pairs).  With u = 2^-24 the
+// k-th addition of a sum begun at zero is off by at most (k + 5) u^2 of it, so a lane's 32 of
+// a block by 700 u^2; a block's or eight entries' sum joins the others for 5 u^2, and where the
+// running sum crosses is off by less than 3000 u^2, 2^-36, of the whole for 2^20 entries and
+// one CTA a request.
 // The card adds 64-bit numbers 64 times slower than floats: with the sums over lanes
 // and parts in 64 bits the call of 64 rows of 131072 entries took 44 us.
 //
@@ -19,7 +23,7 @@
 //
 // Measured (one GB300, CUDA-graph replay): 64 requests of up to four drafts, 131072
 // entries, 46 MB read on average (a request whose drafts are all accepted needs no q)
-// 16.0 us; 19.8 with one entry an instruction instead of two.  One request of 32000
+// 16.4 us (16.0 without blocks); 19.8 with one entry an instruction instead of two.  One request of 32000
 // entries 6.2 us: what is left is latency (lengths, tokens, their probabilities, the
 // row, two cluster barriers).
 #include <cstdint>
@@ -39,6 +43,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;             // CTAs a request (portable cluster size)
 constexpr int kUnit = 128;              // entries a warp takes at a time
+constexpr int kBlock = 2048;            // entries whose sum a warp begins at zero
 constexpr unsigned kAll = 0xffffffffu;
 
 struct VerifyParams {
@@ -153,9 +158,9 @@ struct Row {
   __device__ __forceinline__ float less(int v) const {
     return q != nullptr ? weight(__ldg(q + v)) : (v == taken ? 1.f : 0.f);
   }
-  // the sum of a warp's entries [v, v1), v a multiple of kUnit; Q: there is a q
+  // a lane's sum of a warp's entries [v, v1), at most kBlock of them, v a multiple of kUnit; Q: there is a q
   template <bool Q>
-  __device__ __forceinline__ Pair sum(int v, int v1, int lane) const {
+  __device__ __forceinline__ Pair block(int v, int v1, int lane) const {
     Pairs s;
     if (((reinterpret_cast<uintptr_t>(p) | (Q ? reinterpret_cast<uintptr_t>(q) : 0)) & 15u) == 0) {
       constexpr int U = 4;               // 16 entries of p and q a lane in flight
@@ -195,15 +200,24 @@ struct Row {
     }
     return s.both();
   }
+  // and of any number: the lower part of a pair collects what the upper one rounds off, so its own rounding grows with
+  // the additions it has seen (over 2000 of them, from one large entry on, a sum was off by 2^-28 of itself)
+  template <bool Q>
+  __device__ __forceinline__ Pair sum(int v, int v1, int lane) const {
+    Pair s;
+    for (; v < v1; v += kBlock) {
+      s.add(block<Q>(v, min(v + kBlock, v1), lane));
+      s = s.normal();
+    }
+    return s;
+  }
   // entry v to a sum; whether it weighs anything
   __device__ __forceinline__ bool add(Pair& sum, int v) const {
     Pairs one;
     const float a = __ldg(p + v), x = less(v);
     one.add(make_float2(a, 0.f), make_float2(x, 0.f));
-    Pair y;
-    y.hi = one.hi.x;
-    y.lo = one.lo.x;
-    sum.add(y);
+    sum.add(one.hi.x);
+    sum.lo = __fadd_rn(sum.lo, one.lo.x);
     return a > x;
   }
 };
@@ -369,9 +383,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   const int a0 = min(v0 + tid * per, v1), a1 = min(a0 + per, v1);
   Pair own;
   int last = -1;
+  for (int v = a0; v < a1; v += 8) {       // (eight from zero, as a block's)
+    Pair eight;
+    const int v1 = min(v + 8, a1);
 #pragma unroll 4
-  for (int v = a0; v < a1; ++v) {
-    if (row.add(own, v)) last = v;
+    for (int u = v; u < v1; ++u)
+      if (row.add(eight, u)) last = u;
+    own.add(eight);
+    own = own.normal();
   }
   const Pair incl = lane_sums(own, lane);
   if (lane == 31) s_scan[warp] = make_float2(incl.hi, incl.lo);
@@ -396,13 +415,21 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   if (best == 0x7fffffff) {
     if (tid == 0) out[kept] = s_last;
   } else if (tid == best) {
-    int pick = last;
-    for (int v = a0; v < a1; ++v) {
-      if (row.add(before, v) && before.above(rest)) {
-        pick = v;
-        break;
+    int pick = -1;
+    rest.add(before.minus());              // what is left of it for this thread's entries
+    for (int v = a0; v < a1 && pick < 0; v += 8) {
+      rest = rest.normal();
+      Pair eight;
+      const int v1 = min(v + 8, a1);
+      for (int u = v; u < v1; ++u) {
+        if (row.add(eight, u) && eight.above(rest)) {
+          pick = u;
+          break;
+        }
       }
+      rest.add(eight.minus());
     }
+    if (pick < 0) pick = last;
     out[kept] = pick;
   }
 }
