@@ -562,7 +562,8 @@ pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_len
 
 /* Attention over an 8-bit cache with a scale for each page and kv head: as pa_decode / pa_extend
  * with K_j = code * k_scales[page][kv head], V_j likewise.  With query_start_loc NULL one row a
- * request at seq_lens[b] - 1 (total_q == batch); else rows query_start_loc[b] .. of request b, at
+ * request at seq_lens[b] - 1 (total_q == batch; for plans that are not chunked, as none of max_new 1 is,
+ * else PA_ERR_INVALID_ARG); else rows query_start_loc[b] .. of request b, at
  * most max_new of them, at the request's last positions.
  *   k_cache, v_cache   device bytes [num_pages, page_size, Hkv, head_dim], strides as for pa_decode
  *   k_scales, v_scales device fp32 [num_pages, Hkv], rows scale_stride apart, finite and >= 0

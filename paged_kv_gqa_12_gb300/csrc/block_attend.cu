@@ -1236,7 +1236,10 @@ int heads_log2(const pa_block_shape& s, int warps) {
 // 348 / 485, 16 rows 423 / 489 and 454 / 486, 20 rows 518 / 487 and 562 / 488; 4 such requests, 32 rows (128 a kv head)
 // 68 / 143 and 75 / 137; one of 131071 tokens, 32 rows, int8 376 / 1973.  (Between 48 and 64 rows the split form is
 // ahead at heads of 128; 64 and 256 were not measured there.)
+// One row a request is never chunked, whatever its group: such a plan's calls may leave query_start_loc out, which
+// the chunked form's kernels read.
 bool chunked_form(const pa_block_shape& s) {
+  if (s.max_new == 1) return false;
   const bool fills = static_cast<int64_t>(s.max_batch) * s.num_kv_heads >= 2 * static_cast<int64_t>(s.num_sms);
   return rows_of(s) > (fills ? 48 : 128);
 }
@@ -1390,7 +1393,7 @@ extern "C" pa_status pa_block_attend(
         static_cast<int64_t>(plan->group_requests) * s.max_pages_per_seq > INT32_MAX ||
         plan->scratch_bytes < chunk_scratch(s, plan->group_requests).end)
       return PA_ERR_INVALID_ARG;
-    if (!query_start_loc && batch > 0) return PA_ERR_INVALID_ARG;      // (one row a request: a plan of max_new 1)
+    if (!query_start_loc && batch > 0) return PA_ERR_INVALID_ARG;
   } else {
     if (plan->ctas < 1 || plan->ctas > kMaxCtas || plan->min_tiles < 1 || plan->row_groups != groups ||
         plan->head_group != 1 << hg || plan->tile_tokens != 16 * v.groups * (v.warps >> hg) || plan->smem_bytes != v.smem ||
