@@ -1078,7 +1078,7 @@ struct CopyParams {
   int64_t bt_stride;
   const int32_t* seq_lens;
   const int32_t* qsl;
-  int num_pages, page_size, num_kv_heads, window, maxp, max_kv, total_q;
+  int num_pages, page_size, num_kv_heads, window, maxp, max_kv, max_new, total_q;
   uint16_t* kc;
   uint16_t* vc;
   float2* page_scales;        // [copy page][Hkv]: K scale, log2 of the V scale
@@ -1138,7 +1138,7 @@ __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
   const int qs = p.qsl[b];
   const int n = p.qsl[b + 1] - qs;
   const int ctx = L - n;
-  if (n <= 0 || ctx < 0 || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + n > p.total_q) return;
+  if (n <= 0 || n > p.max_new || ctx < 0 || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + n > p.total_q) return;
   const int ps = p.page_size;
   const int first = p.window > 0 ? max(0, ctx - p.window + 1) : 0;
   if ((i + 1) * ps <= first || i * ps >= L) return;
@@ -1503,6 +1503,7 @@ extern "C" pa_status pa_block_attend(
   cp.window = s.window;
   cp.maxp = static_cast<int>(maxp);
   cp.max_kv = s.max_pages_per_seq * s.page_size;
+  cp.max_new = s.max_new;
   cp.total_q = total_q;
   cp.kc = reinterpret_cast<uint16_t*>(sc + at.k);
   cp.vc = reinterpret_cast<uint16_t*>(sc + at.v);
@@ -1524,7 +1525,7 @@ extern "C" pa_status pa_block_attend(
       if (cudaGetLastError() != cudaSuccess) return PA_ERR_CUDA;
     }
     st = extend_over_copy(as_shape(s, PA_MODE_EXTEND), tmq, cp.kc, cp.vc, cp.page_scales, static_cast<int32_t>(n * maxp),
-                          cp.bt_copy, cp.seq_lens, cp.qsl, n, total_q, scale, sinks, out, out_stride_tok,
+                          cp.bt_copy, cp.seq_lens, cp.qsl, n, total_q, s.max_new, scale, sinks, out, out_stride_tok,
                           out_stride_head, lse, sc, sc + at.work, stream);
     if (st != PA_OK) return st;
   }

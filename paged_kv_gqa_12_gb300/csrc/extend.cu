@@ -79,6 +79,7 @@ struct ExtendParams {
   int batch, total_q, num_q_heads, num_kv_heads, group, page_size, num_pages;
   int tm;                 // tokens per tile (128 / group, rounded down)
   int max_kv;             // capacity: keys per request
+  int max_new;            // capacity: query rows per request
   int block_n;            // keys per tile
   float scale_log2, cap_log2, scale_over_cap;
   int window;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kSchedThreads) extend_schedule_kernel(const Ex
     const int qlen = p.qsl[b + 1] - qs;
     const int L = p.seq_lens[b];
     if (qlen == 0) continue;
-    if (qlen < 0 || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) {
+    if (qlen < 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) {
       if (lane == 0) atomicOr(p.err, kErrCapacity);
       continue;
     }
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kSchedThreads) extend_schedule_kernel(const Ex
     const int qs = p.qsl[b];
     const int qlen = p.qsl[b + 1] - qs;
     const int L = p.seq_lens[b];
-    if (qlen <= 0 || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) continue;
+    if (qlen <= 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) continue;
     const int nmt = (qlen + p.tm - 1) / p.tm;
     for (int mt = lane; mt < nmt; mt += 32) {
       const int pos = atomicAdd(&s_off[min(tile_cost(L - qlen, qlen, mt, p.tm, p.window, p.block_n), kBuckets - 1)], 1);
@@ -1132,6 +1133,7 @@ struct ExtendCall {
   const int32_t* seq_lens;
   const int32_t* qsl;
   int32_t batch, total_q;
+  int32_t max_new;          // most query rows of a request
   float scale;
   const float* sinks;
   bool fp8_tiles;           // the attention kernel dequantises e4m3 tiles
@@ -1173,6 +1175,7 @@ pa_status run_tiles(const pa_shape& s, const CUtensorMap& tmq, const ExtendCall&
   p.num_pages = c.pages;
   p.tm = kRows / G;
   p.max_kv = s.max_pages_per_seq * s.page_size;
+  p.max_new = c.max_new;
   p.block_n = ch.block_n;
   p.scale_log2 = c.scale * kLog2eHost;
   p.cap_log2 = s.soft_cap > 0.f ? s.soft_cap * kLog2eHost : 0.f;
@@ -1228,9 +1231,9 @@ pa_status extend_q_map(CUtensorMap* map, const pa_shape& s, const void* q, int64
 
 pa_status extend_over_copy(const pa_shape& s, const CUtensorMap& tmq, const void* k_copy, const void* v_copy,
                            const float2* page_scales, int32_t copy_pages, const int32_t* table,
-                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q, float scale,
-                           const float* sinks, void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
-                           void* header, void* work, void* stream) {
+                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q,
+                           int32_t max_new, float scale, const float* sinks, void* out, int64_t out_stride_tok,
+                           int64_t out_stride_head, float* lse, void* header, void* work, void* stream) {
   ExtendCall c{};
   c.kbase = k_copy;
   c.vbase = v_copy;
@@ -1244,6 +1247,7 @@ pa_status extend_over_copy(const pa_shape& s, const CUtensorMap& tmq, const void
   c.qsl = query_start_loc;
   c.batch = batch;
   c.total_q = total_q;
+  c.max_new = max_new;
   c.scale = scale;
   c.sinks = sinks;
   c.k_scale = c.v_scale = 1.f;
@@ -1384,6 +1388,7 @@ extern "C" pa_status pa_extend(const pa_plan_t* plan, const void* q, int64_t q_s
   call.qsl = query_start_loc;
   call.batch = batch;
   call.total_q = total_q;
+  call.max_new = INT_MAX;
   call.scale = scale;
   call.sinks = sinks;
   call.fp8_tiles = fp8_tiles;

@@ -24,8 +24,8 @@ pa_status extend_q_map(CUtensorMap* map, const pa_shape& s, const void* q, int64
 // kernel.  `work` holds the work list, `header` is a scratch header.
 pa_status extend_over_copy(const pa_shape& s, const CUtensorMap& tmq, const void* k_copy, const void* v_copy,
                            const float2* page_scales, int32_t copy_pages, const int32_t* table,
-                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q, float scale,
-                           const float* sinks, void* out, int64_t out_stride_tok, int64_t out_stride_head, float* lse,
-                           void* header, void* work, void* stream);
+                           const int32_t* seq_lens, const int32_t* query_start_loc, int32_t batch, int32_t total_q,
+                           int32_t max_new, float scale, const float* sinks, void* out, int64_t out_stride_tok,
+                           int64_t out_stride_head, float* lse, void* header, void* work, void* stream);
 
 }  // namespace pa

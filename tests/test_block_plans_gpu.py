@@ -1,4 +1,4 @@
-"""Calls of pa_block_attend whose plan's form the sizes decide: decode of large groups."""
+"""Calls of pa_block_attend whose plan's form the sizes decide: decode of large groups, chunks of more rows than planned."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -24,3 +24,28 @@ def test_decode_of_large_groups_planned_for_many_requests(kind, Hq, Hkv, D, batc
     assert got[2] == 0 and plan.chunked == 0
     at._close(got, ref.attend(s["q"], s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["table"], s["seq"], None,
                               s["scale"], sinks=s["sinks"]))
+
+
+@pytest.mark.parametrize("group", [0, 1])
+def test_more_rows_than_a_chunked_plan_holds(group):
+    new = [40, 70, 60, 61, 3]
+    s = at._problem(13, "int8", 8, 2, 64, 16, [30, 40, 0, 5, 9], new)
+    if group:                                        # requests attended one at a time
+        wide = torch.zeros(5, 1 << 18, dtype=torch.int32)
+        wide[:, :s["table"].shape[1]] = s["table"]
+        s["table"] = wide
+    d = at._dev(s)
+    plan = at._plan(s, max_new=60)
+    assert plan.chunked == 1 and (plan.group_requests == 1) == bool(group)
+    scratch = pb.alloc_scratch(plan)
+    at._call(s, d, plan, scratch)
+    assert pb.check(scratch) == pb.DEVICE_CAPACITY
+    out, lse = d["out"].cpu(), d["lse"].cpu()
+    for b, n in enumerate(new):
+        r = slice(s["qsl"][b], s["qsl"][b + 1])
+        if n > 60:
+            assert (out[r] == 7).all() and (lse[r] == 7).all()
+        else:
+            one = ref.attend(s["q"][r], s["k_cache"], s["v_cache"], s["k_scales"], s["v_scales"], s["table"][b:b + 1],
+                             [s["seq"][b]], [0, n], s["scale"], chunked=True)
+            at._close((out[r], lse[r]), one, b)
