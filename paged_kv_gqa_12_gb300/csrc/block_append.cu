@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kCta, 4) block_append_kernel(const BlockAppend
   if (b < p.batch) {
     const int qs = p.qsl != nullptr ? p.qsl[b] : b;
     const int L = p.seq_lens[b];
-    const int n = p.qsl != nullptr ? p.qsl[b + 1] - qs : (L == 0 ? 0 : 1);      // (L 0: a padded batch's request)
+    const int n = p.qsl != nullptr ? packed_rows(qs, p.qsl[b + 1]) : (L == 0 ? 0 : 1);      // (L 0: a padded batch's request)
     const int64_t k = p.qsl != nullptr ? item - ((qs >> ps_log2) + 2 * static_cast<int64_t>(b)) : 0;
     if (n != 0) {
       if (n < 0 || L < n || L > (static_cast<int64_t>(p.max_pages) << ps_log2) || qs < 0 ||

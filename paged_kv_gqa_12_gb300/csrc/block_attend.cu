@@ -162,7 +162,7 @@ __device__ __forceinline__ bool load_request(const BlockParams& p, int b, int ts
   constexpr int hw = T::HW;
   r.L = p.seq_lens[b];
   r.qs = p.qsl != nullptr ? p.qsl[b] : b;
-  r.n_new = p.qsl != nullptr ? p.qsl[b + 1] - r.qs : 1;
+  r.n_new = p.qsl != nullptr ? packed_rows(r.qs, p.qsl[b + 1]) : 1;
   r.lo = r.tile0 = r.n_tiles = r.ys = 0;
   r.weight = hw > 8 && r.n_new * p.group > 8 ? T::WIDE : kTileWeight;
   if (r.n_new == 0) return true;
@@ -1136,7 +1136,7 @@ __global__ void __launch_bounds__(256) block_copy_kernel(const CopyParams p) {
   if (threadIdx.x == 0) p.bt_copy[dst_page] = static_cast<int32_t>(dst_page);   // (the same thread marks it below)
   const int L = p.seq_lens[b];
   const int qs = p.qsl[b];
-  const int n = p.qsl[b + 1] - qs;
+  const int n = packed_rows(qs, p.qsl[b + 1]);
   const int ctx = L - n;
   if (n <= 0 || n > p.max_new || ctx < 0 || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + n > p.total_q) return;
   const int ps = p.page_size;

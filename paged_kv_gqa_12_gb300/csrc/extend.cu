@@ -121,7 +121,7 @@ __device__ __forceinline__ bool item_range(const ExtendParams& p, const WorkItem
   const int mt = it.mt;
   ctx = L - qlen;
   t0 = mt * p.tm;
-  if (qlen <= 0 || ctx < 0 || L > p.max_kv || qs < 0 || qs + qlen > p.total_q || t0 >= qlen) return false;
+  if (qlen <= 0 || ctx < 0 || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + qlen > p.total_q || t0 >= qlen) return false;
   t_end = min(qlen, t0 + p.tm);
   const int pos_min = ctx + t0;
   const int pos_max = ctx + t_end - 1;
@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(kSchedThreads) extend_schedule_kernel(const Ex
   constexpr int kSchedWarps = kSchedThreads / 32;
   for (int b = warp; b < p.batch; b += kSchedWarps) {
     const int qs = p.qsl[b];
-    const int qlen = p.qsl[b + 1] - qs;
+    const int qlen = packed_rows(qs, p.qsl[b + 1]);
     const int L = p.seq_lens[b];
     if (qlen == 0) continue;
-    if (qlen < 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) {
+    if (qlen < 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + qlen > p.total_q) {
       if (lane == 0) atomicOr(p.err, kErrCapacity);
       continue;
     }
@@ -200,9 +200,9 @@ __global__ void __launch_bounds__(kSchedThreads) extend_schedule_kernel(const Ex
   __syncthreads();
   for (int b = warp; b < p.batch; b += kSchedWarps) {
     const int qs = p.qsl[b];
-    const int qlen = p.qsl[b + 1] - qs;
+    const int qlen = packed_rows(qs, p.qsl[b + 1]);
     const int L = p.seq_lens[b];
-    if (qlen <= 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || qs + qlen > p.total_q) continue;
+    if (qlen <= 0 || qlen > p.max_new || L < qlen || L > p.max_kv || qs < 0 || static_cast<int64_t>(qs) + qlen > p.total_q) continue;
     const int nmt = (qlen + p.tm - 1) / p.tm;
     for (int mt = lane; mt < nmt; mt += 32) {
       const int pos = atomicAdd(&s_off[min(tile_cost(L - qlen, qlen, mt, p.tm, p.window, p.block_n), kBuckets - 1)], 1);

@@ -24,6 +24,12 @@ constexpr uint32_t kErrPageId = PA_DEVICE_PAGE_ID;               // a page id ou
 // Wall-clock bound on every device-side wait (nanoseconds of %globaltimer).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
+// Rows of a request between two entries of query_start_loc, in arithmetic that wraps: entries that are not a
+// packing's may lie any distance apart, and begin + rows, in 64 bits, is then still compared with the rows there are.
+__host__ __device__ constexpr int32_t packed_rows(int32_t begin, int32_t end) {
+  return static_cast<int32_t>(static_cast<uint32_t>(end) - static_cast<uint32_t>(begin));
+}
+
 // Decode launch parameters (by value to both decode kernels).
 struct DecodeParams {
   const uint16_t* q;          // bf16 [B, Hq, D]

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_tokens_kernel(const Verify
   const int rank = static_cast<int>(cluster.block_rank());
   const int b = blockIdx.x / C;
   const int qs = p.qsl[b];
-  const int n = p.qsl[b + 1] - qs;
+  const int n = packed_rows(qs, p.qsl[b + 1]);
   int32_t* out = p.out + static_cast<int64_t>(b) * p.out_stride;
   // (the same in all threads of the cluster)
   if (n < 0 || n > p.out_width || qs < 0 || static_cast<int64_t>(qs) + n > p.total_rows) {
