@@ -73,3 +73,32 @@ def test_the_crossing(B, peaks, small, seed):
     slack = whole >> 36
     assert at <= token < at + 4096
     assert running <= target + slack and running + int(n[token]) > target - slack, (token, at, (running - target) / whole)
+
+
+@pytest.mark.parametrize("B", [1, 400])
+@pytest.mark.parametrize("off", [0, 1])
+def test_the_crossing_after_a_rejection(B, off):
+    # rows that are not 16-byte aligned are summed another way; a rejected draft's entry is taken off
+    V = 1 << 20
+    p, w, at = _row(V, True, 2.0 ** -18, 0)
+    x = 70000
+    both = torch.zeros(2, V + 8)
+    both[0, off:V + off] = torch.from_numpy(p)
+    probs = both.cuda()[:, off:V + off]
+    q = torch.zeros(2, V + 8)
+    q[0, off + x] = 0.5                              # the draft: 0.5 of it, and it has less of the target
+    qsl = torch.full((B + 1,), 2, dtype=torch.int32, device="cuda")
+    qsl[0] = 0
+    out = torch.full((B, 2), 99, dtype=torch.int32, device="cuda")
+    num = torch.full((B,), 99, dtype=torch.int32, device="cuda")
+    pb.verify_tokens(torch.tensor([0, x], dtype=torch.int32, device="cuda"), probs, qsl, torch.full((2,), 0.9, device="cuda"),
+                     torch.full((B,), float(w), device="cuda"), out, num, draft_probs=q.cuda()[:, off:V + off])
+    assert num.tolist() == [1] + [0] * (B - 1) and out[0, 1] == -1
+    token = int(out[0, 0])
+    n = np.array(_whole(p), dtype=object)
+    n[x] = 0
+    whole = int(n.sum())
+    target = int(float(w) * 2 ** 24) * whole // 2 ** 24
+    running = int(n[:token].sum())
+    slack = whole >> 36
+    assert running <= target + slack and running + int(n[token]) > target - slack, (token, at, (running - target) / whole)
