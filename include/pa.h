@@ -567,7 +567,8 @@ pa_status pa_block_plan(const pa_block_shape* shape, const int32_t* host_seq_len
  * most max_new of them, at the request's last positions.
  *   k_cache, v_cache   device bytes [num_pages, page_size, Hkv, head_dim], strides as for pa_decode
  *   k_scales, v_scales device fp32 [num_pages, Hkv], rows scale_stride apart, finite and >= 0
- *                  (a V scale below 2^-100 counts as 2^-100)
+ *                  (a V scale below 2^-100 counts as 2^-100, and those of the pages that one row
+ *                  attends to lie less than 2^126 apart: keys of smaller ones lose their weight)
  * q and out rows are 4-byte aligned for a plan that is not chunked, 16-byte aligned for one that
  * is.  Few rows: the codes enter the products exactly and the scales in fp32; q is scaled by a
  * power of two a row and exact in f16 down to 2^-32 of its row's largest value, weights are rounded to
