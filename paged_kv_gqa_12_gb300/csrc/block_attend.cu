@@ -694,25 +694,31 @@ block_split_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constan
       if (lane == 0) mbar_arrive(&empty[stage]);
     }
     };
-    for (int k = 0, k1; k < n; k = k1) {
-      k1 = n;
-      // (a tile with masked keys by itself: with one group of keys a warp the loop over the others holds fewer registers
-      // without that code, 16 rows of heads of 256 312 us for 329; with two groups one loop is better, 115 for 117)
-      if constexpr (!I8 && MT == 1) {
-        const int t0 = (tile_begin + k) * TS + key0;
-        if (t0 < full_lo || t0 + 16 > full_hi) {
-          dead = dead || !__all_sync(0xffffffffu, mbar_wait(&full[it % NS], (it / NS) & 1, p.err));
-          if (!dead) clean(it % NS, t0);
-          k1 = k + 1;
-        } else {
-          k1 = min(n, (full_hi - 16 - key0) / TS - tile_begin + 1);          // up to the next with masked keys
+    // (a tile with masked keys by itself: with one group of keys a warp the loop over the others holds fewer registers
+    // without that code, 64 requests of heads of 256 with one to four rows 249 us for 263, with four 314 for 334; with two
+    // groups one loop is better, heads of 128 113 for 117.  Rows beyond 8 are left out around the whole walk: inside it
+    // their accumulators stay in registers, 249 us become 314)
+    auto walk = [&](auto nj_tag) {
+      if constexpr (I8 || MT > 1) {
+        tiles(nj_tag, 0, n);
+      } else {
+        for (int k = 0, k1; k < n; k = k1) {
+          const int t0 = (tile_begin + k) * TS + key0;
+          if (t0 < full_lo || t0 + 16 > full_hi) {
+            dead = dead || !__all_sync(0xffffffffu, mbar_wait(&full[it % NS], (it / NS) & 1, p.err));
+            if (!dead) clean(it % NS, t0);
+            k1 = k + 1;
+          } else {
+            k1 = min(n, (full_hi - 16 - key0) / TS - tile_begin + 1);          // up to the next with masked keys
+          }
+          tiles(nj_tag, k, k1);
         }
       }
-      if (NH8 == 2 && R <= 8) {
-        tiles(std::integral_constant<int, 1>{}, k, k1);
-      } else {
-        tiles(std::integral_constant<int, NH8>{}, k, k1);
-      }
+    };
+    if (NH8 == 2 && R <= 8) {
+      walk(std::integral_constant<int, 1>{});
+    } else {
+      walk(std::integral_constant<int, NH8>{});
     }
 
     if (MT > 1) load_request<T>(p, b, TS, hgroups, r);   // (again, rather than in registers over the tiles)
